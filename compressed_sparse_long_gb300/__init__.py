@@ -20,14 +20,22 @@ __all__ = [
     "v4a_index_topk_noalloc_capacity",
     "v4a_attn_decode", "v4a_attn_prefill", "v4a_attn_workspace_size", "v4a_slot_mapping",
     "v4a_attn_decode_q8", "v4a_attn_q8_workspace_size", "v4a_attn_plan",
+    "RopeCfg", "LatentCfg", "rope_cfg", "latent_cfg", "v4a_rope", "v4a_latent_insert",
+    "v4a_latent_gather", "v4a_latent_attn", "v4a_latent_attn_workspace_size",
+    "v4a_latent_attn_expanded",
     "v4a_get_error", "v4a_version",
+    "BF16", "ROPE_INTERLEAVED", "ROPE_HALF", "ROPE_SCALE_NONE", "ROPE_SCALE_LINEAR",
+    "ROPE_SCALE_BY_PARTS", "ROPE_SCALE_YARN", "MAX_SEQ",
     "C4A", "C128A", "FP32", "BF16_FP8", "IDX_DEFAULT", "IDX_FP4", "DEV_MISSING_PAGE", "DEV_BAD_PAGE", "DEV_BAD_INDEX", "DEV_BAD_POS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libv4a.so")
 
 C4A, C128A = 0, 1
-FP32, BF16_FP8 = 0, 1
+FP32, BF16_FP8, BF16 = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BY_PARTS, ROPE_SCALE_YARN = 0, 1, 2, 3
+MAX_SEQ = 1024
 IDX_DEFAULT, IDX_FP4 = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE, ERR_TOO_LARGE = 0, -1, -2, -3, -4, -5
 DEV_MISSING_PAGE, DEV_BAD_PAGE, DEV_BAD_INDEX, DEV_BAD_POS = 1, 2, 4, 8
@@ -61,9 +69,26 @@ class Cache(ctypes.Structure):
                 ("row_width", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class RopeCfg(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_float), ("factor", ctypes.c_float),
+                ("orig_max_pos", ctypes.c_float), ("low", ctypes.c_float),
+                ("high", ctypes.c_float), ("amplitude", ctypes.c_float)]
+
+
+class LatentCfg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rms_eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
+                ("rope", RopeCfg)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFG, _CACHE = ctypes.POINTER(LayerCfg), ctypes.POINTER(Cache)
+_ROPE, _LATENT = ctypes.POINTER(RopeCfg), ctypes.POINTER(LatentCfg)
 
 _SIGS = {
     "v4a_version": (_I32, []),
@@ -92,6 +117,17 @@ _SIGS = {
     "v4a_index_topk_noalloc_capacity": (_SZ, []),
     "v4a_index_topk_noalloc": (ctypes.c_int, [_CFG, _I32, _P, _P, _I64, _P, _P, _CACHE, _I32,
                                               _P, _P, _P]),
+    "v4a_rope": (ctypes.c_int, [_ROPE, _I32, _I32, _I32, _P, _P, _I64, _I64, _P, _I64, _I64, _I32,
+                                _P, _P]),
+    "v4a_latent_insert": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P,
+                                         _CACHE, _P, _P]),
+    "v4a_latent_gather": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _P, _CACHE, _P, _P, _P]),
+    "v4a_latent_attn_workspace_size": (_SZ, [_LATENT, _I32, _I32, _I64]),
+    "v4a_latent_attn": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _P, _I64, _P, _CACHE, _P, _P, _SZ,
+                                       _P, _P]),
+    "v4a_latent_attn_expanded": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _I32, _P, _P, _P, _I64,
+                                                _I64, _P, _I64, _P, _I64, _I64, _I32, _P, _P,
+                                                _P]),
     "v4a_get_error": (ctypes.c_int, [_P, _P, ctypes.POINTER(_I32)]),
 }
 
@@ -270,6 +306,65 @@ def v4a_attn_prefill(cfg, n_q, q_seq, q_pos, max_pos, q, topk, k, attn, swa, out
 def v4a_slot_mapping(c, n, seq, row, slots, dev_err=None, stream=None):
     _check("v4a_slot_mapping", library().v4a_slot_mapping(
         ctypes.byref(c), n, _ptr(seq), _ptr(row), _ptr(slots), _ptr(dev_err), _stream(stream)))
+
+
+def rope_cfg(dim: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0,
+             scaling: int = ROPE_SCALE_NONE, factor: float = 1.0, orig_max_pos: float = 0.0,
+             low: float = 0.0, high: float = 0.0, amplitude: float = 1.0) -> RopeCfg:
+    """A rotation of `dim` values a row (see v4a_rope_cfg in include/v4a.h)."""
+    return RopeCfg(dim, layout, scaling, 0, base, factor, orig_max_pos, low, high, amplitude)
+
+
+def latent_cfg(dtype: int, n_heads: int, latent_dim: int, rope: RopeCfg, nope_dim: int = 128,
+               v_dim: int = 128, rms_eps: float = 1e-6,
+               softmax_scale: float | None = None) -> LatentCfg:
+    """A latent-attention layer; the softmax scale defaults to the expanded key's width ^ -1/2."""
+    return LatentCfg(dtype, n_heads, latent_dim, nope_dim, v_dim, 0, rms_eps,
+                     softmax_scale if softmax_scale else (nope_dim + rope.dim) ** -0.5, rope)
+
+
+def v4a_rope(rope, dtype, n_tokens, n_heads, pos, x, x_token_stride, x_head_stride, y,
+             y_token_stride, y_head_stride, inverse=False, dev_err=None, stream=None):
+    _check("v4a_rope", library().v4a_rope(
+        ctypes.byref(rope), dtype, n_tokens, n_heads, _ptr(pos), _ptr(x), x_token_stride,
+        x_head_stride, _ptr(y), y_token_stride, y_head_stride, int(inverse), _ptr(dev_err),
+        _stream(stream)))
+
+
+def v4a_latent_insert(cfg, n_seq, n_tokens, cu_tokens, start_pos, c, c_stride, k_pe, k_stride,
+                      gamma, cache, dev_err=None, stream=None):
+    _check("v4a_latent_insert", library().v4a_latent_insert(
+        ctypes.byref(cfg), n_seq, n_tokens, _ptr(cu_tokens), _ptr(start_pos), _ptr(c), c_stride,
+        _ptr(k_pe), k_stride, _ptr(gamma), ctypes.byref(cache), _ptr(dev_err), _stream(stream)))
+
+
+def v4a_latent_gather(cfg, n_seq, n_rows, cu_rows, start_pos, cache, out, dev_err=None,
+                      stream=None):
+    _check("v4a_latent_gather", library().v4a_latent_gather(
+        ctypes.byref(cfg), n_seq, n_rows, _ptr(cu_rows), _ptr(start_pos), ctypes.byref(cache),
+        _ptr(out), _ptr(dev_err), _stream(stream)))
+
+
+def v4a_latent_attn_workspace_size(cfg, n_seq, n_tokens, max_pos) -> int:
+    return library().v4a_latent_attn_workspace_size(ctypes.byref(cfg), n_seq, n_tokens, max_pos)
+
+
+def v4a_latent_attn(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, q, cache, out, workspace,
+                    dev_err=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("v4a_latent_attn", library().v4a_latent_attn(
+        ctypes.byref(cfg), n_seq, n_tokens, _ptr(cu_tokens), _ptr(start_pos), max_pos, _ptr(q),
+        ctypes.byref(cache), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_err),
+        _stream(stream)))
+
+
+def v4a_latent_attn_expanded(cfg, n_seq, n_q, cu_q, n_k, cu_k, q, k, k_token_stride,
+                             k_head_stride, k_pe, k_pe_stride, v, v_token_stride, v_head_stride,
+                             causal, out, dev_err=None, stream=None):
+    _check("v4a_latent_attn_expanded", library().v4a_latent_attn_expanded(
+        ctypes.byref(cfg), n_seq, n_q, _ptr(cu_q), n_k, _ptr(cu_k), _ptr(q), _ptr(k),
+        k_token_stride, k_head_stride, _ptr(k_pe), k_pe_stride, _ptr(v), v_token_stride,
+        v_head_stride, int(causal), _ptr(out), _ptr(dev_err), _stream(stream)))
 
 
 def v4a_get_error(dev_err, stream=None) -> int:

@@ -1,0 +1,294 @@
+// Launch parameters, work plan and launchers of the latent-attention kernels (internal).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace v4a {
+
+constexpr int kRotMaxPairs = 128;
+
+// A rotation's turning rates as turns per position, phi_i and psi_i = frac(4096 phi_i), each
+// split into fp32 hi + lo on the host (in double), as in Rope.
+struct RotTab {
+  int32_t dim, layout;
+  float amp;
+  float phi_hi[kRotMaxPairs], phi_lo[kRotMaxPairs];
+  float psi_hi[kRotMaxPairs], psi_lo[kRotMaxPairs];
+};
+
+struct RopeParams {
+  int32_t n_tokens, n_heads, inverse;
+  const int64_t* pos;
+  const void* x;
+  void* y;
+  int64_t x_ts, x_hs, y_ts, y_hs;
+  int32_t* err;
+  RotTab rot;
+};
+
+struct LatentInsertParams {
+  int32_t n_seq, n_tokens, C;
+  const int32_t* cu;
+  const int64_t* start;
+  const void* c;
+  const void* k_pe;
+  int64_t c_stride, k_stride;
+  const float* gamma;
+  float eps;
+  CacheView cache;
+  int32_t* err;
+  RotTab rot;
+};
+
+struct LatentGatherParams {
+  int32_t n_seq, n_rows, row_bytes;
+  const int32_t* cu;
+  const int64_t* start;
+  CacheView cache;
+  void* out;
+  int32_t* err;
+};
+
+// The work of an absorbed call. The rows (token, head) of a sequence are consecutive rows of
+// q; they are cut into units of NR rows, and the sequence's keys into tiles of TK. Lengths are
+// known on the device only, so every CTA derives the plan from cu and start: U consecutive
+// units of a sequence form a team's share (its members walk the same key tiles at the same
+// time and meet in L2), `teams` teams take equal parts of all (share, tile) pairs in order.
+// A unit whose tiles fall to several teams is left as partial results that a second kernel
+// merges. With teams == 0 whole units go to the CTAs in turn and nothing is merged.
+struct LatentPlan {
+  int32_t NR, TK, U, teams;
+};
+
+struct LatentAttnParams {
+  int32_t n_seq, n_tokens, H, C, R;   // R = rotary dims
+  float scale;
+  int64_t max_pos;
+  const int32_t* cu;
+  const int64_t* start;
+  const void* q;
+  void* out;
+  CacheView cache;
+  LatentPlan plan;
+  float* part_o;                      // [teams * U][2][NR][C] unnormalised, fp32
+  float* part_ml;                     // [teams * U][2][NR][2] maximum (log2 units) and sum
+  int32_t* err;
+};
+
+struct LatentExpandedParams {
+  int32_t n_seq, n_q, n_k, H, DN, DR, DV, causal;
+  float scale;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const void* q;
+  const void* k;
+  const void* k_pe;
+  const void* v;
+  void* out;
+  int64_t k_ts, k_hs, pe_ts, v_ts, v_hs;
+  int32_t* err;
+};
+
+int launch_rope(const RopeParams& p, int dtype, cudaStream_t st);
+int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st);
+int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);
+int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
+int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st);
+
+// ------------------------------------------------------------------ device-side plan
+#ifdef __CUDACC__
+
+// Rows of a packed batch that belong to sequence b, inside [0, n) whatever cu holds.
+__device__ __forceinline__ int cu_at(const int32_t* cu, int i, int n) {
+  return min(max(__ldg(cu + i), 0), n);
+}
+
+// Sequence of packed row t: the last b with cu[b] <= t, or -1 when t is outside the batch.
+// The whole warp takes part; 32 probes a round.
+__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_seq;
+  if (t < __ldg(cu) || t >= __ldg(cu + n_seq)) return -1;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool in = lane * step < n && __ldg(cu + lo + lane * step) <= t;
+    const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// One sequence's share of the plan.
+struct LatentSeq {
+  int row0;          // first row of the batch's (token, head) rows
+  int rows;          // rows of the sequence
+  int units, shares; // units of NR rows, shares of U units
+  int tiles;         // key tiles of the whole sequence (1 in whole-unit plans)
+  int64_t start;     // position of its first new token
+};
+
+__device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b) {
+  LatentSeq s;
+  const int a = cu_at(p.cu, b, p.n_tokens);
+  const int n = max(cu_at(p.cu, b + 1, p.n_tokens) - a, 0);
+  s.row0 = a * p.H;
+  s.rows = n * p.H;
+  s.start = __ldg(p.start + b);
+  s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
+  s.shares = (s.units + p.plan.U - 1) / p.plan.U;
+  const int64_t keys = min(s.start + n, p.max_pos + 1);
+  s.tiles = p.plan.teams == 0 ? 1 : (keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK));
+  return s;
+}
+
+// Keys that token i of a sequence sees (0 for a position below 0, capped at max_pos + 1).
+__device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, const LatentSeq& s, int i) {
+  return max((int64_t)0, min(s.start + i, p.max_pos) + 1);
+}
+
+// Exclusive prefix sums of shares * tiles over the sequences into pre[0 .. n_seq] (shared
+// memory), by the whole block.
+__device__ __forceinline__ void latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.n_seq; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    int w = 0;
+    if (b < p.n_seq) {
+      const LatentSeq s = latent_seq(p, b);
+      w = s.shares * s.tiles;
+    }
+    int x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_tot[warp] = x;
+    __syncthreads();
+    int before = carry, all = 0;
+    for (int i = 0; i < nw; ++i) {
+      if (i < warp) before += warp_tot[i];
+      all += warp_tot[i];
+    }
+    if (b < p.n_seq) pre[b] = before + x - w;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[p.n_seq] = carry;
+  __syncthreads();
+}
+
+// The sequence that holds position x of the prefix sums (pre[b] <= x < pre[b + 1]).
+__device__ __forceinline__ int latent_seq_at(const int32_t* pre, int n_seq, int x) {
+  int lo = 0, hi = n_seq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Teams that share `total` pairs, team g taking [g * total / n, (g + 1) * total / n).
+__device__ __forceinline__ int latent_teams(const LatentPlan& pl, int total) { return min(pl.teams, total); }
+__device__ __forceinline__ int latent_team_begin(int g, int total, int n) {
+  return (int)((int64_t)g * total / n);
+}
+__device__ __forceinline__ int latent_team_of(int x, int total, int n) {
+  return (int)((((int64_t)x + 1) * n - 1) / total);
+}
+
+// One piece of work of a CTA: a unit and a range of its key tiles.
+struct LatentPiece {
+  int seq, unit, row0, rows;   // row0: first row of the unit in q; rows <= NR
+  int tile0, tile1;            // key tiles of the sequence
+  int64_t keys;                // keys the unit's last row sees
+  int64_t start;               // position of the sequence's first token
+  int seq_row0;                // first row of the sequence
+  int whole;                   // the piece holds every tile of the unit: write the result
+  int slot;                    // where its partial result goes otherwise
+};
+
+// Walks a CTA's pieces. All threads call it alike.
+struct LatentWalk {
+  int x, x1, team, member, total, n;
+  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int cta, int n_cta) {
+    total = pre[p.n_seq];
+    const int U = p.plan.U;
+    team = cta / U;
+    member = cta % U;
+    if (p.plan.teams == 0) {       // whole shares in turn, the teams striding over them
+      n = n_cta / U;
+      x = team;
+      x1 = total;
+    } else {
+      n = latent_teams(p.plan, total);
+      x = team < n ? latent_team_begin(team, total, n) : 0;
+      x1 = team < n ? latent_team_begin(team + 1, total, n) : 0;
+    }
+  }
+  // The next piece, or false. A piece may have no unit (rows == 0) or no keys.
+  __device__ __forceinline__ bool next(const LatentAttnParams& p, const int32_t* pre, LatentPiece& w) {
+    if (x >= x1) return false;
+    const int b = latent_seq_at(pre, p.n_seq, x);
+    const LatentSeq s = latent_seq(p, b);
+    const int r = x - pre[b];
+    const int share = r / s.tiles, t = r - share * s.tiles;
+    w.seq = b;
+    w.start = s.start;
+    w.seq_row0 = s.row0;
+    w.unit = share * p.plan.U + member;
+    const int ur = w.unit * p.plan.NR;
+    w.row0 = s.row0 + ur;
+    w.rows = max(0, min(p.plan.NR, s.rows - ur));
+    w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
+    const int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
+    if (p.plan.teams == 0) {
+      w.tile0 = 0;
+      w.tile1 = unit_tiles;
+      w.whole = 1;
+      w.slot = 0;
+      x += n;
+    } else {
+      const int take = min(s.tiles - t, x1 - x);
+      w.whole = take == s.tiles;
+      w.slot = ((team * p.plan.U + member) << 1) + (t == 0 ? 1 : 0);
+      w.tile0 = min(t, unit_tiles);
+      w.tile1 = min(t + take, unit_tiles);
+      x += take;
+    }
+    return true;
+  }
+};
+
+// Angle of position pos (0 <= pos < 2^36) and a pair's constants: pos = 4096 hi + lo, the
+// angle in turns is frac(hi psi + lo phi). Products are exact in two floats, the integer parts
+// are dropped exactly, and what the reduced angle loses to rounding turns the result by its
+// first-order term, so cosine and sine are good to a few units of 2^-24.
+__device__ __forceinline__ void rot_cs(int64_t pos, float phi_hi, float phi_lo, float psi_hi, float psi_lo,
+                                       float& c, float& s) {
+  const float hi = (float)(int32_t)(pos >> 12), lo = (float)(int32_t)(pos & 4095);
+  const float p1 = hi * psi_hi, e1 = fmaf(hi, psi_lo, fmaf(hi, psi_hi, -p1));
+  const float p2 = lo * phi_hi, e2 = fmaf(lo, phi_lo, fmaf(lo, phi_hi, -p2));
+  const float r1 = p1 - rintf(p1), r2 = p2 - rintf(p2);
+  float a = r1 + r2;
+  const float bb = a - r1;
+  const float tail = ((r1 - (a - bb)) + (r2 - bb)) + (e1 + e2);
+  a -= rintf(a);
+  const float t = a + tail, d = (tail - (t - a)) * 6.2831853071795865f;
+  float c0, s0;
+  sincospif(2.0f * t, &s0, &c0);
+  c = fmaf(-s0, d, c0);
+  s = fmaf(c0, d, s0);
+}
+
+#endif  // __CUDACC__
+
+}  // namespace v4a

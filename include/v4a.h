@@ -66,6 +66,7 @@ typedef struct CUstream_st* v4a_stream_t; /* a cudaStream_t; NULL = legacy defau
 /* arithmetic / storage */
 #define V4A_FP32 0                /* fp32 inputs, fp32 caches, fp32 output */
 #define V4A_BF16_FP8 1            /* bf16 inputs, fp8 e4m3 caches + fp32 row scale, bf16 output */
+#define V4A_BF16 2                /* bf16 inputs, bf16 caches, bf16 output (v4a_rope, v4a_latent_*) */
 
 /* indexer-cache formats (v4a_layer_cfg.idx_format) */
 #define V4A_IDX_DEFAULT 0         /* the layer's cache type: fp8 e4m3 (BF16_FP8) or fp32 (FP32) */
@@ -311,6 +312,169 @@ int v4a_attn_prefill(const v4a_layer_cfg* cfg, int32_t n_q, const int32_t* q_seq
 int v4a_slot_mapping(const v4a_cache* cache, int32_t n, const int32_t* seq,
                      const int64_t* row, int32_t* slots, int32_t* dev_err,
                      v4a_stream_t stream);
+
+/*
+ * Latent attention: the layer whose cache holds one shared vector a token, a latent of
+ * latent_dim values and a rotary key of rope.dim values, from which every head's key and
+ * value are projections ([notes] 压缩参数细节 and 8.7x 节省的算术推导: the V3.2 stack that the
+ * compressed layer is compared with, 576 bf16 values a token). v4a_latent_insert writes the
+ * cache, v4a_latent_attn reads it in the absorbed form (the key projection applied to the
+ * query, the value projection to the output: one shared key row for all heads),
+ * v4a_latent_gather copies cached rows out for the projections of the expanded form, and
+ * v4a_latent_attn_expanded attends with projected keys and values. v4a_rope rotates the
+ * query's rotary part (and anything else that needs it).
+ *
+ * These calls describe a batch as v4a_compress_insert does: sequence b owns rows
+ * cu[b] .. cu[b+1]-1 of the packed inputs, at positions start_pos[b] + (row - cu[b]).
+ * cu is non-decreasing; rows at or behind cu[n_seq] belong to no sequence: inputs there are
+ * not used and outputs there are left as they were. At most V4A_MAX_SEQ sequences a call.
+ * Every call reads its inputs only after the kernels enqueued before it on the stream have
+ * completed. Two calls that may overlap need workspaces of their own.
+ */
+#define V4A_MAX_SEQ 1024
+#define V4A_MAX_POS ((int64_t)1 << 36)  /* positions are below this */
+
+/* pairs of a rotation: (2i, 2i+1) or (i, i + dim/2) */
+#define V4A_ROPE_INTERLEAVED 0
+#define V4A_ROPE_HALF 1
+
+/* how the turning rates theta_i = base^(-2i/dim) are scaled for long contexts. With
+ * turns_i = orig_max_pos * theta_i / (2 pi), every rate is theta_i (t_i + (1 - t_i) / factor):
+ *   NONE      t_i = 1
+ *   LINEAR    t_i = 0 (position interpolation)
+ *   BY_PARTS  t_i = clamp((turns_i - low) / (high - low), 0, 1): a ramp in the turns
+ *   YARN      t_i = 1 - clamp((i - a) / (b - a), 0, 1): a ramp in the pair index, where
+ *             pair(t) = dim ln(orig_max_pos / (2 pi t)) / (2 ln base) is the index of the
+ *             pair that makes t turns, a = max(floor(pair(high)), 0),
+ *             b = min(ceil(pair(low)), dim - 1), and b - a is at least 1e-3
+ * (the "by parts" interpolation of Peng et al., "YaRN: Efficient Context Window Extension of
+ * Large Language Models", 2023, with both ramps in use for it). */
+#define V4A_ROPE_SCALE_NONE 0
+#define V4A_ROPE_SCALE_LINEAR 1
+#define V4A_ROPE_SCALE_BY_PARTS 2
+#define V4A_ROPE_SCALE_YARN 3
+
+typedef struct v4a_rope_cfg {
+  int32_t dim;           /* rotated dims: even, 2 .. 256 */
+  int32_t layout;        /* V4A_ROPE_INTERLEAVED or V4A_ROPE_HALF */
+  int32_t scaling;       /* V4A_ROPE_SCALE_* */
+  int32_t reserved;      /* must be 0 */
+  float base;            /* > 0; > 1 for YARN */
+  float factor;          /* > 0; unused for NONE */
+  float orig_max_pos;    /* BY_PARTS, YARN: > 0 */
+  float low, high;       /* BY_PARTS, YARN: turns, 0 < low < high */
+  float amplitude;       /* > 0, on cosine and sine alike (1 = a rotation) */
+} v4a_rope_cfg;
+
+typedef struct v4a_latent_cfg {
+  int32_t dtype;         /* V4A_BF16 or V4A_FP32: inputs, cache and outputs */
+  int32_t n_heads;       /* H */
+  int32_t latent_dim;    /* C: a multiple of 8, 8 .. 1024 */
+  int32_t nope_dim;      /* dims of an expanded key before its rotary part: multiple of 8, .. 256 */
+  int32_t v_dim;         /* dims of an expanded value: multiple of 8, 8 .. 256 */
+  int32_t reserved;      /* must be 0 */
+  float rms_eps;         /* of v4a_latent_insert's norm */
+  float softmax_scale;   /* > 0, of both attention forms */
+  v4a_rope_cfg rope;     /* rope.dim: a multiple of 8, 8 .. 128 */
+} v4a_latent_cfg;
+
+/*
+ * v4a_rope — rotate rows of n_heads x rope->dim values by their token's position.
+ *   y_pair = amplitude * (x0 c - x1 s, x0 s + x1 c), (c, s) = (cos, sin)(pos[t] * rate_i)
+ * inverse != 0 turns the other way (s -> -s): with amplitude 1 the inverse, and for any
+ * amplitude the gradient of the forward call with respect to x.
+ * The rotated part of a wider head is given by its pointer and strides.
+ *
+ * dtype: V4A_FP32 or V4A_BF16 (computed in fp32, the angle reduced exactly, rounded once)
+ * pos:   device int64 [n_tokens], each in [0, V4A_MAX_POS); a token outside it is left
+ *        unwritten and sets V4A_DEV_BAD_POS
+ * x, y:  device, element (t, h, d) at t * token_stride + h * head_stride + d (strides in
+ *        elements, >= 0; y's rows must not overlap one another); y == x with equal strides
+ *        rotates in place, any other element of y must not be an element of x
+ * Rows on 16-byte boundaries take 16-byte accesses, others single elements.
+ */
+int v4a_rope(const v4a_rope_cfg* rope, int32_t dtype, int32_t n_tokens, int32_t n_heads,
+             const int64_t* pos, const void* x, int64_t x_token_stride, int64_t x_head_stride,
+             void* y, int64_t y_token_stride, int64_t y_head_stride, int32_t inverse,
+             int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_latent_insert — write the cache rows of new tokens:
+ *   row = [ gamma * c / sqrt(mean(c^2) + rms_eps) | rope(k_pe, pos) ],
+ * computed in fp32 and rounded once; gamma == NULL stores c as it is.
+ *
+ * c:     device [n_tokens, C] with c_stride elements between tokens; k_pe: device
+ *        [n_tokens, rope.dim], k_stride apart (two parts of one projection's output, say).
+ *        Pointers on 16-byte boundaries, strides multiples of 16 bytes.
+ * gamma: device fp32 [C], 16-byte aligned, or NULL
+ * cache: rows_per_block 256, row_width C + rope.dim, no scales
+ * Tokens without a page or with a position outside [0, V4A_MAX_POS) are not written and set
+ * V4A_DEV_MISSING_PAGE / V4A_DEV_BAD_PAGE / V4A_DEV_BAD_POS.
+ */
+int v4a_latent_insert(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                      const int32_t* cu_tokens, const int64_t* start_pos, const void* c,
+                      int64_t c_stride, const void* k_pe, int64_t k_stride, const float* gamma,
+                      const v4a_cache* cache, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_latent_gather — copy cached rows out: out row cu_rows[b] + i = the cache's row of
+ * position start_pos[b] + i of sequence b. out: device [n_rows, C + rope.dim], 16-byte
+ * aligned. A row without a page (or at a negative position) is zeroed and sets
+ * V4A_DEV_MISSING_PAGE / V4A_DEV_BAD_PAGE.
+ */
+int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows,
+                      const int32_t* cu_rows, const int64_t* start_pos, const v4a_cache* cache,
+                      void* out, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_latent_attn — absorbed latent attention of each sequence's newest tokens (one or many)
+ * over its cached rows, their own included (insert them first):
+ *   out[t, h] = sum_x softmax_x(softmax_scale * q[t, h] . row_x) row_x[0:C],  x <= pos(t).
+ *
+ * q:     device [n_tokens, H, C + rope.dim], the rotary part already rotated, 16-byte aligned
+ * out:   device [n_tokens, H, C], 16-byte aligned
+ * max_pos: no position of the call is above it; a token beyond it sees the keys up to it and
+ *        sets V4A_DEV_BAD_POS
+ * workspace: device, >= v4a_latent_attn_workspace_size(...) bytes, 256-byte aligned (may be
+ *        NULL where that is 0)
+ * Keys in a block without a page are left out (and set the error word); a token that sees no
+ * key gives zeros. Rows of the cache behind a sequence's last token are not used, whatever
+ * they hold. A key that is not finite makes the outputs of its call's later tokens not finite,
+ * and may do so to earlier tokens of the same call.
+ * bf16 with C = 512 and rope.dim = 64 runs on the tensor cores; other shapes on CUDA cores.
+ */
+size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                                      int64_t max_pos);
+int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                    const int32_t* cu_tokens, const int64_t* start_pos, int64_t max_pos,
+                    const void* q, const v4a_cache* cache, void* out, void* workspace,
+                    size_t workspace_bytes, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_latent_attn_expanded — latent attention with projected keys and values, for prompts:
+ * sequence b has query rows cu_q[b] .. cu_q[b+1]-1 and key rows cu_k[b] .. cu_k[b+1]-1,
+ *   s = softmax_scale * (q[i, h, 0:nope] . k[x, h] + q[i, h, nope:] . k_pe[x])
+ *   out[i, h] = sum_x softmax_x(s) v[x, h].
+ * causal != 0: the sequence's last query sees its last key, each query before it one key
+ * fewer; causal == 0: every query sees every key. A query that sees no key gives zeros.
+ *
+ * q:    device [n_q, H, nope + rope.dim] (rotary part last, rotated); out: device [n_q, H, v_dim]
+ * k, v: device, element (x, h, d) at x * token_stride + h * head_stride + d (strides in
+ *       elements, so k and v may be parts of one projection's output); k_pe: device
+ *       [n_k, rope.dim], k_pe_stride elements between tokens, shared by the heads
+ * All pointers on 16-byte boundaries, strides positive multiples of 16 bytes.
+ * Key and value rows at or behind cu_k[n_seq], and other sequences' rows, are not used,
+ * whatever they hold. A value that is not finite may reach queries of its sequence that do
+ * not see it.
+ * bf16 with nope = 128, rope.dim = 64 and v_dim = 128 runs on the tensor cores; other shapes
+ * on CUDA cores.
+ */
+int v4a_latent_attn_expanded(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_q,
+                             const int32_t* cu_q, int32_t n_k, const int32_t* cu_k, const void* q,
+                             const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                             const void* k_pe, int64_t k_pe_stride, const void* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int32_t causal,
+                             void* out, int32_t* dev_err, v4a_stream_t stream);
 
 /* Synchronise `stream`, read the device error word, clear it. *flags_out (may be NULL)
  * receives the bits. Returns V4A_OK, V4A_ERR_DEVICE if any bit was set, or V4A_ERR_CUDA. */
