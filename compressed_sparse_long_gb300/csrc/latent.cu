@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
     int rows, t0, t1, qa = 0, ka = 0, nq = 0, nk = 0;
     int64_t keys;
     if constexpr (kPaged) {
-      if (!walk.next(p, pre, w)) break;
+      if (!walk.next(p, w)) break;
       rows = w.rows;
       keys = w.keys;
       t0 = w.tile0;
@@ -557,13 +557,18 @@ cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream
 }
 
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
-  int64_t grid = (int64_t)p.plan.teams * p.plan.U;
-  if (grid == 0) {
-    grid = ((int64_t)p.n_tokens * p.H + p.plan.NR - 1) / p.plan.NR + p.n_seq;
-    if (grid > 65536) grid = 65536;
+  cudaError_t e;
+  if (p.plan.tc) {
+    e = launch_latent_attn_tc(p, st);
+  } else {
+    int64_t grid = (int64_t)p.plan.teams * p.plan.U;
+    if (grid == 0) {
+      grid = ((int64_t)p.n_tokens * p.H + p.plan.NR - 1) / p.plan.NR + p.n_seq;
+      if (grid > 65536) grid = 65536;
+    }
+    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, grid, st)
+                          : run_gen<float, true>(p, p.C + p.R, p.C, grid, st);
   }
-  cudaError_t e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, grid, st)
-                                    : run_gen<float, true>(p, p.C + p.R, p.C, grid, st);
   if (e == cudaSuccess) e = launch_latent_merge(p, dtype, st);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }

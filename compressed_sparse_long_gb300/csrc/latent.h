@@ -63,6 +63,7 @@ struct LatentGatherParams {
 // merges. With teams == 0 whole units go to the CTAs in turn and nothing is merged.
 struct LatentPlan {
   int32_t NR, TK, U, teams;
+  int32_t tc;                         // tensor-core kernel
 };
 
 struct LatentAttnParams {
@@ -99,6 +100,7 @@ int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st);
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st);
 
 // ------------------------------------------------------------------ device-side plan
@@ -207,21 +209,22 @@ __device__ __forceinline__ int latent_team_of(int x, int total, int n) {
 
 // One piece of work of a CTA: a unit and a range of its key tiles.
 struct LatentPiece {
-  int seq, unit, row0, rows;   // row0: first row of the unit in q; rows <= NR
+  int seq, row0, rows;         // row0: first row of the unit in q; rows <= NR
   int tile0, tile1;            // key tiles of the sequence
-  int64_t keys;                // keys the unit's last row sees
+  int64_t keys, keys0;         // keys that the unit's last and first rows see
   int64_t start;               // position of the sequence's first token
   int seq_row0;                // first row of the sequence
   int whole;                   // the piece holds every tile of the unit: write the result
   int slot;                    // where its partial result goes otherwise
 };
 
-// Walks a CTA's pieces. All threads call it alike.
+// Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
+// the prefix sums are read in begin() only.
 struct LatentWalk {
-  int x, x1, team, member, total, n;
+  int x, x1, team, member, n;
+  int b, base;      // current sequence and the pairs before it
   __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int cta, int n_cta) {
-    total = pre[p.n_seq];
-    const int U = p.plan.U;
+    const int total = pre[p.n_seq], U = p.plan.U;
     team = cta / U;
     member = cta % U;
     if (p.plan.teams == 0) {       // whole shares in turn, the teams striding over them
@@ -233,22 +236,27 @@ struct LatentWalk {
       x = team < n ? latent_team_begin(team, total, n) : 0;
       x1 = team < n ? latent_team_begin(team + 1, total, n) : 0;
     }
+    b = x < x1 ? latent_seq_at(pre, p.n_seq, x) : 0;
+    base = x < x1 ? pre[b] : 0;
   }
   // The next piece, or false. A piece may have no unit (rows == 0) or no keys.
-  __device__ __forceinline__ bool next(const LatentAttnParams& p, const int32_t* pre, LatentPiece& w) {
+  __device__ __forceinline__ bool next(const LatentAttnParams& p, LatentPiece& w) {
     if (x >= x1) return false;
-    const int b = latent_seq_at(pre, p.n_seq, x);
-    const LatentSeq s = latent_seq(p, b);
-    const int r = x - pre[b];
+    LatentSeq s = latent_seq(p, b);
+    while (x >= base + s.shares * s.tiles) {
+      base += s.shares * s.tiles;
+      s = latent_seq(p, ++b);
+    }
+    const int r = x - base;
     const int share = r / s.tiles, t = r - share * s.tiles;
     w.seq = b;
     w.start = s.start;
     w.seq_row0 = s.row0;
-    w.unit = share * p.plan.U + member;
-    const int ur = w.unit * p.plan.NR;
+    const int unit = share * p.plan.U + member, ur = unit * p.plan.NR;
     w.row0 = s.row0 + ur;
     w.rows = max(0, min(p.plan.NR, s.rows - ur));
     w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
+    w.keys0 = w.rows > 0 ? latent_visible(p, s, ur / p.H) : 0;
     const int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
     if (p.plan.teams == 0) {
       w.tile0 = 0;

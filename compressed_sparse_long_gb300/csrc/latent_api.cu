@@ -107,7 +107,8 @@ bool on_tensor_cores(const v4a_latent_cfg* c) {
 
 // The plan of an absorbed call. False when the tiles cannot be counted in 31 bits.
 bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t max_pos, LatentPlan* pl) {
-  const bool tc = false;
+  const bool tc = on_tensor_cores(c);
+  pl->tc = tc;
   pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
   pl->U = 1;
