@@ -854,6 +854,21 @@ bool encode_byte_rows_map(CUtensorMap* map, const void* base, uint64_t n_rows, u
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over a 3-D byte tensor: rows of row_bytes, n1 of them stride1 bytes apart, n2 times
+// stride2 bytes apart (strides multiples of 16), boxes of box_bytes x 1 x box_n2.
+bool encode_byte_rows_map3(CUtensorMap* map, const void* base, uint32_t row_bytes, uint64_t n1, uint64_t stride1,
+                           uint64_t n2, uint64_t stride2, uint32_t box_bytes, uint32_t box_n2) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride1, (cuuint64_t)stride2};
+  const cuuint32_t box[3] = {box_bytes, 1, box_n2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 template <int NQ, bool kFp4>

@@ -93,6 +93,9 @@ cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t st);
 // when the driver entry point is missing or the driver refuses the map.
 bool encode_byte_rows_map(CUtensorMap* map, const void* base, uint64_t n_rows, uint32_t row_bytes,
                           uint32_t box_bytes, uint32_t box_rows);
+// The same over a 3-D byte tensor (n2 x n1 rows, strides in bytes), boxes of one row along n1.
+bool encode_byte_rows_map3(CUtensorMap* map, const void* base, uint32_t row_bytes, uint64_t n1, uint64_t stride1,
+                           uint64_t n2, uint64_t stride2, uint32_t box_bytes, uint32_t box_n2);
 int launch_slot_mapping(const CacheView& c, int32_t n, const int32_t* seq, const int64_t* row,
                         int32_t* slots, int32_t* err, cudaStream_t st);
 

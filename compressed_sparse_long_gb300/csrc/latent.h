@@ -101,6 +101,7 @@ int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st);
+cudaError_t launch_latent_expanded_tc(const LatentExpandedParams& p, cudaStream_t st);
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st);
 
 // ------------------------------------------------------------------ device-side plan
@@ -155,18 +156,15 @@ __device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, con
   return max((int64_t)0, min(s.start + i, p.max_pos) + 1);
 }
 
-// Exclusive prefix sums of shares * tiles over the sequences into pre[0 .. n_seq] (shared
-// memory), by the whole block.
-__device__ __forceinline__ void latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+// Exclusive prefix sums of weight(b) over the sequences into pre[0 .. n_seq] (shared memory),
+// by the whole block.
+template <typename F>
+__device__ __forceinline__ void seq_prefix(int n_seq, int32_t* pre, int32_t* warp_tot, F weight) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   int carry = 0;
-  for (int b0 = 0; b0 < p.n_seq; b0 += blockDim.x) {
+  for (int b0 = 0; b0 < n_seq; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    int w = 0;
-    if (b < p.n_seq) {
-      const LatentSeq s = latent_seq(p, b);
-      w = s.shares * s.tiles;
-    }
+    const int w = b < n_seq ? weight(b) : 0;
     int x = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,12 +178,19 @@ __device__ __forceinline__ void latent_prefix(const LatentAttnParams& p, int32_t
       if (i < warp) before += warp_tot[i];
       all += warp_tot[i];
     }
-    if (b < p.n_seq) pre[b] = before + x - w;
+    if (b < n_seq) pre[b] = before + x - w;
     carry += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[p.n_seq] = carry;
+  if (threadIdx.x == 0) pre[n_seq] = carry;
   __syncthreads();
+}
+// (share, tile) pairs of the sequences of an absorbed call.
+__device__ __forceinline__ void latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+  seq_prefix(p.n_seq, pre, warp_tot, [&](int b) {
+    const LatentSeq s = latent_seq(p, b);
+    return s.shares * s.tiles;
+  });
 }
 
 // The sequence that holds position x of the prefix sums (pre[b] <= x < pre[b + 1]).
