@@ -15,7 +15,7 @@
 //
 // Warps 0-3 / 4-7: softmax and output of tile 0 / 1, a thread a query (so maxima and sums need
 // no exchange). The running maximum is raised only when it grows by more than 2^8. Warp 8:
-// copies. Warp 9: products. (Warps 10 and 11 only complete their warpgroup.)
+// copies. Warps 9 and 10: products of tile 0 / 1. (Warp 11 only completes its warpgroup.)
 #include "kernels.h"
 #include "latent.h"
 #include "tc.cuh"
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pfull = bars + 16;                   // [2]
   uint64_t* ofull = bars + 18;                   // [2]
   uint64_t* oempty = bars + 20;                  // [2]
-  uint64_t* done = bars + 22;
+  uint64_t* done = bars + 22;                    // [2]
   int* misc = reinterpret_cast<int*>(sm + kOffMisc);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(qfull + i, 1);
       tc::mbar_init(qempty + i, 1);
       tc::mbar_init(pefull + i, 1);
-      tc::mbar_init(peempty + i, 1);
+      tc::mbar_init(peempty + i, 2);
+      tc::mbar_init(done + i, 1);
       tc::mbar_init(sfull + i, 1);
       tc::mbar_init(pfull + i, 4);
       tc::mbar_init(ofull + i, 1);
@@ -165,9 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(full + i, 1);
-      tc::mbar_init(empty + i, 1);
+      tc::mbar_init(empty + i, 2);                // both tiles' products
     }
-    tc::mbar_init(done, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
@@ -359,101 +359,98 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 9 || warp == 10) {
     // ---------------------------------------------------------------------- products
+    const int tile = warp - 9;
     constexpr uint32_t idesc_s = tc::idesc_bf16(kT, kT);
     constexpr uint32_t idesc_o = tc::idesc_bf16(kT, kT, false, true);
-    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(qbuf), 16, 1024);        // K-major
-    const uint64_t dk = tc::sdesc_sw128(tc::smem_u32(kvbuf), 16, 1024);       // K-major
-    const uint64_t dpe = tc::sdesc_sw128(tc::smem_u32(pebuf), 16, 1024);      // K-major
-    const uint64_t dv = tc::sdesc_sw128(tc::smem_u32(kvbuf), kBlk, 1024);     // MN-major
+    const uint32_t ut = tc::uniform(tile), dS = tc::uniform(tmem) + ut * 128, dO = dS + 256;
+    const uint32_t kv = tc::uniform(tc::smem_u32(kvbuf)), pe = tc::uniform(tc::smem_u32(pebuf));
+    const uint32_t q_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(qbuf)) + ut * 3 * kBlk, 16);
     int c = 0, e = 0;                             // slot uses: K of step t at c, V at c + 1
-    int nq[2] = {0, 0};                           // items of each query tile
-    int gp[2] = {0, 0};                           // products P V of each tile
+    int nq = 0, gp = 0;                           // items and products P V of this tile
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, p.err));
       return ok;
     };
-    // S of query tile i with the keys of slot use kc and rotary-slot use ec
-    auto issue_s = [&](int i, int kc, int ec) {
+    auto commit = [&](uint64_t* bar) {
+      if (ok && tc::elect_one()) tc::mma_commit(bar);
+      __syncwarp();
+    };
+    // S with the keys of slot use kc and rotary-slot use ec
+    auto issue_s = [&](int kc, int ec) {
       if (!wait_all(full + kc % 3, (kc / 3) & 1) || !wait_all(pefull + (ec & 1), (ec / 2) & 1)) return;
       tc::fence_after_sync();
-      if (lane == 0) {
-        const uint64_t qd = dq + (uint64_t)((3 * i * kBlk) >> 4);
-        const uint64_t kd = dk + (uint64_t)(((kc % 3) * 2 * kBlk) >> 4);
-        const uint64_t pd = dpe + (uint64_t)(((ec & 1) * kBlk) >> 4);
+      const uint32_t k_lo = tc::uniform(tc::sdesc_lo(kv + (kc % 3) * 2 * kBlk, 16));
+      const uint32_t e_lo = tc::uniform(tc::sdesc_lo(pe + (ec & 1) * kBlk, 16));
+      if (tc::elect_one()) {
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)              // 16 dims, 32 bytes
-            tc::mma_bf16(tmem + i * 128, qd + (uint64_t)((b * kBlk) >> 4) + 2 * s,
-                         (b < 2 ? kd + (uint64_t)((b * kBlk) >> 4) : pd) + 2 * s, idesc_s, (b | s) ? 1u : 0u);
+            tc::mma_bf16_lo<idesc_s>(dS, q_lo + ((b * kBlk) >> 4) + 2 * s,
+                                     (b < 2 ? k_lo + ((b * kBlk) >> 4) : e_lo) + 2 * s, (b | s) ? 1u : 0u);
         }
-        tc::mma_commit(sfull + i);
+        tc::mma_commit(sfull + tile);
       }
       __syncwarp();
     };
-    auto commit = [&](uint64_t* bar) {
-      if (ok && lane == 0) tc::mma_commit(bar);
-      __syncwarp();
+    // Both warps release every slot use, a tile that skips it too, and only once it was full:
+    // an arrival for a later use must not count for this one.
+    auto release_k = [&](int kc, int ec) {
+      if (!wait_all(full + kc % 3, (kc / 3) & 1) || !wait_all(pefull + (ec & 1), (ec / 2) & 1)) return;
+      commit(empty + kc % 3);
+      commit(peempty + (ec & 1));
     };
     while (ok && walk.next(p, w)) {
-      const int n0 = w.tiles[0], n1 = w.tiles[1], n = max(n0, n1);
+      const int n = max(w.tiles[0], w.tiles[1]), mine = w.tiles[tile];
       if (n == 0) continue;
-      // step 0's logits
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (w.tiles[i] == 0) continue;
-        if (!wait_all(qfull + i, nq[i] & 1)) break;
-        issue_s(i, c, e);
-        if (w.tiles[i] == 1) commit(qempty + i);
+      if (mine > 0) {
+        if (!wait_all(qfull + tile, nq & 1)) break;
+        issue_s(c, e);                             // step 0's logits
+        if (mine == 1) commit(qempty + tile);
       }
-      commit(empty + c % 3);
-      commit(peempty + (e & 1));
+      release_k(c, e);
       for (int t = 0; t < n && ok; ++t, c += 2, ++e) {
         const int vs = (c + 1) % 3;
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (t < w.tiles[i]) {
-            if (!wait_all(full + vs, ((c + 1) / 3) & 1)) break;
-            if (!wait_all(pfull + i, gp[i] & 1)) break;
-            if (t == 0 && nq[i] > 0 && !wait_all(oempty + i, (nq[i] - 1) & 1)) break;
-            const int valid = w.nk - t * kT;
-            if (valid < kT) {                      // 0 times what lies behind the keys must be 0
-              for (int b = 0; b < 2; ++b)
-                for (int o = valid * 128 + lane * 16; o < kBlk; o += 512)
-                  *reinterpret_cast<uint4*>(kvbuf + (2 * vs + b) * kBlk + o) = make_uint4(0, 0, 0, 0);
-              tc::fence_proxy_async();
-              __syncwarp();
-            }
-            tc::fence_after_sync();
-            if (lane == 0) {
-              const uint64_t vd = dv + (uint64_t)((vs * 2 * kBlk) >> 4);
-#pragma unroll
-              for (int s = 0; s < 8; ++s)          // 16 keys: 8 columns of P, 2 KB of V
-                tc::mma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + 8 * s, vd + (uint64_t)((s * 2048) >> 4),
-                                idesc_o, (t > 0 || s > 0) ? 1u : 0u);
-              if (t + 1 == w.tiles[i]) tc::mma_commit(ofull + i);
-            }
+        if (!wait_all(full + vs, ((c + 1) / 3) & 1)) break;
+        if (t < mine) {
+          if (!wait_all(pfull + tile, gp & 1)) break;
+          if (t == 0 && nq > 0 && !wait_all(oempty + tile, (nq - 1) & 1)) break;
+          const int valid = w.nk - t * kT;
+          if (valid < kT) {                        // 0 times what lies behind the keys must be 0
+            // (the other tile's warp may be doing the same, or its product reading these zeros)
+            for (int b = 0; b < 2; ++b)
+              for (int o = valid * 128 + lane * 16; o < kBlk; o += 512)
+                *reinterpret_cast<uint4*>(kvbuf + (2 * vs + b) * kBlk + o) = make_uint4(0, 0, 0, 0);
+            tc::fence_proxy_async();
             __syncwarp();
-            ++gp[i];
           }
-          if (i == 1) commit(empty + vs);
-          if (t + 1 < w.tiles[i]) {
-            issue_s(i, c + 2, e + 1);
-            if (t + 2 == w.tiles[i]) commit(qempty + i);
+          tc::fence_after_sync();
+          const uint32_t v_lo = tc::uniform(tc::sdesc_lo(kv + vs * 2 * kBlk, kBlk));
+          const uint32_t acc = tc::uniform(t > 0);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)            // 16 keys: 8 columns of P, 2 KB of V
+              tc::mma_bf16_ta_lo<idesc_o>(dO, dS + 8 * s, v_lo + ((s * 2048) >> 4), s > 0 ? 1u : acc);
+            if (t + 1 == mine) tc::mma_commit(ofull + tile);
           }
+          __syncwarp();
+          ++gp;
         }
-        if (t + 1 < n) {
-          commit(empty + (c + 2) % 3);
-          commit(peempty + ((e + 1) & 1));
+        commit(empty + vs);
+        if (t + 1 < mine) {
+          issue_s(c + 2, e + 1);
+          if (t + 2 == mine) commit(qempty + tile);
         }
+        if (t + 1 < n) release_k(c + 2, e + 1);
       }
-      for (int i = 0; i < 2; ++i)
-        if (w.tiles[i] > 0) ++nq[i];
+      if (mine > 0) ++nq;
     }
-    if (lane == 0) {
-      tc::mma_commit(done);
-      tc::mbar_wait_drain(done, 0);
+    if (tc::elect_one()) {
+      tc::mma_commit(done + tile);
+      tc::mbar_wait_drain(done + tile, 0);
     }
     __syncwarp();
   }

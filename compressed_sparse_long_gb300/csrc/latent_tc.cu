@@ -388,12 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------------- products
     constexpr uint32_t idesc_s = tc::idesc_bf16(kTK, kNR);
     constexpr uint32_t idesc_o = tc::idesc_bf16(128, kNR, true, true);
-    const uint32_t k0 = tc::smem_u32(kbuf);
-    const uint64_t dk = tc::sdesc_sw128(k0, 16, 1024);                      // keys, K-major
-    const uint64_t dx = tc::sdesc_sw128(tc::smem_u32(xbuf), 16, 1024);      // rotary keys, K-major
-    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(qbuf), 16, 1024);      // rows, K-major
-    const uint64_t dv = tc::sdesc_sw128(k0, kKBlock, 1024);                 // V^T, MN-major
-    const uint64_t dp = tc::sdesc_sw128(tc::smem_u32(xbuf), 16, 1024);      // P^T, MN-major
+    const uint32_t k0 = tc::uniform(tc::smem_u32(kbuf)), x0 = tc::uniform(tc::smem_u32(xbuf));
+    const uint32_t k_lo = tc::sdesc_lo(k0, 16), x_lo = tc::sdesc_lo(x0, 16);   // keys, rotary keys / P^T
+    const uint32_t q_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(qbuf)), 16);   // rows
+    const uint32_t v_lo = tc::sdesc_lo(k0, kKBlock);                           // V^T, MN-major
+    const uint32_t dS = tc::uniform(tmem) + kSCol, dO = tc::uniform(tmem) + kOCol;
     int g = 0, u = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -403,19 +402,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.tile0 >= w.tile1) continue;
       if (!wait_all(qfull, u & 1)) break;
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
-        for (int j = 0; j < 5 && ok; ++j) {
-          ok = wait_all(j < 4 ? vfull + j : xfull, g & 1);
-          if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+          if (ok) ok = wait_all(j < 4 ? vfull + j : xfull, g & 1);
+          if (!ok) continue;
           tc::fence_after_sync();
-          if (lane == 0) {
-            const int nb = j < 4 ? 2 : 1;
-            for (int b = 0; b < nb; ++b) {
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int b = 0; b < (j < 4 ? 2 : 1); ++b) {
               const int kb = 2 * j + b;
-              const uint64_t ad = j < 4 ? dk + (uint64_t)((kb * kKBlock) >> 4) : dx;
-              const uint64_t bd = dq + (uint64_t)((kb * kQBlock) >> 4);
 #pragma unroll
               for (int s = 0; s < 4; ++s)          // 16 dims, 32 bytes
-                tc::mma_bf16(tmem + kSCol, ad + 2 * s, bd + 2 * s, idesc_s, (kb | s) ? 1u : 0u);
+                tc::mma_bf16_lo<idesc_s>(dS, (j < 4 ? k_lo + ((kb * kKBlock) >> 4) : x_lo) + 2 * s,
+                                         q_lo + ((kb * kQBlock) >> 4) + 2 * s, (kb | s) ? 1u : 0u);
             }
             if (j == 4) {
               tc::mma_commit(sfull);
@@ -428,13 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_all(pfull, g & 1)) { ok = false; break; }
         if (t == w.tile0 && u > 0 && !wait_all(oempty, (u - 1) & 1)) { ok = false; break; }
         tc::fence_after_sync();
-        if (lane == 0) {
+        const uint32_t acc = tc::uniform(t > w.tile0);
+        if (tc::elect_one()) {
+#pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const uint64_t ad = dv + (uint64_t)((2 * b * kKBlock) >> 4);
 #pragma unroll
             for (int s = 0; s < 8; ++s)            // 16 keys, 2 KB
-              tc::mma_bf16(tmem + kOCol + b * kNR, ad + (uint64_t)((s * 2048) >> 4),
-                           dp + (uint64_t)((s * 2048) >> 4), idesc_o, (t > w.tile0 || s > 0) ? 1u : 0u);
+              tc::mma_bf16_lo<idesc_o>(dO + b * kNR, v_lo + ((2 * b * kKBlock + s * 2048) >> 4),
+                                       x_lo + ((s * 2048) >> 4), s > 0 ? 1u : acc);
             tc::mma_commit(vempty + b);
           }
           tc::mma_commit(pvdone);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++u;
     }
-    if (lane == 0) {
+    if (tc::elect_one()) {
       tc::mma_commit(done);
       tc::mbar_wait_drain(done, 0);
     }

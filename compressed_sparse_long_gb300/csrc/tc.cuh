@@ -202,6 +202,41 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// One lane of a converged warp. Products issued under it with operands that are the same in
+// every lane take them from uniform registers; under `lane == 0` each operand word is moved
+// there one by one, about 95 cycles a product.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+// A value that is the same in every lane, as one word for the whole warp.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// sdesc_sw128 in two words: the low one holds the address and LBO, the high one is constant.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // SBO 1024, 128B swizzle
+
+// mma_bf16 and mma_bf16_ta with descriptors of high word kSdescHi.
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3}; setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p; }" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_bf16_ta_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 b; mov.b64 b, {%2, %3}; setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+
 // Byte offset of 16-byte chunk `c` (0..7) of row `r` inside a 128B-swizzled region whose
 // 8-row groups are 1024 bytes apart.
 __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {
