@@ -111,8 +111,10 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   pl->tc = tc;
   pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
-  pl->U = 1;
   const int64_t rows = (int64_t)n_tokens * c->n_heads;
+  // units of a sequence that walk its keys together: as many as an average sequence has, up to 4
+  pl->U = 1;
+  while (tc && pl->U < 4 && n_seq > 0 && rows / n_seq >= 2 * pl->U * pl->NR) pl->U *= 2;
   const int64_t units = (rows + pl->NR - 1) / pl->NR + n_seq;   // at most, over the sequences
   const int64_t tiles = max_pos / pl->TK + 1;
   const int sms = sm_count();
@@ -122,7 +124,7 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   if (units < 4 * ctas) {
     if (units * tiles >= INT32_MAX) return false;
     pl->teams = (int32_t)(ctas / pl->U);
-    if (units * tiles < pl->teams) pl->teams = (int32_t)(units * tiles);
+    if (units * tiles < pl->teams) pl->teams = (int32_t)(units * tiles);   // (an upper bound)
     if (tiles == 1) pl->teams = 0;                              // nothing to split
   }
   return true;

@@ -16,9 +16,11 @@
 // tensor pipe for 128 heads and chunks (an N = 64 product costs what an N = 128 one does).
 //
 // Warps 0-7: softmax and output. A thread holds one key's 32 logits (warps 0-3 rows 0-31, warps
-// 4-7 rows 32-63 of the unit); maxima over the keys go by redux and through shared memory. The
-// running maximum of a row is raised only when it grows by more than 2^8; then the accumulator
-// and the sums are rescaled. Warp 8: copies. Warp 9: products.
+// 4-7 rows 32-63 of the unit). A row's weights are taken against a reference, its maximum over
+// the first tile; maxima over the keys (redux, and through shared memory) are needed again only
+// where a tile is masked or a weight would pass 2^40, and then the reference is raised where it
+// is exceeded by more than 2^8 and the accumulator and sums rescaled. Warp 8: copies, with the
+// next tile requested into L2 a tile ahead. Warp 9: products.
 #include "kernels.h"
 #include "latent.h"
 #include "tc.cuh"
@@ -41,7 +43,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kKBlock, "the plan's prefix sums use a key block before its first copy");
 constexpr uint32_t kSCol = 0, kOCol = 64, kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.0f;                                   // log2 units
+constexpr float kRaise = 8.0f, kLimit = 40.0f;                   // log2 units
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
@@ -121,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
   volatile int* tile_ok = misc + 2;                              // [2] by tile parity
+  volatile int* raised = misc + 4;                               // [2 halves][2 parities] tile + 1
   int32_t* warp_tot = misc + 8;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(redb + 1, 4);
     tc::mbar_init(done, 1);
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) raised[i] = 0;
     tc::fence_mbar_init();
   }
   if (warp == 9) {
@@ -187,69 +191,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         vis = max((int64_t)0, min(pos, p.max_pos) + 1);
         if (quad == 0 && (pos > p.max_pos || pos < 0)) raise_err(p.err, V4A_DEV_BAD_POS);
       }
-      float m = -INFINITY;                        // row c's running maximum, log2 units
+      float m = -INFINITY;                        // row c's reference, log2 units
       float l[32];                                // this key lane's sums, by row
 #pragma unroll
       for (int c = 0; c < 32; ++c) l[c] = 0.f;
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+        // (the tile's last copy is complete before its products are)
+        if (!tc::mbar_wait(xfull, g & 1, abort_flag, p.err)) { ok = false; break; }
+        const int64_t x0 = (int64_t)t * kTK;
+        const int valid = tile_ok[g & 1] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
+        // A tile that every row sees whole, with every row's reference set: the weights are
+        // taken against the references as they are, unless one of them would pass 2^kLimit
+        // (weights and sums are floating-point numbers, so a reference need not be the
+        // maximum). The group agrees on that while it computes the exponentials.
+        bool slow = valid < kTK || w.keys0 < x0 + kTK || __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
+        float4 ref[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ref[c] = *reinterpret_cast<const float4*>(mb + 4 * c);
         if (!tc::mbar_wait(sfull, g & 1, abort_flag, p.err)) { ok = false; break; }
         tc::fence_after_sync();
         float s[32];
         tc::tmem_ld32(scol, s);
         tc::tmem_wait_ld();
-        if (!tc::mbar_wait(xfull, g & 1, abort_flag, p.err)) { ok = false; break; }
-        const int64_t x0 = (int64_t)t * kTK;
-        const int valid = tile_ok[g & 1] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
-        if (valid < kTK || w.keys0 < x0 + kTK) {  // some row does not see the whole tile
+        if (!slow) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 mv = ref[c / 4];
+            s[c] = fmaf(s[c], k2, -mv.x);
+            s[c + 1] = fmaf(s[c + 1], k2, -mv.y);
+            s[c + 2] = fmaf(s[c + 2], k2, -mv.z);
+            s[c + 3] = fmaf(s[c + 3], k2, -mv.w);
+            top = fmaxf(top, fmaxf(fmaxf(s[c], s[c + 1]), fmaxf(s[c + 2], s[c + 3])));
+          }
+          const bool over = __any_sync(0xffffffffu, top > kLimit);
+          if (lane == 0) {
+            if (over) raised[half * 2 + (g & 1)] = g + 1;
+            tc::mbar_arrive(redb + half);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = fast_exp2(s[c]);
+          if (!tc::mbar_wait(redb + half, ru & 1, abort_flag, p.err)) { ok = false; break; }
+          ++ru;
+          slow = raised[half * 2 + (g & 1)] == g + 1;
+          if (slow) {
+            tc::tmem_ld32(scol, s);
+            tc::tmem_wait_ld();
+          }
+        }
+        if (slow) {
           const int seen = min((int)max((int64_t)0, min(vis - x0, (int64_t)kTK)), valid);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
-        }
-        float* rb = red_max + (ru & 1) * 256 + half * 128;
+          float* rb = red_max + (ru & 1) * 256 + half * 128;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float mc = redux_max(s[c]);
-          if (lane == c) rb[c * 4 + quad] = mc;
-        }
-        if (!group_sync()) { ok = false; break; }
-        const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
-        const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * k2;
-        float corr = 1.f;
-        if (t == w.tile0) {
-          m = mt;
-        } else if (mt > m + kRaise) {
-          corr = fast_exp2(m - mt);               // 0 from -inf
-          m = mt;
-        }
-        mb[lane] = m == -INFINITY ? 0.f : m;
-        const bool raise = t > w.tile0 && __any_sync(0xffffffffu, corr != 1.f);
-        __syncwarp();
-        if (raise) {
-          // S^T of this tile is done, and with it every product issued before it
-#pragma unroll
-          for (int c = 0; c < 32; ++c) l[c] *= __shfl_sync(0xffffffffu, corr, c);
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            float o[32];
-            tc::tmem_ld32(ocol + b * kNR, o);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] *= __shfl_sync(0xffffffffu, corr, c);
-            st32(ocol + b * kNR, o);
+          for (int c = 0; c < 32; ++c) {
+            const float mc = redux_max(s[c]);
+            if (lane == c) rb[c * 4 + quad] = mc;
           }
-          tc::tmem_wait_st();
-        }
+          if (!group_sync()) { ok = false; break; }
+          const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
+          const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * k2;
+          float corr = 1.f;
+          if (t == w.tile0) {
+            m = mt;
+          } else if (mt > m + kRaise) {
+            corr = fast_exp2(m - mt);             // 0 from -inf
+            m = mt;
+          }
+          __syncwarp();
+          mb[lane] = m == -INFINITY ? 0.f : m;
+          const bool raise = t > w.tile0 && __any_sync(0xffffffffu, corr != 1.f);
+          __syncwarp();
+          if (raise) {
+            // S^T of this tile is done, and with it every product issued before it
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 mv = *reinterpret_cast<const float4*>(mb + c);
-          s[c] = fast_exp2(fmaf(s[c], k2, -mv.x));
-          s[c + 1] = fast_exp2(fmaf(s[c + 1], k2, -mv.y));
-          s[c + 2] = fast_exp2(fmaf(s[c + 2], k2, -mv.z));
-          s[c + 3] = fast_exp2(fmaf(s[c + 3], k2, -mv.w));
-        }
+            for (int c = 0; c < 32; ++c) l[c] *= __shfl_sync(0xffffffffu, corr, c);
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              float o[32];
+              tc::tmem_ld32(ocol + b * kNR, o);
+              tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) l[c] += s[c];
+              for (int c = 0; c < 32; ++c) o[c] *= __shfl_sync(0xffffffffu, corr, c);
+              st32(ocol + b * kNR, o);
+            }
+            tc::tmem_wait_st();
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(mb + c);
+            s[c] = fast_exp2(fmaf(s[c], k2, -mv.x));
+            s[c + 1] = fast_exp2(fmaf(s[c + 1], k2, -mv.y));
+            s[c + 2] = fast_exp2(fmaf(s[c + 2], k2, -mv.z));
+            s[c + 3] = fast_exp2(fmaf(s[c + 3], k2, -mv.w));
+          }
+        }
         // P^T, MN-major [128 keys][64 rows]: this key's half row. The weights are rounded to
         // bf16, the second product's type; the sums above take them unrounded.
 #pragma unroll
@@ -268,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(pfull);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) l[c] += s[c];
       }
       if (!ok) break;
       // ---- sums over the keys: lane c gets row c's
@@ -372,6 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             tc::mbar_arrive(xfull);
           }
+          if (t + 1 < w.tile1) {             // the next tile's rows into L2
+            const int64_t ahead = tile_slot(p, w.seq, t + 1);
+            if (ahead >= 0) {
+              const uint8_t* rows = reinterpret_cast<const uint8_t*>(p.cache.data) + ahead * (kW * 2);
+#pragma unroll 1
+              for (int i = 0; i < 9; ++i)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(rows + i * kKBlock), "r"(kKBlock)
+                             : "memory");
+            }
+          }
         }
         ++u;
       }
@@ -474,6 +524,7 @@ cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st) {
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     grid = (rows + kNR - 1) / kNR + p.n_seq;
     if (grid > sms) grid = sms;
+    grid = (grid + p.plan.U - 1) / p.plan.U * p.plan.U;
   }
   const cudaError_t e =
       cudaFuncSetAttribute(latent_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
