@@ -139,108 +139,149 @@ int run_rope(const RopeParams& p, cudaStream_t st) {
 }
 
 // ----------------------------------------------------------------------------- insert
-// One warp per token: the latent row in registers (16-byte vectors, lane l taking vectors
-// l, l + 32, ..), its mean square by shuffles, then the rotary part. Bound: latency at decode,
-// HBM for prompts (each row is read and written once).
+// One warp per token at a time: the latent row in registers (16-byte vectors, lane l taking
+// vectors l, l + 32, ..), requested before the token's place is looked up; its mean square by
+// shuffles; then the rotary part, lane i turning pairs i, i + 32 with rates it keeps. Bound:
+// latency at decode, HBM for prompts (each row is read and written once).
 constexpr int kInsertWarps = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const __grid_constant__ LatentInsertParams p) {
   constexpr int kV = 16 / (int)sizeof(T), kMaxVec = 1024 / kV / 32;
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kInsertWarps + (threadIdx.x >> 5);
+  const int np = p.rot.dim / 2, nv = p.C / kV;
+  float rate[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = min(lane + 32 * j, np - 1);
+    rate[j][0] = p.rot.phi_hi[i];
+    rate[j][1] = p.rot.phi_lo[i];
+    rate[j][2] = p.rot.psi_hi[i];
+    rate[j][3] = p.rot.psi_lo[i];
+  }
   pdl_wait();
-  if (t >= p.n_tokens) return;
-  const int b = warp_find_seq(p.cu, p.n_seq, t);
-  if (b < 0) return;
-  const int64_t pos = __ldg(p.start + b) + (t - __ldg(p.cu + b));
-  if (pos < 0 || pos >= V4A_MAX_POS) {
-    if (lane == 0) raise_err(p.err, V4A_DEV_BAD_POS);
-    return;
-  }
-  const int64_t slot = slot_of(p.cache, b, pos);
-  if (slot < 0) {
-    if (lane == 0) slot_ok(slot, p.err);
-    return;
-  }
-  T* row = reinterpret_cast<T*>(p.cache.data) + slot * (int64_t)p.cache.width;
-  const T* c = reinterpret_cast<const T*>(p.c) + (int64_t)t * p.c_stride;
-  const int nv = p.C / kV;
-  float f[kMaxVec][kV];
-  float ss = 0.f;
+  for (int64_t t = (int64_t)blockIdx.x * kInsertWarps + (threadIdx.x >> 5); t < p.n_tokens;
+       t += (int64_t)gridDim.x * kInsertWarps) {
+    const T* c = reinterpret_cast<const T*>(p.c) + t * p.c_stride;
+    const T* k = reinterpret_cast<const T*>(p.k_pe) + t * p.k_stride;
+    float f[kMaxVec][kV];
 #pragma unroll
-  for (int i = 0; i < kMaxVec; ++i) {
-    const int v = lane + 32 * i;
-    if (v < nv) {
-      load_pack<T, kV>(c + v * kV, f[i]);
+    for (int i = 0; i < kMaxVec; ++i)
+      if (lane + 32 * i < nv) load_pack<T, kV>(c + (lane + 32 * i) * kV, f[i]);
+    float x0[2], x1[2];
+    const bool half = p.rot.layout == V4A_ROPE_HALF;
 #pragma unroll
-      for (int k = 0; k < kV; ++k) ss = fmaf(f[i][k], f[i][k], ss);
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (i < np) {
+        x0[j] = Elem<T>::to_f(k[half ? i : 2 * i]);
+        x1[j] = Elem<T>::to_f(k[half ? i + np : 2 * i + 1]);
+      }
     }
-  }
-  float r = 1.f;
-  if (p.gamma) r = 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps);
+    const int b = warp_find_seq(p.cu, p.n_seq, (int)t);
+    if (b < 0) continue;
+    const int64_t pos = __ldg(p.start + b) + (t - __ldg(p.cu + b));
+    if (pos < 0 || pos >= V4A_MAX_POS) {
+      if (lane == 0) raise_err(p.err, V4A_DEV_BAD_POS);
+      continue;
+    }
+    const int64_t slot = slot_of(p.cache, b, pos);
+    if (slot < 0) {
+      if (lane == 0) slot_ok(slot, p.err);
+      continue;
+    }
+    T* row = reinterpret_cast<T*>(p.cache.data) + slot * (int64_t)p.cache.width;
+    float r = 1.f;
+    if (p.gamma) {
+      float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxVec; ++i) {
-    const int v = lane + 32 * i;
-    if (v < nv) {
+      for (int i = 0; i < kMaxVec; ++i)
+        if (lane + 32 * i < nv) {
+#pragma unroll
+          for (int e = 0; e < kV; ++e) ss = fmaf(f[i][e], f[i][e], ss);
+        }
+      r = 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxVec; ++i) {
+      const int v = lane + 32 * i;
+      if (v >= nv) continue;
       if (p.gamma) {
 #pragma unroll
-        for (int k = 0; k < kV; k += 4) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + v * kV + k));
-          f[i][k] *= r * g.x;
-          f[i][k + 1] *= r * g.y;
-          f[i][k + 2] *= r * g.z;
-          f[i][k + 3] *= r * g.w;
+        for (int e = 0; e < kV; e += 4) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + v * kV + e));
+          f[i][e] *= r * g.x;
+          f[i][e + 1] *= r * g.y;
+          f[i][e + 2] *= r * g.z;
+          f[i][e + 3] *= r * g.w;
         }
       }
       store_pack<T, kV>(row + v * kV, f[i]);
     }
-  }
-  const T* k = reinterpret_cast<const T*>(p.k_pe) + (int64_t)t * p.k_stride;
-  const int np = p.rot.dim / 2;
-  for (int i = lane; i < np; i += 32) {
-    const int a = p.rot.layout == V4A_ROPE_HALF ? i : 2 * i, d = p.rot.layout == V4A_ROPE_HALF ? np : 1;
-    float cc, sn;
-    rot_cs(pos, p.rot.phi_hi[i], p.rot.phi_lo[i], p.rot.psi_hi[i], p.rot.psi_lo[i], cc, sn);
-    cc *= p.rot.amp;
-    sn *= p.rot.amp;
-    const float x0 = Elem<T>::to_f(k[a]), x1 = Elem<T>::to_f(k[a + d]);
-    row[p.C + a] = Elem<T>::from_f(x0 * cc - x1 * sn);
-    row[p.C + a + d] = Elem<T>::from_f(x0 * sn + x1 * cc);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (i >= np) continue;
+      float cc, sn;
+      rot_cs(pos, rate[j][0], rate[j][1], rate[j][2], rate[j][3], cc, sn);
+      cc *= p.rot.amp;
+      sn *= p.rot.amp;
+      const T y0 = Elem<T>::from_f(x0[j] * cc - x1[j] * sn), y1 = Elem<T>::from_f(x0[j] * sn + x1[j] * cc);
+      row[p.C + (half ? i : 2 * i)] = y0;
+      row[p.C + (half ? i + np : 2 * i + 1)] = y1;
+    }
   }
 }
 
 // ----------------------------------------------------------------------------- gather
-// A block copies 64 rows: their pool rows are looked up first (a warp per row, in turn), then
-// all threads copy 16-byte vectors, several in flight. Bound: HBM.
+// A block copies `rows` rows: their pool rows are looked up first, a thread a row, then all
+// threads copy 16-byte vectors, eight in flight each. Bound: HBM; for few rows, latency.
 constexpr int kGatherRows = 64, kGatherThreads = 256;
 
-__global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __grid_constant__ LatentGatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __grid_constant__ LatentGatherParams p,
+                                                                       int rows) {
   __shared__ int64_t slots[kGatherRows];   // pool row, -1: zeros, -2: no row of the batch
-  const int r0 = blockIdx.x * kGatherRows, nr = min(kGatherRows, p.n_rows - r0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * rows, nr = min(rows, p.n_rows - r0);
   pdl_wait();
-  for (int r = warp; r < nr; r += kGatherThreads / 32) {
-    const int b = warp_find_seq(p.cu, p.n_seq, r0 + r);
-    if (lane == 0) {
-      int64_t s = -2;
-      if (b >= 0) {
-        s = slot_of(p.cache, b, __ldg(p.start + b) + (r0 + r - __ldg(p.cu + b)));
-        if (!slot_ok(s, p.err)) s = -1;
-      }
-      slots[r] = s;
+  if (threadIdx.x < nr) {
+    const int t = r0 + threadIdx.x;
+    int lo = 0, hi = p.n_seq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid;
     }
+    const int a = __ldg(p.cu + lo);
+    int64_t s = -2;
+    if (t >= a && t < __ldg(p.cu + lo + 1)) {
+      s = slot_of(p.cache, lo, __ldg(p.start + lo) + (t - a));
+      if (!slot_ok(s, p.err)) s = -1;
+    }
+    slots[threadIdx.x] = s;
   }
   __syncthreads();
-  const int nv = p.row_bytes / 16;
+  const int nv = p.row_bytes / 16, total = nr * nv;
   const uint4* pool = reinterpret_cast<const uint4*>(p.cache.data);
   uint4* out = reinterpret_cast<uint4*>(p.out) + (int64_t)r0 * nv;
-#pragma unroll 6
-  for (int k = threadIdx.x; k < nr * nv; k += kGatherThreads) {
-    const int r = k / nv;
-    const int64_t s = slots[r];
-    if (s == -2) continue;
-    out[k] = s < 0 ? make_uint4(0, 0, 0, 0) : __ldg(pool + s * nv + (k - r * nv));
+  const int dr = kGatherThreads / nv, dc = kGatherThreads % nv;   // a step of all threads
+  int r = threadIdx.x / nv, c = threadIdx.x % nv;
+  for (int k = threadIdx.x; k < total; k += 8 * kGatherThreads) {
+    uint4 v[8];
+    bool put[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      put[i] = false;
+      if (k + i * kGatherThreads < total) {
+        const int64_t s = slots[r];
+        put[i] = s != -2;
+        v[i] = s < 0 ? make_uint4(0, 0, 0, 0) : __ldg(pool + s * nv + c);
+        r += dr;
+        c += dc;
+        if (c >= nv) { c -= nv; ++r; }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (put[i]) out[k + i * kGatherThreads] = v[i];
   }
 }
 
@@ -298,6 +339,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
   LatentWalk walk;
   LatentPiece w;
   int seq = 0, head = 0, item = blockIdx.x;
+  bool posted = false;
   if constexpr (kPaged) {
     latent_prefix(p, pre, warp_tot);
     walk.begin(p, pre, blockIdx.x, gridDim.x);
@@ -307,7 +349,10 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
     int rows, t0, t1, qa = 0, ka = 0, nq = 0, nk = 0;
     int64_t keys;
     if constexpr (kPaged) {
-      if (!walk.next(p, w)) break;
+      const bool more = walk.next(p, w);
+      if (threadIdx.x == 0 && !posted) walk.post(p, more ? &w : nullptr);
+      posted = true;
+      if (!more) break;
       rows = w.rows;
       keys = w.keys;
       t0 = w.tile0;
@@ -363,28 +408,33 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
     for (int t = t0; t < t1; ++t) {
       const int64_t x0 = (int64_t)t * kGenKeys;
       __syncthreads();
-      for (int k = warp; k < kGenKeys; k += kGenThreads / 32) {
-        const int64_t x = x0 + k;
-        bool ok = x < keys;
+      // lane k resolves key k's row; a warp then copies four rows
+      int64_t at = -1;
+      if (x0 + lane < keys) {
         if constexpr (kPaged) {
-          int64_t s = -1;
-          if (ok) {
-            s = slot_of(p.cache, w.seq, x);
-            ok = s >= 0;
-            if (!ok && lane == 0) slot_ok(s, p.err);
-          }
-          if (ok) load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.cache.data) + s * (int64_t)DK, DK, lane);
-        } else if (ok) {
-          const int64_t g = ka + x;
-          load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.k) + g * p.k_ts + (int64_t)head * p.k_hs, p.DN, lane);
-          load_row_f<T>(ks + k * KS + p.DN, reinterpret_cast<const T*>(p.k_pe) + g * p.pe_ts, p.DR, lane);
-          load_row_f<T>(vs + k * VS, reinterpret_cast<const T*>(p.v) + g * p.v_ts + (int64_t)head * p.v_hs, DV, lane);
+          at = slot_of(p.cache, w.seq, x0 + lane);
+          if (at < 0 && warp == 0) slot_ok(at, p.err);
+        } else {
+          at = ka + x0 + lane;
         }
-        if (!ok) {
+      }
+      if (warp == 0) kvalid[lane] = at >= 0;
+#pragma unroll
+      for (int i = 0; i < kGenKeys / 8; ++i) {
+        const int k = warp * (kGenKeys / 8) + i;
+        const int64_t g = __shfl_sync(0xffffffffu, at, k);
+        if (g >= 0) {
+          if constexpr (kPaged) {
+            load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.cache.data) + g * (int64_t)DK, DK, lane);
+          } else {
+            load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.k) + g * p.k_ts + (int64_t)head * p.k_hs, p.DN, lane);
+            load_row_f<T>(ks + k * KS + p.DN, reinterpret_cast<const T*>(p.k_pe) + g * p.pe_ts, p.DR, lane);
+            load_row_f<T>(vs + k * VS, reinterpret_cast<const T*>(p.v) + g * p.v_ts + (int64_t)head * p.v_hs, DV, lane);
+          }
+        } else {
           for (int d = lane; d < DK; d += 32) ks[k * KS + d] = 0.f;
           if (!kPaged) for (int d = lane; d < DV; d += 32) vs[k * VS + d] = 0.f;
         }
-        if (lane == 0) kvalid[k] = ok;
       }
       __syncthreads();
       float s0 = 0.f, s1 = 0.f;
@@ -452,65 +502,74 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
 
 // ------------------------------------------------------------------------------ merge
 // The results of a unit whose tiles fell to several teams: out = sum_i w_i o_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max). Block (g, member, rows): the share in which team g begins, if it
-// is the first team to begin inside it. A warp per row.
-constexpr int kMergeWarps = 8;
+// with w_i = 2^(m_i - max). Block (g, member, rows) does the job that team g posted; a warp a
+// row. Bound: latency (job, statistics, partial results: three loads in a row).
+constexpr int kMergeWarps = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
-  __shared__ int32_t pre[V4A_MAX_SEQ + 1];
-  __shared__ int32_t warp_tot[kMergeWarps];
   pdl_wait();
-  latent_prefix(p, pre, warp_tot);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int U = p.plan.U, NR = p.plan.NR;
   const int g = blockIdx.x / U + 1, member = blockIdx.x % U;
-  const int total = pre[p.n_seq], n = latent_teams(p.plan, total);
-  if (g >= n) return;
-  const int x = latent_team_begin(g, total, n);
-  const int b = latent_seq_at(pre, p.n_seq, x);
-  const LatentSeq s = latent_seq(p, b);
-  const int share = (x - pre[b]) / s.tiles, x0 = pre[b] + share * s.tiles;
-  if (x == x0 || latent_team_begin(g - 1, total, n) > x0) return;
-  const int last = latent_team_of(x0 + s.tiles - 1, total, n);
-  const int unit_row = (share * U + member) * NR;
-  const int r = blockIdx.y * kMergeWarps + warp;
-  if (r >= NR || unit_row + r >= s.rows) return;
-  // team g - 1's piece begins the share (slot 1), the others begin inside it (slot 0)
+  const int4 job = *reinterpret_cast<const int4*>(p.part_job + 4 * (g * U + member));
+  const int r = blockIdx.y * kMergeWarps + warp, last = job.z;
+  if (r >= job.x) return;
+  // team g - 1's piece begins the unit (slot 1), the others begin inside it (slot 0)
   auto slot = [&](int i) { return (int64_t)(((i * U + member) << 1) + (i == g - 1 ? 1 : 0)) * NR + r; };
   float m = -INFINITY;
   for (int i = g - 1 + lane; i <= last; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2]);
   m = warp_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  for (int i = g - 1 + lane; i <= last; i += 32)
-    l += exp2f(p.part_ml[slot(i) * 2] - ref) * p.part_ml[slot(i) * 2 + 1];
-  l = warp_sum(l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* out = reinterpret_cast<T*>(p.out) + (int64_t)(s.row0 + unit_row + r) * p.C;
-  for (int d = lane * 4; d < p.C; d += 128) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = g - 1; i <= last; ++i) {
-      const int64_t at = slot(i);
-      const float mi = p.part_ml[at * 2];
-      if (mi == -INFINITY && p.part_ml[at * 2 + 1] == 0.f) continue;    // a range without a key
-      const float wi = exp2f(mi - ref);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * p.C + d);
-      a.x = fmaf(wi, v.x, a.x);
-      a.y = fmaf(wi, v.y, a.y);
-      a.z = fmaf(wi, v.z, a.z);
-      a.w = fmaf(wi, v.w, a.w);
-    }
-    float f[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
-    if constexpr (sizeof(T) == 4) {
-      store_pack<T, 4>(out + d, f);
-    } else {
-      uint2 u;
-      T* e = reinterpret_cast<T*>(&u);
+  T* out = reinterpret_cast<T*>(p.out) + (int64_t)(job.y + r) * p.C;
+  for (int d0 = 0; d0 < p.C; d0 += 512) {
+    float l = 0.f;
+    float4 a[4] = {};
+    for (int i0 = g - 1; i0 <= last; i0 += 32) {
+      // a lane a piece: its weight, 0 for a range without a key (whose o was not written)
+      const int i = i0 + lane;
+      float w = 0.f;
+      if (i <= last) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
+        if (ml.x != -INFINITY || ml.y != 0.f) w = exp2f(ml.x - ref);
+        l = fmaf(w, ml.y, l);
+      }
+      const int cnt = min(32, last - i0 + 1);
+#pragma unroll 2
+      for (int k = 0; k < cnt; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        if (wk == 0.f) continue;                  // alike in every lane
+        const float* o = p.part_o + slot(i0 + k) * p.C + d0 + lane * 4;
+        float4 v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = Elem<T>::from_f(f[k]);
-      *reinterpret_cast<uint2*>(out + d) = u;
+        for (int j = 0; j < 4; ++j)
+          if (d0 + lane * 4 + 128 * j < p.C) v[j] = *reinterpret_cast<const float4*>(o + 128 * j);
+          else v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j].x = fmaf(wk, v[j].x, a[j].x);
+          a[j].y = fmaf(wk, v[j].y, a[j].y);
+          a[j].z = fmaf(wk, v[j].z, a[j].z);
+          a[j].w = fmaf(wk, v[j].w, a[j].w);
+        }
+      }
+    }
+    l = warp_sum(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = d0 + lane * 4 + 128 * j;
+      if (d >= p.C) continue;
+      float f[4] = {a[j].x * inv, a[j].y * inv, a[j].z * inv, a[j].w * inv};
+      if constexpr (sizeof(T) == 4) {
+        store_pack<T, 4>(out + d, f);
+      } else {
+        uint2 u;
+        T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = Elem<T>::from_f(f[k]);
+        *reinterpret_cast<uint2*>(out + d) = u;
+      }
     }
   }
 }
@@ -538,15 +597,21 @@ int launch_rope(const RopeParams& p, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.n_tokens + (int64_t)kInsertWarps - 1) / kInsertWarps)), block(32 * kInsertWarps);
+  int64_t blocks = (p.n_tokens + (int64_t)kInsertWarps - 1) / kInsertWarps;
+  if (blocks > 152 * 12) blocks = 152 * 12;      // then a warp takes several tokens in turn
+  const dim3 grid((unsigned)blocks), block(32 * kInsertWarps);
   const cudaError_t e = dtype == V4A_BF16 ? launch_pdl(latent_insert_kernel<__nv_bfloat16>, grid, block, 0, st, p)
                                           : launch_pdl(latent_insert_kernel<float>, grid, block, 0, st, p);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.n_rows + (int64_t)kGatherRows - 1) / kGatherRows));
-  return launch_pdl(latent_gather_kernel, grid, dim3(kGatherThreads), 0, st, p) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  // fewer rows a block while that leaves SMs without one
+  int rows = kGatherRows;
+  while (rows > 8 && (int64_t)p.n_rows < (int64_t)rows * 2 * 152) rows /= 2;
+  const dim3 grid((unsigned)(((int64_t)p.n_rows + rows - 1) / rows));
+  return launch_pdl(latent_gather_kernel, grid, dim3(kGatherThreads), 0, st, p, rows) == cudaSuccess ? V4A_OK
+                                                                                                   : V4A_ERR_CUDA;
 }
 
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st) {

@@ -77,7 +77,8 @@ struct LatentAttnParams {
   CacheView cache;
   LatentPlan plan;
   float* part_o;                      // [teams * U][2][NR][C] unnormalised, fp32
-  float* part_ml;                     // [teams * U][2][NR][2] maximum (log2 units) and sum
+  float* part_ml;                     // [teams * U][2][NR][2] reference (log2 units) and sum
+  int32_t* part_job;                  // [teams * U][4] what to merge (LatentPiece::job)
   int32_t* err;
 };
 
@@ -221,15 +222,17 @@ struct LatentPiece {
   int seq_row0;                // first row of the sequence
   int whole;                   // the piece holds every tile of the unit: write the result
   int slot;                    // where its partial result goes otherwise
+  int job_rows, job_last;      // set where the piece is the second of its unit's pieces (see below)
 };
 
 // Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
 // the prefix sums are read in begin() only.
 struct LatentWalk {
-  int x, x1, team, member, n;
+  int x, x1, team, member, total, n;
   int b, base;      // current sequence and the pairs before it
   __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int cta, int n_cta) {
-    const int total = pre[p.n_seq], U = p.plan.U;
+    const int U = p.plan.U;
+    total = pre[p.n_seq];
     team = cta / U;
     member = cta % U;
     if (p.plan.teams == 0) {       // whole shares in turn, the teams striding over them
@@ -243,6 +246,14 @@ struct LatentWalk {
     }
     b = x < x1 ? latent_seq_at(pre, p.n_seq, x) : 0;
     base = x < x1 ? pre[b] : 0;
+  }
+  // A team's merge job, if any, is its first piece's: every team posts one, empty or not,
+  // before that piece's results.
+  __device__ __forceinline__ void post(const LatentAttnParams& p, const LatentPiece* w) const {
+    if (p.plan.teams == 0) return;
+    const int rows = w ? w->job_rows : 0;
+    *reinterpret_cast<int4*>(p.part_job + 4 * (team * p.plan.U + member)) =
+        make_int4(rows, rows > 0 ? w->row0 : 0, rows > 0 ? w->job_last : 0, 0);
   }
   // The next piece, or false. A piece may have no unit (rows == 0) or no keys.
   __device__ __forceinline__ bool next(const LatentAttnParams& p, LatentPiece& w) {
@@ -268,6 +279,7 @@ struct LatentWalk {
       w.tile1 = unit_tiles;
       w.whole = 1;
       w.slot = 0;
+      w.job_rows = 0;
       x += n;
     } else {
       const int take = min(s.tiles - t, x1 - x);
@@ -275,6 +287,12 @@ struct LatentWalk {
       w.slot = ((team * p.plan.U + member) << 1) + (t == 0 ? 1 : 0);
       w.tile0 = min(t, unit_tiles);
       w.tile1 = min(t + take, unit_tiles);
+      // The team that holds the second piece of a unit posts the unit's merge: teams team - 1
+      // to job_last hold its pieces, in slot 1 of the first and slot 0 of the others.
+      const int x0 = x - t;
+      const bool second = t > 0 && latent_team_begin(team - 1, total, n) <= x0;
+      w.job_rows = second ? w.rows : 0;
+      w.job_last = second ? latent_team_of(x0 + s.tiles - 1, total, n) : 0;
       x += take;
     }
     return true;

@@ -44,8 +44,13 @@ RotTab make_rot(const v4a_rope_cfg* r) {
     b = std::fmin(std::ceil(pair(r->low)), d - 1);
     b = a + std::fmax(b - a, 1e-3);
   }
+  // theta_i = base^(-2i/d): a power for every eighth pair, products in between
+  double step[8] = {1};
+  for (int k = 1; k < 8; ++k) step[k] = std::pow(base, -2.0 * k / d);
+  double theta0 = 1;
   for (int i = 0; i < r->dim / 2; ++i) {
-    double theta = std::pow(base, -2.0 * i / d);
+    if (i % 8 == 0) theta0 = std::pow(base, -2.0 * i / d);
+    double theta = theta0 * step[i % 8];
     double keep = 1;
     if (r->scaling == V4A_ROPE_SCALE_LINEAR) keep = 0;
     if (r->scaling == V4A_ROPE_SCALE_BY_PARTS)
@@ -130,10 +135,11 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   return true;
 }
 
-size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at) {
+size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, size_t* job_at) {
   const size_t slots = (size_t)pl.teams * pl.U * 2;
   *ml_at = align_up(slots * pl.NR * c->latent_dim * sizeof(float), 256);
-  return pl.teams == 0 ? 0 : *ml_at + align_up(slots * pl.NR * 2 * sizeof(float), 256);
+  *job_at = *ml_at + align_up(slots * pl.NR * 2 * sizeof(float), 256);
+  return pl.teams == 0 ? 0 : *job_at + align_up(slots * 2 * sizeof(int32_t), 256);
 }
 
 }  // namespace
@@ -226,11 +232,11 @@ int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows, 
 size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                                       int64_t max_pos) {
   LatentPlan pl;
-  size_t ml_at;
+  size_t ml_at, job_at;
   if (check_latent(cfg) || n_seq < 0 || n_seq > V4A_MAX_SEQ || n_tokens < 0 || max_pos < 0 ||
       max_pos >= V4A_MAX_POS || n_tokens == 0 || n_seq == 0)
     return 0;
-  return make_plan(cfg, n_seq, n_tokens, max_pos, &pl) ? part_bytes(cfg, pl, &ml_at) : 0;
+  return make_plan(cfg, n_seq, n_tokens, max_pos, &pl) ? part_bytes(cfg, pl, &ml_at, &job_at) : 0;
 }
 
 int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, const int32_t* cu_tokens,
@@ -245,8 +251,8 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, 
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return V4A_ERR_ARG;
   LatentAttnParams p{};
   if (!make_plan(cfg, n_seq, n_tokens, max_pos, &p.plan)) return V4A_ERR_UNSUPPORTED;
-  size_t ml_at = 0;
-  const size_t need = part_bytes(cfg, p.plan, &ml_at);
+  size_t ml_at = 0, job_at = 0;
+  const size_t need = part_bytes(cfg, p.plan, &ml_at, &job_at);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return V4A_ERR_ARG;
   p.n_seq = n_seq;
   p.n_tokens = n_tokens;
@@ -262,6 +268,7 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, 
   p.cache = view_of(cache);
   p.part_o = reinterpret_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + ml_at);
+  p.part_job = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + job_at);
   p.err = dev_err;
   return launch_latent_attn(p, cfg->dtype, reinterpret_cast<cudaStream_t>(stream));
 }

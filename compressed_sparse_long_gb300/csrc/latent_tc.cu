@@ -181,7 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ru;
       return r;
     };
+    bool posted = false;
     while (ok && walk.next(p, w)) {
+      if (tid == 0 && !posted) walk.post(p, &w);
+      posted = true;
       if (w.rows == 0) continue;
       // lane c: row c of this half, the keys it sees
       const int my_row = half * 32 + lane;
@@ -372,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(oempty);
       }
     }
+    if (tid == 0 && !posted) walk.post(p, nullptr);
   } else if (warp == 8) {
     // ------------------------------------------------------------------------ copies
     if (lane == 0) {

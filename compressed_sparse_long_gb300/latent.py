@@ -19,32 +19,43 @@ Prompts, after a cached prefix or none (expanded form)::
 from __future__ import annotations
 
 from contextlib import nullcontext
+from ctypes import byref
 
 import torch
 
-from . import (BF16, FP32, LatentCfg, RopeCfg, v4a_latent_attn, v4a_latent_attn_expanded,
-               v4a_latent_attn_workspace_size, v4a_latent_gather, v4a_latent_insert, v4a_rope)
+from . import (BF16, FP32, Cache, LatentCfg, RopeCfg, _check, library)
 from .layer import PagedPool
 
 _TYPES = {BF16: torch.bfloat16, FP32: torch.float32}
+_KINDS = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
-def _need(t, name, dtype, shape, contiguous=True):
-    """A tensor of this type and shape (None: any size) on the current device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _need(t, name, dev, dtype, shape, contiguous=True):
+    """Check that t is a tensor of this type and shape (None: any size) on device `dev`, the
+    current one. (The calls here are a few microseconds of GPU time at decode sizes, so the
+    checks are kept as cheap as they can be.)"""
+    try:
+        if t.dtype is dtype and t.get_device() == dev:
+            sh = t.shape
+            if len(sh) == len(shape):
+                for w, g in zip(shape, sh):
+                    if w is not None and w != g:
+                        break
+                else:
+                    if t.is_contiguous() or not (contiguous or (t.numel() and t.stride(-1) != 1)):
+                        return
+    except AttributeError:
+        raise ValueError("%s: expected a CUDA tensor" % name) from None
+    if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d"
-                         % (name, t.device, torch.cuda.current_device()))
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+    if t.dtype is not dtype:
         raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+    if len(t.shape) != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
         raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if contiguous and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if not contiguous and t.numel() and t.stride(-1) != 1:
-        raise ValueError("%s: its last dimension must have stride 1" % name)
-    return t
+    raise ValueError("%s must be contiguous" % name if contiguous else
+                     "%s: its last dimension must have stride 1" % name)
 
 
 def _stride(t, d):
@@ -57,24 +68,45 @@ def _on(stream):
     return nullcontext() if stream is None or isinstance(stream, int) else torch.cuda.stream(stream)
 
 
+def _raw(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _word(dev_err, dev):
+    if dev_err is None:
+        return None
+    _need(dev_err, "dev_err", dev, torch.int32, (1,))
+    return dev_err.data_ptr()
+
+
 def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
          inverse: bool = False, dev_err=None, stream=None) -> torch.Tensor:
     """Rotate x [n, H, dim] or [n, dim] (bf16 or fp32, any strides with a dense last dimension:
     a slice of wider heads, say) at positions pos [n] int64. ``out`` is a new tensor unless
     given; ``out=x`` rotates in place. ``inverse`` turns back; it is also the gradient's map."""
-    kinds = {torch.bfloat16: BF16, torch.float32: FP32}
-    if not isinstance(x, torch.Tensor) or x.dtype not in kinds or x.dim() not in (2, 3):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _KINDS or x.dim() not in (2, 3):
         raise ValueError("x: expected a bfloat16 or float32 tensor [n, H, dim] or [n, dim]")
-    _need(x, "x", x.dtype, (None,) * (x.dim() - 1) + (cfg.dim,), contiguous=False)
-    _need(pos, "pos", torch.int64, (x.shape[0],))
+    dev = torch.cuda.current_device() if x.is_cuda else -2
+    shape = x.shape
+    _need(x, "x", dev, x.dtype, (None,) * (len(shape) - 1) + (cfg.dim,), contiguous=False)
+    _need(pos, "pos", dev, torch.int64, (shape[0],))
     if out is None:
-        with _on(stream):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(shape, x.dtype, x.device, stream)
     else:
-        _need(out, "out", x.dtype, tuple(x.shape), contiguous=False)
-    heads, xh, oh = (1, 0, 0) if x.dim() == 2 else (x.shape[1], _stride(x, 1), _stride(out, 1))
-    v4a_rope(cfg, kinds[x.dtype], x.shape[0], heads, pos, x, _stride(x, 0), xh, out,
-             _stride(out, 0), oh, inverse, dev_err, stream)
+        _need(out, "out", dev, x.dtype, shape, contiguous=False)
+    heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
+    _check("v4a_rope", library().v4a_rope(
+        byref(cfg), _KINDS[x.dtype], shape[0], heads, pos.data_ptr(), x.data_ptr(), _stride(x, 0),
+        xh, out.data_ptr(), _stride(out, 0), oh, inverse, _word(dev_err, dev), _raw(stream, dev)))
     return out
 
 
@@ -91,25 +123,32 @@ class LatentLayer:
         self.cfg, self.pool, self.gamma = cfg, pool, gamma
         self.dtype = _TYPES[cfg.dtype]
         self.width = cfg.latent_dim + cfg.rope.dim
+        dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
         if pool is not None:
-            _need(pool.data, "pool.data", self.dtype, (None, self.width))
-            _need(pool.block_table, "pool.block_table", torch.int32, (None, None))
+            _need(pool.data, "pool.data", dev, self.dtype, (None, self.width))
+            _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
         if gamma is not None:
-            _need(gamma, "gamma", torch.float32, (cfg.latent_dim,))
+            _need(gamma, "gamma", dev, torch.float32, (cfg.latent_dim,))
         self._ws = {}
 
     def _batch(self, cu, start):
-        _need(cu, "cu", torch.int32, (None,))
-        n_seq = cu.numel() - 1
-        if n_seq < 0:
-            raise ValueError("cu: expected the sequences' first rows and the end")
+        """(device, sequences, cache descriptor) of a call over the cache."""
         if self.pool is None:
             raise ValueError("this layer has no cache")
-        if n_seq > self.pool.block_table.shape[0]:
-            raise ValueError("cu has %d sequences, the block table %d"
-                             % (n_seq, self.pool.block_table.shape[0]))
-        _need(start, "start", torch.int64, (n_seq,))
-        return n_seq
+        data, bt = self.pool.data, self.pool.block_table
+        dev = torch.cuda.current_device() if data.is_cuda else -2
+        _need(cu, "cu", dev, torch.int32, (None,))
+        n_seq = cu.shape[0] - 1
+        if n_seq < 0:
+            raise ValueError("cu: expected the sequences' first rows and the end")
+        _need(start, "start", dev, torch.int64, (n_seq,))
+        _need(data, "pool.data", dev, self.dtype, (None, self.width))
+        _need(bt, "pool.block_table", dev, torch.int32, (None, None))
+        if n_seq > bt.shape[0]:
+            raise ValueError("cu has %d sequences, the block table %d" % (n_seq, bt.shape[0]))
+        rows = self.pool.rows_per_block
+        return dev, n_seq, Cache(data.data_ptr(), None, bt.data_ptr(), bt.shape[1], rows,
+                                 data.shape[0] // rows, self.width, 0)
 
     def _workspace(self, nbytes, device, stream):
         """Kept per stream, so calls on two streams never share one; a call being captured
@@ -119,49 +158,56 @@ class LatentLayer:
         with _on(stream):
             if torch.cuda.is_current_stream_capturing():
                 return torch.empty(nbytes, dtype=torch.uint8, device=device)
-            key = stream if isinstance(stream, int) else torch.cuda.current_stream().cuda_stream
+            key = _raw(stream, device)
             ws = self._ws.get(key)
-            if ws is None or ws.numel() < nbytes:
+            if ws is None or ws.shape[0] < nbytes:
                 ws = self._ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
             return ws
 
     def insert(self, cu, start, c, k_pe, dev_err=None, stream=None):
         """Write the cache rows of new tokens: c [n, latent_dim], k_pe [n, rope dim] (rows may
         be strided: two slices of one projection's output)."""
-        n_seq = self._batch(cu, start)
-        _need(c, "c", self.dtype, (None, self.cfg.latent_dim), contiguous=False)
-        _need(k_pe, "k_pe", self.dtype, (c.shape[0], self.cfg.rope.dim), contiguous=False)
-        v4a_latent_insert(self.cfg, n_seq, c.shape[0], cu, start, c, _stride(c, 0), k_pe,
-                          _stride(k_pe, 0), self.gamma, self.pool.c, dev_err, stream)
+        dev, n_seq, cache = self._batch(cu, start)
+        _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
+        _need(k_pe, "k_pe", dev, self.dtype, (c.shape[0], self.cfg.rope.dim), contiguous=False)
+        _check("v4a_latent_insert", library().v4a_latent_insert(
+            byref(self.cfg), n_seq, c.shape[0], cu.data_ptr(), start.data_ptr(), c.data_ptr(),
+            _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),
+            None if self.gamma is None else self.gamma.data_ptr(), byref(cache),
+            _word(dev_err, dev), _raw(stream, dev)))
 
     def gather(self, cu, start, n_rows, out=None, dev_err=None, stream=None):
         """Copy cached rows out: sequence b's rows cu[b] .. cu[b+1]-1 of the result are its
         cache rows from position start[b] on. n_rows is cu's last value (rows of a larger
         result behind it are left as they are)."""
-        n_seq = self._batch(cu, start)
+        dev, n_seq, cache = self._batch(cu, start)
         if out is None:
-            with _on(stream):
-                out = torch.empty((n_rows, self.width), dtype=self.dtype, device=cu.device)
+            out = _new((n_rows, self.width), self.dtype, cu.device, stream)
         else:
-            _need(out, "out", self.dtype, (n_rows, self.width))
-        v4a_latent_gather(self.cfg, n_seq, n_rows, cu, start, self.pool.c, out, dev_err, stream)
+            _need(out, "out", dev, self.dtype, (n_rows, self.width))
+        _check("v4a_latent_gather", library().v4a_latent_gather(
+            byref(self.cfg), n_seq, n_rows, cu.data_ptr(), start.data_ptr(), byref(cache),
+            out.data_ptr(), _word(dev_err, dev), _raw(stream, dev)))
         return out
 
     def attention(self, cu, start, max_pos, q, out=None, dev_err=None, stream=None):
         """Absorbed attention of q [n, H, latent_dim + rope dim] over the cache: one new token
         a sequence (decode) or chunks; returns [n, H, latent_dim]."""
-        n_seq = self._batch(cu, start)
+        dev, n_seq, cache = self._batch(cu, start)
         h = self.cfg.n_heads
-        _need(q, "q", self.dtype, (None, h, self.width))
-        shape = (q.shape[0], h, self.cfg.latent_dim)
+        _need(q, "q", dev, self.dtype, (None, h, self.width))
+        n = q.shape[0]
         if out is None:
-            with _on(stream):
-                out = torch.empty(shape, dtype=self.dtype, device=q.device)
+            out = _new((n, h, self.cfg.latent_dim), self.dtype, q.device, stream)
         else:
-            _need(out, "out", self.dtype, shape)
-        nb = v4a_latent_attn_workspace_size(self.cfg, n_seq, q.shape[0], max_pos)
-        v4a_latent_attn(self.cfg, n_seq, q.shape[0], cu, start, max_pos, q, self.pool.c, out,
-                        self._workspace(nb, q.device, stream), dev_err, stream)
+            _need(out, "out", dev, self.dtype, (n, h, self.cfg.latent_dim))
+        lib, cfg = library(), byref(self.cfg)
+        nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
+        ws = self._workspace(nb, q.device, stream)
+        _check("v4a_latent_attn", lib.v4a_latent_attn(
+            cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
+            out.data_ptr(), None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev),
+            _raw(stream, dev)))
         return out
 
     def attention_expanded(self, cu_q, cu_k, q, k, k_pe, v, causal=True, out=None, dev_err=None,
@@ -170,23 +216,27 @@ class LatentLayer:
         (shared by the heads), v [n_k, H, v_dim]; k, k_pe and v may be strided slices of wider
         rows. Returns [n_q, H, v_dim]."""
         c = self.cfg
-        _need(cu_q, "cu_q", torch.int32, (None,))
-        _need(cu_k, "cu_k", torch.int32, (cu_q.numel(),))
-        if cu_q.numel() == 0:
+        dev = torch.cuda.current_device() if q.is_cuda else -2
+        _need(cu_q, "cu_q", dev, torch.int32, (None,))
+        n_seq = cu_q.shape[0] - 1
+        if n_seq < 0:
             raise ValueError("cu_q: expected the sequences' first rows and the end")
-        _need(q, "q", self.dtype, (None, c.n_heads, c.nope_dim + c.rope.dim))
-        _need(k, "k", self.dtype, (None, c.n_heads, c.nope_dim), contiguous=False)
-        _need(k_pe, "k_pe", self.dtype, (k.shape[0], c.rope.dim), contiguous=False)
-        _need(v, "v", self.dtype, (k.shape[0], c.n_heads, c.v_dim), contiguous=False)
+        _need(cu_k, "cu_k", dev, torch.int32, (n_seq + 1,))
+        _need(q, "q", dev, self.dtype, (None, c.n_heads, c.nope_dim + c.rope.dim))
+        _need(k, "k", dev, self.dtype, (None, c.n_heads, c.nope_dim), contiguous=False)
+        n_k = k.shape[0]
+        _need(k_pe, "k_pe", dev, self.dtype, (n_k, c.rope.dim), contiguous=False)
+        _need(v, "v", dev, self.dtype, (n_k, c.n_heads, c.v_dim), contiguous=False)
         shape = (q.shape[0], c.n_heads, c.v_dim)
         if out is None:
-            with _on(stream):
-                out = torch.empty(shape, dtype=self.dtype, device=q.device)
+            out = _new(shape, self.dtype, q.device, stream)
         else:
-            _need(out, "out", self.dtype, shape)
-        v4a_latent_attn_expanded(c, cu_q.numel() - 1, q.shape[0], cu_q, k.shape[0], cu_k, q, k,
-                                 _stride(k, 0), _stride(k, 1), k_pe, _stride(k_pe, 0), v,
-                                 _stride(v, 0), _stride(v, 1), causal, out, dev_err, stream)
+            _need(out, "out", dev, self.dtype, shape)
+        _check("v4a_latent_attn_expanded", library().v4a_latent_attn_expanded(
+            byref(c), n_seq, q.shape[0], cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
+            k.data_ptr(), _stride(k, 0), _stride(k, 1), k_pe.data_ptr(), _stride(k_pe, 0),
+            v.data_ptr(), _stride(v, 0), _stride(v, 1), causal, out.data_ptr(),
+            _word(dev_err, dev), _raw(stream, dev)))
         return out
 
     def step(self, cu, start, max_pos, pos, c, k_pe, q, out=None, dev_err=None, stream=None):
