@@ -341,8 +341,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
   int seq = 0, head = 0, item = blockIdx.x;
   bool posted = false;
   if constexpr (kPaged) {
-    latent_prefix(p, pre, warp_tot);
-    walk.begin(p, pre, blockIdx.x, gridDim.x);
+    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
   }
   for (;;) {
     // ---- the next unit: its query rows and its keys
@@ -502,19 +501,18 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
 
 // ------------------------------------------------------------------------------ merge
 // The results of a unit whose tiles fell to several teams: out = sum_i w_i o_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max). Block (g, member, rows) does the job that team g posted; a warp a
-// row. Bound: latency (job, statistics, partial results: three loads in a row).
+// with w_i = 2^(m_i - max). Block (cta, rows) does the job that the CTA posted; a warp a row.
+// Bound: latency (job, statistics, partial results: three loads in a row).
 constexpr int kMergeWarps = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int U = p.plan.U, NR = p.plan.NR;
-  const int g = blockIdx.x / U + 1, member = blockIdx.x % U;
-  const int4 job = *reinterpret_cast<const int4*>(p.part_job + 4 * (g * U + member));
-  const int r = blockIdx.y * kMergeWarps + warp, last = job.z;
+  const int4 job = *reinterpret_cast<const int4*>(p.part_job + 4 * blockIdx.x);
+  const int r = blockIdx.y * kMergeWarps + warp, NR = p.plan.NR;
   if (r >= job.x) return;
+  const int U = job.w, g = blockIdx.x / U, member = blockIdx.x % U, last = job.z;
   // team g - 1's piece begins the unit (slot 1), the others begin inside it (slot 0)
   auto slot = [&](int i) { return (int64_t)(((i * U + member) << 1) + (i == g - 1 ? 1 : 0)) * NR + r; };
   float m = -INFINITY;
@@ -615,8 +613,8 @@ int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st) {
-  if (p.plan.teams < 2) return cudaSuccess;
-  const dim3 grid((unsigned)((p.plan.teams - 1) * p.plan.U), (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps));
+  if (!p.plan.split) return cudaSuccess;
+  const dim3 grid((unsigned)p.plan.ctas, (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps));
   return dtype == V4A_BF16 ? launch_pdl(latent_merge_kernel<__nv_bfloat16>, grid, dim3(32 * kMergeWarps), 0, st, p)
                            : launch_pdl(latent_merge_kernel<float>, grid, dim3(32 * kMergeWarps), 0, st, p);
 }
@@ -626,13 +624,8 @@ int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
   if (p.plan.tc) {
     e = launch_latent_attn_tc(p, st);
   } else {
-    int64_t grid = (int64_t)p.plan.teams * p.plan.U;
-    if (grid == 0) {
-      grid = ((int64_t)p.n_tokens * p.H + p.plan.NR - 1) / p.plan.NR + p.n_seq;
-      if (grid > 65536) grid = 65536;
-    }
-    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, grid, st)
-                          : run_gen<float, true>(p, p.C + p.R, p.C, grid, st);
+    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, p.plan.ctas, st)
+                          : run_gen<float, true>(p, p.C + p.R, p.C, p.plan.ctas, st);
   }
   if (e == cudaSuccess) e = launch_latent_merge(p, dtype, st);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;

@@ -57,12 +57,16 @@ struct LatentGatherParams {
 // The work of an absorbed call. The rows (token, head) of a sequence are consecutive rows of
 // q; they are cut into units of NR rows, and the sequence's keys into tiles of TK. Lengths are
 // known on the device only, so every CTA derives the plan from cu and start: U consecutive
-// units of a sequence form a team's share (its members walk the same key tiles at the same
-// time and meet in L2), `teams` teams take equal parts of all (share, tile) pairs in order.
-// A unit whose tiles fall to several teams is left as partial results that a second kernel
-// merges. With teams == 0 whole units go to the CTAs in turn and nothing is merged.
+// units of a sequence form a share (its members walk the same key tiles at the same time and
+// meet in L2), CTAs in teams of U take equal parts of all (share, tile) pairs in order. A unit
+// whose tiles fall to several teams is left as partial results that a second kernel merges.
+// U is 1, 2 or 4, at most max_U, the largest that costs no more than 1/8 in members without a
+// unit. Without split, whole units go to the CTAs in turn and nothing is merged.
 struct LatentPlan {
-  int32_t NR, TK, U, teams;
+  int32_t NR, TK;
+  int32_t max_U;
+  int32_t ctas;                       // a multiple of max_U
+  int32_t split;
   int32_t tc;                         // tensor-core kernel
 };
 
@@ -76,9 +80,9 @@ struct LatentAttnParams {
   void* out;
   CacheView cache;
   LatentPlan plan;
-  float* part_o;                      // [teams * U][2][NR][C] unnormalised, fp32
-  float* part_ml;                     // [teams * U][2][NR][2] reference (log2 units) and sum
-  int32_t* part_job;                  // [teams * U][4] what to merge (LatentPiece::job)
+  float* part_o;                      // [ctas][2][NR][C] unnormalised, fp32
+  float* part_ml;                     // [ctas][2][NR][2] reference (log2 units) and sum
+  int32_t* part_job;                  // [ctas][4] what to merge (LatentPiece::job)
   int32_t* err;
 };
 
@@ -129,13 +133,15 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t
   return lo;
 }
 
-// One sequence's share of the plan.
+// One sequence's part of the plan.
 struct LatentSeq {
   int row0;          // first row of the batch's (token, head) rows
   int rows;          // rows of the sequence
-  int units, shares; // units of NR rows, shares of U units
+  int units;         // units of NR rows
   int tiles;         // key tiles of the whole sequence (1 in whole-unit plans)
   int64_t start;     // position of its first new token
+  __device__ __forceinline__ int shares(int U) const { return (units + U - 1) / U; }
+  __device__ __forceinline__ int pairs(int U) const { return shares(U) * tiles; }
 };
 
 __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b) {
@@ -146,9 +152,8 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b
   s.rows = n * p.H;
   s.start = __ldg(p.start + b);
   s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
-  s.shares = (s.units + p.plan.U - 1) / p.plan.U;
   const int64_t keys = min(s.start + n, p.max_pos + 1);
-  s.tiles = p.plan.teams == 0 ? 1 : (keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK));
+  s.tiles = !p.plan.split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
   return s;
 }
 
@@ -186,12 +191,37 @@ __device__ __forceinline__ void seq_prefix(int n_seq, int32_t* pre, int32_t* war
   if (threadIdx.x == 0) pre[n_seq] = carry;
   __syncthreads();
 }
-// (share, tile) pairs of the sequences of an absorbed call.
-__device__ __forceinline__ void latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
-  seq_prefix(p.n_seq, pre, warp_tot, [&](int b) {
-    const LatentSeq s = latent_seq(p, b);
-    return s.shares * s.tiles;
-  });
+// Sum of v over the block.
+__device__ __forceinline__ int block_sum(int v, int32_t* warp_tot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_tot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += warp_tot[i];
+  return v;
+}
+// U and the (share, tile) pairs before each sequence of an absorbed call, by the whole block.
+__device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+  int U = p.plan.max_U;
+  if (U > 1) {
+    int c1 = 0, c2 = 0, c4 = 0;
+    for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) {
+      const LatentSeq s = latent_seq(p, b);
+      c1 += s.pairs(1);
+      c2 += s.pairs(2);
+      c4 += s.pairs(4);
+    }
+    c1 = block_sum(c1, warp_tot);
+    c2 = block_sum(c2, warp_tot);
+    c4 = block_sum(c4, warp_tot);
+    const int most = c1 + c1 / 8;
+    if (U == 4 && (int64_t)c4 * 4 > most) U = 2;
+    if (U == 2 && (int64_t)c2 * 2 > most) U = 1;
+  }
+  seq_prefix(p.n_seq, pre, warp_tot, [&](int b) { return latent_seq(p, b).pairs(U); });
+  return U;
 }
 
 // The sequence that holds position x of the prefix sums (pre[b] <= x < pre[b + 1]).
@@ -204,8 +234,7 @@ __device__ __forceinline__ int latent_seq_at(const int32_t* pre, int n_seq, int 
   return lo;
 }
 
-// Teams that share `total` pairs, team g taking [g * total / n, (g + 1) * total / n).
-__device__ __forceinline__ int latent_teams(const LatentPlan& pl, int total) { return min(pl.teams, total); }
+// n teams share `total` pairs, team g taking [g * total / n, (g + 1) * total / n).
 __device__ __forceinline__ int latent_team_begin(int g, int total, int n) {
   return (int)((int64_t)g * total / n);
 }
@@ -228,19 +257,20 @@ struct LatentPiece {
 // Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
 // the prefix sums are read in begin() only.
 struct LatentWalk {
-  int x, x1, team, member, total, n;
+  int x, x1, cta, team, member, U, total, n;
   int b, base;      // current sequence and the pairs before it
-  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int cta, int n_cta) {
-    const int U = p.plan.U;
+  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int U_) {
+    U = U_;
+    cta = blockIdx.x;
     total = pre[p.n_seq];
     team = cta / U;
     member = cta % U;
-    if (p.plan.teams == 0) {       // whole shares in turn, the teams striding over them
-      n = n_cta / U;
+    if (!p.plan.split) {           // whole shares in turn, the teams striding over them
+      n = p.plan.ctas / U;
       x = team;
       x1 = total;
     } else {
-      n = latent_teams(p.plan, total);
+      n = min(p.plan.ctas / U, total);
       x = team < n ? latent_team_begin(team, total, n) : 0;
       x1 = team < n ? latent_team_begin(team + 1, total, n) : 0;
     }
@@ -250,17 +280,17 @@ struct LatentWalk {
   // A team's merge job, if any, is its first piece's: every team posts one, empty or not,
   // before that piece's results.
   __device__ __forceinline__ void post(const LatentAttnParams& p, const LatentPiece* w) const {
-    if (p.plan.teams == 0) return;
+    if (!p.plan.split) return;
     const int rows = w ? w->job_rows : 0;
-    *reinterpret_cast<int4*>(p.part_job + 4 * (team * p.plan.U + member)) =
-        make_int4(rows, rows > 0 ? w->row0 : 0, rows > 0 ? w->job_last : 0, 0);
+    *reinterpret_cast<int4*>(p.part_job + 4 * cta) =
+        make_int4(rows, rows > 0 ? w->row0 : 0, rows > 0 ? w->job_last : 0, U);
   }
   // The next piece, or false. A piece may have no unit (rows == 0) or no keys.
   __device__ __forceinline__ bool next(const LatentAttnParams& p, LatentPiece& w) {
     if (x >= x1) return false;
     LatentSeq s = latent_seq(p, b);
-    while (x >= base + s.shares * s.tiles) {
-      base += s.shares * s.tiles;
+    while (x >= base + s.pairs(U)) {
+      base += s.pairs(U);
       s = latent_seq(p, ++b);
     }
     const int r = x - base;
@@ -268,13 +298,13 @@ struct LatentWalk {
     w.seq = b;
     w.start = s.start;
     w.seq_row0 = s.row0;
-    const int unit = share * p.plan.U + member, ur = unit * p.plan.NR;
+    const int unit = share * U + member, ur = unit * p.plan.NR;
     w.row0 = s.row0 + ur;
     w.rows = max(0, min(p.plan.NR, s.rows - ur));
     w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
     w.keys0 = w.rows > 0 ? latent_visible(p, s, ur / p.H) : 0;
     const int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
-    if (p.plan.teams == 0) {
+    if (!p.plan.split) {
       w.tile0 = 0;
       w.tile1 = unit_tiles;
       w.whole = 1;
@@ -284,7 +314,7 @@ struct LatentWalk {
     } else {
       const int take = min(s.tiles - t, x1 - x);
       w.whole = take == s.tiles;
-      w.slot = ((team * p.plan.U + member) << 1) + (t == 0 ? 1 : 0);
+      w.slot = (cta << 1) + (t == 0 ? 1 : 0);
       w.tile0 = min(t, unit_tiles);
       w.tile1 = min(t + take, unit_tiles);
       // The team that holds the second piece of a unit posts the unit's merge: teams team - 1

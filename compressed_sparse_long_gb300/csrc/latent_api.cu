@@ -117,29 +117,28 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
   const int64_t rows = (int64_t)n_tokens * c->n_heads;
-  // units of a sequence that walk its keys together: as many as an average sequence has, up to 4
-  pl->U = 1;
-  while (tc && pl->U < 4 && n_seq > 0 && rows / n_seq >= 2 * pl->U * pl->NR) pl->U *= 2;
   const int64_t units = (rows + pl->NR - 1) / pl->NR + n_seq;   // at most, over the sequences
   const int64_t tiles = max_pos / pl->TK + 1;
-  const int sms = sm_count();
-  const int64_t ctas = tc ? sms : 2 * sms;
   if (rows > INT32_MAX / 2) return false;
-  pl->teams = 0;
-  if (units < 4 * ctas) {
-    if (units * tiles >= INT32_MAX) return false;
-    pl->teams = (int32_t)(ctas / pl->U);
-    if (units * tiles < pl->teams) pl->teams = (int32_t)(units * tiles);   // (an upper bound)
-    if (tiles == 1) pl->teams = 0;                              // nothing to split
-  }
+  // sharing key tiles pays where an average sequence has several units (the device decides)
+  pl->max_U = 1;
+  while (tc && pl->max_U < 4 && rows / n_seq >= 2 * pl->max_U * pl->NR) pl->max_U *= 2;
+  const int64_t most = tc ? sm_count() / 4 * 4 : 2 * sm_count();  // CTAs at once
+  // Units are split along the keys where that fills the GPU (fewer than four a CTA) or evens
+  // out sequences of different lengths (few new tokens each). Prompts, whose units' key counts
+  // rise from one to the next, go as whole units, neighbours to neighbouring CTAs.
+  pl->split = tiles > 1 && (units < 4 * most || n_tokens < 4 * (int64_t)n_seq);
+  if (pl->split && units * tiles >= INT32_MAX) return false;
+  const int64_t want = (pl->split ? units * tiles : units) + 3;
+  pl->ctas = (int32_t)(want < most ? want / 4 * 4 : tc || pl->split ? most : want < 65536 ? want / 4 * 4 : 65536);
   return true;
 }
 
 size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, size_t* job_at) {
-  const size_t slots = (size_t)pl.teams * pl.U * 2;
+  const size_t slots = (size_t)pl.ctas * 2;
   *ml_at = align_up(slots * pl.NR * c->latent_dim * sizeof(float), 256);
   *job_at = *ml_at + align_up(slots * pl.NR * 2 * sizeof(float), 256);
-  return pl.teams == 0 ? 0 : *job_at + align_up(slots * 2 * sizeof(int32_t), 256);
+  return pl.split ? *job_at + align_up(slots * 2 * sizeof(int32_t), 256) : 0;
 }
 
 }  // namespace

@@ -155,8 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   LatentPiece w;
   {
     int32_t* pre = reinterpret_cast<int32_t*>(kbuf);
-    latent_prefix(p, pre, warp_tot);
-    walk.begin(p, pre, blockIdx.x, gridDim.x);
+    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
   }
   tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
   tc::fence_before_sync();
@@ -521,19 +520,10 @@ cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st) {
   if (!encode_byte_rows_map(&qmap, p.q, (uint64_t)rows, kW * 2, 128, kNR) ||
       !encode_byte_rows_map(&kmap, p.cache.data, (uint64_t)pool_rows, kW * 2, 128, kTK))
     return cudaErrorInvalidValue;
-  int64_t grid = (int64_t)p.plan.teams * p.plan.U;
-  if (grid == 0) {
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    grid = (rows + kNR - 1) / kNR + p.n_seq;
-    if (grid > sms) grid = sms;
-    grid = (grid + p.plan.U - 1) / p.plan.U * p.plan.U;
-  }
   const cudaError_t e =
       cudaFuncSetAttribute(latent_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_attn_tc, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, st, p, qmap, kmap);
+  return launch_pdl(latent_attn_tc, dim3((unsigned)p.plan.ctas), dim3(kThreads), kSmemBytes, st, p, qmap, kmap);
 }
 
 }  // namespace v4a

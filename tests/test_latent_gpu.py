@@ -232,6 +232,10 @@ SHAPES = [
     (BF, 5, 512, 64, [200, 400], [77, 13]),
     (BF, 96, 512, 64, [130], [130]),
     (BF, 64, 512, 64, [5000], [2]),
+    (BF, 64, 512, 64, [700, 40, 2], [650, 40, 1]),       # many units: whole ones in turn
+    (BF, 128, 512, 64, [300, 290], [290, 1]),
+    (BF, 40, 512, 64, [256, 255], [2, 255]),
+    (F32, 16, 64, 16, [1300], [1300]),
 ]
 
 
