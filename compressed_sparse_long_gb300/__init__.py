@@ -22,7 +22,7 @@ __all__ = [
     "v4a_attn_decode_q8", "v4a_attn_q8_workspace_size", "v4a_attn_plan",
     "RopeCfg", "LatentCfg", "rope_cfg", "latent_cfg", "v4a_rope", "v4a_latent_insert",
     "v4a_latent_gather", "v4a_latent_attn", "v4a_latent_attn_workspace_size",
-    "v4a_latent_attn_expanded",
+    "v4a_latent_attn_expanded", "v4a_latent_attn_expanded_workspace_size",
     "v4a_get_error", "v4a_version",
     "BF16", "ROPE_INTERLEAVED", "ROPE_HALF", "ROPE_SCALE_NONE", "ROPE_SCALE_LINEAR",
     "ROPE_SCALE_BY_PARTS", "ROPE_SCALE_YARN", "MAX_SEQ",
@@ -127,7 +127,8 @@ _SIGS = {
                                        _P, _P]),
     "v4a_latent_attn_expanded": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _I32, _P, _P, _P, _I64,
                                                 _I64, _P, _I64, _P, _I64, _I64, _I32, _P, _P,
-                                                _P]),
+                                                _SZ, _P, _P]),
+    "v4a_latent_attn_expanded_workspace_size": (_SZ, [_LATENT, _I32, _I32, _I32]),
     "v4a_get_error": (ctypes.c_int, [_P, _P, ctypes.POINTER(_I32)]),
 }
 
@@ -360,11 +361,17 @@ def v4a_latent_attn(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, q, cach
 
 def v4a_latent_attn_expanded(cfg, n_seq, n_q, cu_q, n_k, cu_k, q, k, k_token_stride,
                              k_head_stride, k_pe, k_pe_stride, v, v_token_stride, v_head_stride,
-                             causal, out, dev_err=None, stream=None):
+                             causal, out, workspace, dev_err=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("v4a_latent_attn_expanded", library().v4a_latent_attn_expanded(
         ctypes.byref(cfg), n_seq, n_q, _ptr(cu_q), n_k, _ptr(cu_k), _ptr(q), _ptr(k),
         k_token_stride, k_head_stride, _ptr(k_pe), k_pe_stride, _ptr(v), v_token_stride,
-        v_head_stride, int(causal), _ptr(out), _ptr(dev_err), _stream(stream)))
+        v_head_stride, int(causal), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_err),
+        _stream(stream)))
+
+
+def v4a_latent_attn_expanded_workspace_size(cfg, n_seq, n_q, n_k) -> int:
+    return library().v4a_latent_attn_expanded_workspace_size(ctypes.byref(cfg), n_seq, n_q, n_k)
 
 
 def v4a_get_error(dev_err, stream=None) -> int:

@@ -632,8 +632,7 @@ int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st) {
-  if (dtype == V4A_BF16 && p.DN == 128 && p.DR == 64 && p.DV == 128)
-    return launch_latent_expanded_tc(p, st) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  if (p.tc) return launch_latent_expanded_tc(p, st) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
   int64_t grid = ((int64_t)p.n_q / kGenRows + p.n_seq) * p.H;
   if (grid > 65536) grid = 65536;
   const cudaError_t e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, false>(p, p.DN + p.DR, p.DV, grid, st)

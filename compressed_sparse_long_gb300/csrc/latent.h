@@ -97,6 +97,13 @@ struct LatentExpandedParams {
   const void* v;
   void* out;
   int64_t k_ts, k_hs, pe_ts, v_ts, v_hs;
+  // tensor-core kernel: pairs of CTAs, whether items may be split among them, steps that starting
+  // an item counts for (0 without split: then every item is one step and no pair gets part of
+  // one, so the partial results' pointers are not used), partial results
+  int32_t tc, pairs, split, setup;
+  float* part_o;                      // [pairs][2][512][128] unnormalised, fp32
+  float* part_ml;                     // [pairs][2][512][2] reference (log2 units) and sum
+  int32_t* part_job;                  // [pairs][8] what to merge
   int32_t* err;
 };
 

@@ -237,6 +237,67 @@ __device__ __forceinline__ void mma_bf16_ta_lo(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
+// ------------------------------------------------------------------------ CTA pairs
+// Two CTAs of a cluster work on one product (cta_group::2): the CTA of even rank issues it, each
+// CTA holds its half of the rows of A and D, and half of the columns of B.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address, in the cluster's window, of the same place in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// Arrive on a barrier of any CTA of the cluster. What it publishes is tensor memory (completed
+// by tcgen05.wait::st) or copies that have landed, so nothing of this thread's own stores has to
+// be visible across the cluster first: a release at cluster scope costs 1500 cycles more.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The same after ordinary stores that the arrival publishes.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_bf16_pair_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3}; setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p; }" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_bf16_ta_pair_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 b; mov.b64 b, {%2, %3}; setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once every product issued so far by this thread has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // Byte offset of 16-byte chunk `c` (0..7) of row `r` inside a 128B-swizzled region whose
 // 8-row groups are 1024 bytes apart.
 __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {

@@ -232,11 +232,14 @@ class LatentLayer:
             out = _new(shape, self.dtype, q.device, stream)
         else:
             _need(out, "out", dev, self.dtype, shape)
-        _check("v4a_latent_attn_expanded", library().v4a_latent_attn_expanded(
-            byref(c), n_seq, q.shape[0], cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
+        lib, cfg = library(), byref(c)
+        nb = lib.v4a_latent_attn_expanded_workspace_size(cfg, n_seq, q.shape[0], n_k)
+        ws = self._workspace(nb, q.device, stream)
+        _check("v4a_latent_attn_expanded", lib.v4a_latent_attn_expanded(
+            cfg, n_seq, q.shape[0], cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), _stride(k, 0), _stride(k, 1), k_pe.data_ptr(), _stride(k_pe, 0),
             v.data_ptr(), _stride(v, 0), _stride(v, 1), causal, out.data_ptr(),
-            _word(dev_err, dev), _raw(stream, dev)))
+            None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev), _raw(stream, dev)))
         return out
 
     def step(self, cu, start, max_pos, pos, c, k_pe, q, out=None, dev_err=None, stream=None):

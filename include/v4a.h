@@ -462,6 +462,8 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
  * k, v: device, element (x, h, d) at x * token_stride + h * head_stride + d (strides in
  *       elements, so k and v may be parts of one projection's output); k_pe: device
  *       [n_k, rope.dim], k_pe_stride elements between tokens, shared by the heads
+ * workspace: device, >= v4a_latent_attn_expanded_workspace_size(...) bytes, 256-byte aligned
+ *       (may be NULL where that is 0)
  * All pointers on 16-byte boundaries, strides positive multiples of 16 bytes.
  * Key and value rows at or behind cu_k[n_seq], and other sequences' rows, are not used,
  * whatever they hold. A value that is not finite may reach queries of its sequence that do
@@ -469,12 +471,15 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
  * bf16 with nope = 128, rope.dim = 64 and v_dim = 128 runs on the tensor cores; other shapes
  * on CUDA cores.
  */
+size_t v4a_latent_attn_expanded_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_q,
+                                               int32_t n_k);
 int v4a_latent_attn_expanded(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_q,
                              const int32_t* cu_q, int32_t n_k, const int32_t* cu_k, const void* q,
                              const void* k, int64_t k_token_stride, int64_t k_head_stride,
                              const void* k_pe, int64_t k_pe_stride, const void* v,
                              int64_t v_token_stride, int64_t v_head_stride, int32_t causal,
-                             void* out, int32_t* dev_err, v4a_stream_t stream);
+                             void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                             v4a_stream_t stream);
 
 /* Synchronise `stream`, read the device error word, clear it. *flags_out (may be NULL)
  * receives the bits. Returns V4A_OK, V4A_ERR_DEVICE if any bit was set, or V4A_ERR_CUDA. */

@@ -117,7 +117,7 @@ def test_bad_layers_are_refused(lib, kw, want):
     got = _calls(lib, _cfg(**kw), v4a.Cache(**CACHE))
     assert set(got.values()) == {want}, got
     e = lib.v4a_latent_attn_expanded(B(_cfg(**kw)), 1, 1, 64, 1, 64, 4096, 4096, 128, 128, 4096, 64,
-                                     4096, 128, 128, 1, 4096, None, None)
+                                     4096, 128, 128, 1, 4096, None, 0, None, None)
     assert e == want
     assert v4a.v4a_latent_attn_workspace_size(_cfg(**kw), 1, 1, 100000) == 0
 
@@ -167,9 +167,9 @@ def test_insert_and_attention_arguments(lib):
 
 def test_expanded_arguments(lib):
     def call(cfg=_cfg(), n_seq=1, n_q=2, cu_q=64, n_k=2, cu_k=64, q=4096, k=4096, kt=128, kh=128,
-             pe=4096, ps=64, v=4096, vt=128, vh=128, out=4096):
+             pe=4096, ps=64, v=4096, vt=128, vh=128, out=4096, ws=None, wb=0):
         return lib.v4a_latent_attn_expanded(B(cfg), n_seq, n_q, cu_q, n_k, cu_k, q, k, kt, kh, pe,
-                                            ps, v, vt, vh, 1, out, None, None)
+                                            ps, v, vt, vh, 1, out, ws, wb, None, None)
     for kw in (dict(n_seq=-1), dict(n_q=-1), dict(n_k=-1), dict(cu_q=None), dict(cu_k=None),
                dict(q=None), dict(out=None), dict(q=4104), dict(out=4104), dict(k=None),
                dict(k=4104), dict(pe=None), dict(v=None), dict(kt=100), dict(kh=0), dict(ps=-64),
@@ -177,6 +177,13 @@ def test_expanded_arguments(lib):
         assert call(**kw) == ARG, kw
     assert call(cfg=_cfg(nope_dim=0, softmax_scale=1.0)) == UNS
     assert call(n_seq=v4a.MAX_SEQ + 1) == UNS
+    need = v4a.v4a_latent_attn_expanded_workspace_size(_cfg(), 1, 2, 5000)
+    assert need > 0 and v4a.v4a_latent_attn_expanded_workspace_size(_cfg(), 1, 2, 128) == 0
+    assert v4a.v4a_latent_attn_expanded_workspace_size(_cfg(nope_dim=64), 1, 2, 5000) == 0
+    for kw in (dict(ws=None, wb=need), dict(ws=4100, wb=need), dict(ws=4096, wb=need - 1)):
+        assert call(n_k=5000, **kw) == ARG, kw
+    # more (item, key tile) steps than the plan counts
+    assert call(n_q=1 << 24, n_k=1 << 24) == UNS
     assert call(n_q=0, q=None, out=None, cu_q=None) == OK and call(n_seq=0) == OK
 
 
