@@ -139,17 +139,46 @@ int run_rope(const RopeParams& p, cudaStream_t st) {
 }
 
 // ----------------------------------------------------------------------------- insert
-// One warp per token at a time: the latent row in registers (16-byte vectors, lane l taking
-// vectors l, l + 32, ..), requested before the token's place is looked up; its mean square by
-// shuffles; then the rotary part, lane i turning pairs i, i + 32 with rates it keeps. Bound:
-// latency at decode, HBM for prompts (each row is read and written once).
-constexpr int kInsertWarps = 4;
+// A block takes up to 32 tokens, whose positions and pool rows are looked up first, a thread a
+// token; a warp then takes one token after the other: the latent row in registers (16-byte
+// vectors, lane l taking vectors l, l + 32, ..; the next token's row is requested before this
+// one is worked on), its mean square by shuffles, and the rotary part, lane i turning pairs i,
+// i + 32 with rates it keeps. Bound: latency at decode, HBM for prompts (each row is read and
+// written once).
+constexpr int kInsertWarps = 8, kInsertTokens = 32;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const __grid_constant__ LatentInsertParams p) {
-  constexpr int kV = 16 / (int)sizeof(T), kMaxVec = 1024 / kV / 32;
-  const int lane = threadIdx.x & 31;
+struct InsertRow {
+  static constexpr int kV = 16 / (int)sizeof(T), kMaxVec = 1024 / kV / 32;
+  uint4 v[kMaxVec];
+  T x0[2], x1[2];
+  __device__ __forceinline__ void load(const LatentInsertParams& p, int64_t t, int lane) {
+    const T* c = reinterpret_cast<const T*>(p.c) + t * p.c_stride;
+    const T* k = reinterpret_cast<const T*>(p.k_pe) + t * p.k_stride;
+    const int nv = p.C / kV, np = p.rot.dim / 2;
+    const bool half = p.rot.layout == V4A_ROPE_HALF;
+#pragma unroll
+    for (int i = 0; i < kMaxVec; ++i)
+      if (lane + 32 * i < nv) v[i] = *reinterpret_cast<const uint4*>(c + (lane + 32 * i) * kV);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (i < np) {
+        x0[j] = k[half ? i : 2 * i];
+        x1[j] = k[half ? i + np : 2 * i + 1];
+      }
+    }
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kInsertWarps)
+    latent_insert_kernel(const __grid_constant__ LatentInsertParams p, int tokens) {
+  constexpr int kV = InsertRow<T>::kV, kMaxVec = InsertRow<T>::kMaxVec;
+  __shared__ int64_t slots[kInsertTokens], at[kInsertTokens];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int np = p.rot.dim / 2, nv = p.C / kV;
+  const int t0 = blockIdx.x * tokens, nt = min(tokens, p.n_tokens - t0);
   float rate[2][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -160,36 +189,30 @@ __global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const 
     rate[j][3] = p.rot.psi_lo[i];
   }
   pdl_wait();
-  for (int64_t t = (int64_t)blockIdx.x * kInsertWarps + (threadIdx.x >> 5); t < p.n_tokens;
-       t += (int64_t)gridDim.x * kInsertWarps) {
-    const T* c = reinterpret_cast<const T*>(p.c) + t * p.c_stride;
-    const T* k = reinterpret_cast<const T*>(p.k_pe) + t * p.k_stride;
-    float f[kMaxVec][kV];
-#pragma unroll
-    for (int i = 0; i < kMaxVec; ++i)
-      if (lane + 32 * i < nv) load_pack<T, kV>(c + (lane + 32 * i) * kV, f[i]);
-    float x0[2], x1[2];
-    const bool half = p.rot.layout == V4A_ROPE_HALF;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = lane + 32 * j;
-      if (i < np) {
-        x0[j] = Elem<T>::to_f(k[half ? i : 2 * i]);
-        x1[j] = Elem<T>::to_f(k[half ? i + np : 2 * i + 1]);
+  InsertRow<T> next;
+  if (warp < nt) next.load(p, t0 + warp, lane);
+  if (threadIdx.x < nt) {
+    const int t = t0 + threadIdx.x, b = find_seq(p.cu, p.n_seq, t);
+    int64_t slot = -1, pos = 0;
+    if (b >= 0) {
+      pos = __ldg(p.start + b) + (t - __ldg(p.cu + b));
+      if (pos < 0 || pos >= V4A_MAX_POS) {
+        raise_err(p.err, V4A_DEV_BAD_POS);
+      } else {
+        slot = slot_of(p.cache, b, pos);
+        slot_ok(slot, p.err);
       }
     }
-    const int b = warp_find_seq(p.cu, p.n_seq, (int)t);
-    if (b < 0) continue;
-    const int64_t pos = __ldg(p.start + b) + (t - __ldg(p.cu + b));
-    if (pos < 0 || pos >= V4A_MAX_POS) {
-      if (lane == 0) raise_err(p.err, V4A_DEV_BAD_POS);
-      continue;
-    }
-    const int64_t slot = slot_of(p.cache, b, pos);
-    if (slot < 0) {
-      if (lane == 0) slot_ok(slot, p.err);
-      continue;
-    }
+    slots[threadIdx.x] = slot;
+    at[threadIdx.x] = pos;
+  }
+  __syncthreads();
+  const bool half = p.rot.layout == V4A_ROPE_HALF;
+  for (int k = warp; k < nt; k += kInsertWarps) {
+    const InsertRow<T> in = next;
+    if (k + kInsertWarps < nt) next.load(p, t0 + k + kInsertWarps, lane);
+    const int64_t slot = slots[k], pos = at[k];
+    if (slot < 0) continue;
     T* row = reinterpret_cast<T*>(p.cache.data) + slot * (int64_t)p.cache.width;
     float r = 1.f;
     if (p.gamma) {
@@ -197,8 +220,12 @@ __global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const 
 #pragma unroll
       for (int i = 0; i < kMaxVec; ++i)
         if (lane + 32 * i < nv) {
+          const T* e = reinterpret_cast<const T*>(&in.v[i]);
 #pragma unroll
-          for (int e = 0; e < kV; ++e) ss = fmaf(f[i][e], f[i][e], ss);
+          for (int q = 0; q < kV; ++q) {
+            const float f = Elem<T>::to_f(e[q]);
+            ss = fmaf(f, f, ss);
+          }
         }
       r = 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps);
     }
@@ -206,17 +233,21 @@ __global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const 
     for (int i = 0; i < kMaxVec; ++i) {
       const int v = lane + 32 * i;
       if (v >= nv) continue;
+      const T* e = reinterpret_cast<const T*>(&in.v[i]);
+      float f[kV];
+#pragma unroll
+      for (int q = 0; q < kV; ++q) f[q] = Elem<T>::to_f(e[q]);
       if (p.gamma) {
 #pragma unroll
-        for (int e = 0; e < kV; e += 4) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + v * kV + e));
-          f[i][e] *= r * g.x;
-          f[i][e + 1] *= r * g.y;
-          f[i][e + 2] *= r * g.z;
-          f[i][e + 3] *= r * g.w;
+        for (int q = 0; q < kV; q += 4) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + v * kV + q));
+          f[q] *= r * g.x;
+          f[q + 1] *= r * g.y;
+          f[q + 2] *= r * g.z;
+          f[q + 3] *= r * g.w;
         }
       }
-      store_pack<T, kV>(row + v * kV, f[i]);
+      store_pack<T, kV>(row + v * kV, f);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -226,9 +257,9 @@ __global__ void __launch_bounds__(32 * kInsertWarps) latent_insert_kernel(const 
       rot_cs(pos, rate[j][0], rate[j][1], rate[j][2], rate[j][3], cc, sn);
       cc *= p.rot.amp;
       sn *= p.rot.amp;
-      const T y0 = Elem<T>::from_f(x0[j] * cc - x1[j] * sn), y1 = Elem<T>::from_f(x0[j] * sn + x1[j] * cc);
-      row[p.C + (half ? i : 2 * i)] = y0;
-      row[p.C + (half ? i + np : 2 * i + 1)] = y1;
+      const float a = Elem<T>::to_f(in.x0[j]), b = Elem<T>::to_f(in.x1[j]);
+      row[p.C + (half ? i : 2 * i)] = Elem<T>::from_f(a * cc - b * sn);
+      row[p.C + (half ? i + np : 2 * i + 1)] = Elem<T>::from_f(a * sn + b * cc);
     }
   }
 }
@@ -245,15 +276,10 @@ __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __g
   pdl_wait();
   if (threadIdx.x < nr) {
     const int t = r0 + threadIdx.x;
-    int lo = 0, hi = p.n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid;
-    }
-    const int a = __ldg(p.cu + lo);
+    const int b = find_seq(p.cu, p.n_seq, t);
     int64_t s = -2;
-    if (t >= a && t < __ldg(p.cu + lo + 1)) {
-      s = slot_of(p.cache, lo, __ldg(p.start + lo) + (t - a));
+    if (b >= 0) {
+      s = slot_of(p.cache, b, __ldg(p.start + b) + (t - __ldg(p.cu + b)));
       if (!slot_ok(s, p.err)) s = -1;
     }
     slots[threadIdx.x] = s;
@@ -595,11 +621,12 @@ int launch_rope(const RopeParams& p, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st) {
-  int64_t blocks = (p.n_tokens + (int64_t)kInsertWarps - 1) / kInsertWarps;
-  if (blocks > 152 * 12) blocks = 152 * 12;      // then a warp takes several tokens in turn
-  const dim3 grid((unsigned)blocks), block(32 * kInsertWarps);
-  const cudaError_t e = dtype == V4A_BF16 ? launch_pdl(latent_insert_kernel<__nv_bfloat16>, grid, block, 0, st, p)
-                                          : launch_pdl(latent_insert_kernel<float>, grid, block, 0, st, p);
+  int tokens = kInsertTokens;                    // fewer a block while that leaves SMs without one
+  while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * 152) tokens /= 2;
+  const dim3 grid((unsigned)((p.n_tokens + (int64_t)tokens - 1) / tokens)), block(32 * kInsertWarps);
+  const cudaError_t e = dtype == V4A_BF16
+                            ? launch_pdl(latent_insert_kernel<__nv_bfloat16>, grid, block, 0, st, p, tokens)
+                            : launch_pdl(latent_insert_kernel<float>, grid, block, 0, st, p, tokens);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 

@@ -125,19 +125,13 @@ __device__ __forceinline__ int cu_at(const int32_t* cu, int i, int n) {
 }
 
 // Sequence of packed row t: the last b with cu[b] <= t, or -1 when t is outside the batch.
-// The whole warp takes part; 32 probes a round.
-__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = n_seq;
-  if (t < __ldg(cu) || t >= __ldg(cu + n_seq)) return -1;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const bool in = lane * step < n && __ldg(cu + lo + lane * step) <= t;
-    const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
-    lo += last * step;
-    n = min(step, n - last * step);
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n_seq, int t) {
+  int lo = 0, hi = n_seq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
   }
-  return lo;
+  return t >= __ldg(cu + lo) && t < __ldg(cu + lo + 1) ? lo : -1;
 }
 
 // One sequence's part of the plan.
@@ -198,17 +192,6 @@ __device__ __forceinline__ void seq_prefix(int n_seq, int32_t* pre, int32_t* war
   if (threadIdx.x == 0) pre[n_seq] = carry;
   __syncthreads();
 }
-// Sum of v over the block.
-__device__ __forceinline__ int block_sum(int v, int32_t* warp_tot) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) warp_tot[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += warp_tot[i];
-  return v;
-}
 // U and the (share, tile) pairs before each sequence of an absorbed call, by the whole block.
 __device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
   int U = p.plan.max_U;
@@ -220,9 +203,21 @@ __device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, int32_t*
       c2 += s.pairs(2);
       c4 += s.pairs(4);
     }
-    c1 = block_sum(c1, warp_tot);
-    c2 = block_sum(c2, warp_tot);
-    c4 = block_sum(c4, warp_tot);
+    if (threadIdx.x < 3) warp_tot[threadIdx.x] = 0;
+    __syncthreads();
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c4 = __reduce_add_sync(0xffffffffu, c4);
+    if ((threadIdx.x & 31) == 0 && c1 > 0) {
+      atomicAdd(warp_tot, c1);
+      atomicAdd(warp_tot + 1, c2);
+      atomicAdd(warp_tot + 2, c4);
+    }
+    __syncthreads();
+    c1 = warp_tot[0];
+    c2 = warp_tot[1];
+    c4 = warp_tot[2];
+    __syncthreads();
     const int most = c1 + c1 / 8;
     if (U == 4 && (int64_t)c4 * 4 > most) U = 2;
     if (U == 2 && (int64_t)c2 * 2 > most) U = 1;
