@@ -17,6 +17,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A kernel parameter array read with an index of each thread's own: through its address, as
+// ordinary memory. (From the constant bank the lanes' different words come one at a time.)
+__device__ __forceinline__ const float* by_address(const float* v) {
+  const float* q;
+  asm volatile("mov.b64 %0, %1;" : "=l"(q) : "l"(v));
+  return q;
+}
+
 // ------------------------------------------------------------------------------- rope
 // Bound: HBM for many tokens, latency for few. A thread takes `VEC` consecutive elements of
 // each half (half layout) or 2 VEC consecutive ones (interleaved): VEC pairs. The block's
@@ -66,7 +74,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int64_t pos = __ldg(p.pos + t0 + t);
     const bool b = pos < 0 || pos >= V4A_MAX_POS;
     float c = 1.f, s = 0.f;
-    if (!b) rot_cs(pos, p.rot.phi_hi[i], p.rot.phi_lo[i], p.rot.psi_hi[i], p.rot.psi_lo[i], c, s);
+    if (!b)
+      rot_cs(pos, by_address(p.rot.phi_hi)[i], by_address(p.rot.phi_lo)[i], by_address(p.rot.psi_hi)[i],
+             by_address(p.rot.psi_lo)[i], c, s);
     if (i == 0) {
       bad[t] = b;
       if (b && h0 == 0) raise_err(p.err, V4A_DEV_BAD_POS);
@@ -147,9 +157,9 @@ int run_rope(const RopeParams& p, cudaStream_t st) {
 // written once).
 constexpr int kInsertWarps = 8, kInsertTokens = 32;
 
-template <typename T>
+template <typename T, int kMaxC>
 struct InsertRow {
-  static constexpr int kV = 16 / (int)sizeof(T), kMaxVec = 1024 / kV / 32;
+  static constexpr int kV = 16 / (int)sizeof(T), kMaxVec = kMaxC / kV / 32;
   uint4 v[kMaxVec];
   T x0[2], x1[2];
   __device__ __forceinline__ void load(const LatentInsertParams& p, int64_t t, int lane) {
@@ -171,10 +181,11 @@ struct InsertRow {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kInsertWarps)
+template <typename T, int kMaxC>
+__global__ void __launch_bounds__(32 * kInsertWarps, kMaxC <= 512 ? 3 : 2)
     latent_insert_kernel(const __grid_constant__ LatentInsertParams p, int tokens) {
-  constexpr int kV = InsertRow<T>::kV, kMaxVec = InsertRow<T>::kMaxVec;
+  using Row = InsertRow<T, kMaxC>;
+  constexpr int kV = Row::kV, kMaxVec = Row::kMaxVec;
   __shared__ int64_t slots[kInsertTokens], at[kInsertTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int np = p.rot.dim / 2, nv = p.C / kV;
@@ -183,13 +194,13 @@ __global__ void __launch_bounds__(32 * kInsertWarps)
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int i = min(lane + 32 * j, np - 1);
-    rate[j][0] = p.rot.phi_hi[i];
-    rate[j][1] = p.rot.phi_lo[i];
-    rate[j][2] = p.rot.psi_hi[i];
-    rate[j][3] = p.rot.psi_lo[i];
+    rate[j][0] = by_address(p.rot.phi_hi)[i];
+    rate[j][1] = by_address(p.rot.phi_lo)[i];
+    rate[j][2] = by_address(p.rot.psi_hi)[i];
+    rate[j][3] = by_address(p.rot.psi_lo)[i];
   }
   pdl_wait();
-  InsertRow<T> next;
+  Row next;
   if (warp < nt) next.load(p, t0 + warp, lane);
   if (threadIdx.x < nt) {
     const int t = t0 + threadIdx.x, b = find_seq(p.cu, p.n_seq, t);
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(32 * kInsertWarps)
   __syncthreads();
   const bool half = p.rot.layout == V4A_ROPE_HALF;
   for (int k = warp; k < nt; k += kInsertWarps) {
-    const InsertRow<T> in = next;
+    const Row in = next;
     if (k + kInsertWarps < nt) next.load(p, t0 + k + kInsertWarps, lane);
     const int64_t slot = slots[k], pos = at[k];
     if (slot < 0) continue;
@@ -624,10 +635,12 @@ int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st
   int tokens = kInsertTokens;                    // fewer a block while that leaves SMs without one
   while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * 152) tokens /= 2;
   const dim3 grid((unsigned)((p.n_tokens + (int64_t)tokens - 1) / tokens)), block(32 * kInsertWarps);
-  const cudaError_t e = dtype == V4A_BF16
-                            ? launch_pdl(latent_insert_kernel<__nv_bfloat16>, grid, block, 0, st, p, tokens)
-                            : launch_pdl(latent_insert_kernel<float>, grid, block, 0, st, p, tokens);
-  return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, st, p, tokens) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  };
+  if (dtype == V4A_BF16)
+    return p.C <= 512 ? go(latent_insert_kernel<__nv_bfloat16, 512>) : go(latent_insert_kernel<__nv_bfloat16, 1024>);
+  return p.C <= 512 ? go(latent_insert_kernel<float, 512>) : go(latent_insert_kernel<float, 1024>);
 }
 
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
