@@ -129,26 +129,41 @@ class LatentLayer:
             _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
         if gamma is not None:
             _need(gamma, "gamma", dev, torch.float32, (cfg.latent_dim,))
-        self._ws = {}
+        self._ws, self._desc = {}, None
+
+    def _describe(self, dev):
+        """The C descriptor of the layer's own pool, made anew when the pool's tensors are."""
+        pool = self.pool
+        if pool is None:
+            raise ValueError("this layer has no cache")
+        data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
+        d = self._desc
+        if d is None or d[0] is not data or d[1] is not bt or d[2] != rows or d[3] != data.data_ptr():
+            _need(data, "pool.data", dev, self.dtype, (None, self.width))
+            _need(bt, "pool.block_table", dev, torch.int32, (None, None))
+            c = Cache(data.data_ptr(), None, bt.data_ptr(), bt.shape[1], rows,
+                      data.shape[0] // rows, self.width, 0)
+            d = self._desc = (data, bt, rows, data.data_ptr(), data.get_device(), bt.shape[0], c)
+        if d[4] != dev:
+            raise ValueError("pool.data is on cuda:%d, the current device is cuda:%d" % (d[4], dev))
+        return d
 
     def _batch(self, cu, start):
         """(device, sequences, cache descriptor) of a call over the cache."""
-        if self.pool is None:
-            raise ValueError("this layer has no cache")
-        data, bt = self.pool.data, self.pool.block_table
-        dev = torch.cuda.current_device() if data.is_cuda else -2
-        _need(cu, "cu", dev, torch.int32, (None,))
-        n_seq = cu.shape[0] - 1
-        if n_seq < 0:
-            raise ValueError("cu: expected the sequences' first rows and the end")
-        _need(start, "start", dev, torch.int64, (n_seq,))
-        _need(data, "pool.data", dev, self.dtype, (None, self.width))
-        _need(bt, "pool.block_table", dev, torch.int32, (None, None))
-        if n_seq > bt.shape[0]:
-            raise ValueError("cu has %d sequences, the block table %d" % (n_seq, bt.shape[0]))
-        rows = self.pool.rows_per_block
-        return dev, n_seq, Cache(data.data_ptr(), None, bt.data_ptr(), bt.shape[1], rows,
-                                 data.shape[0] // rows, self.width, 0)
+        dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        d = self._describe(dev)
+        n_seq = cu.shape[0] - 1 if isinstance(cu, torch.Tensor) and cu.dim() == 1 else -1
+        if not (n_seq >= 0 and cu.dtype is torch.int32 and cu.get_device() == dev
+                and cu.is_contiguous() and start.dtype is torch.int64
+                and start.get_device() == dev and start.shape == (n_seq,)
+                and start.is_contiguous()):
+            _need(cu, "cu", dev, torch.int32, (None,))
+            if n_seq < 0:
+                raise ValueError("cu: expected the sequences' first rows and the end")
+            _need(start, "start", dev, torch.int64, (n_seq,))
+        if n_seq > d[5]:
+            raise ValueError("cu has %d sequences, the block table %d" % (n_seq, d[5]))
+        return dev, n_seq, d[6]
 
     def _workspace(self, nbytes, device, stream):
         """Kept per stream, so calls on two streams never share one; a call being captured
