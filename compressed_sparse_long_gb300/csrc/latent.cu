@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
 // The results of a unit whose tiles fell to several teams: out = sum_i w_i o_i / sum_i w_i l_i
 // with w_i = 2^(m_i - max). Block (cta, rows) does the job that the CTA posted; a warp a row.
 // Bound: latency (job, statistics, partial results: three loads in a row).
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
