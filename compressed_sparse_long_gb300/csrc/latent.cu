@@ -570,15 +570,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
         l = fmaf(w, ml.y, l);
       }
       const int cnt = min(32, last - i0 + 1);
-#pragma unroll 2
+#pragma unroll 4
       for (int k = 0; k < cnt; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (wk == 0.f) continue;                  // alike in every lane
         const float* o = p.part_o + slot(i0 + k) * p.C + d0 + lane * 4;
         float4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (d0 + lane * 4 + 128 * j < p.C) v[j] = *reinterpret_cast<const float4*>(o + 128 * j);
+          if (wk != 0.f && d0 + lane * 4 + 128 * j < p.C) v[j] = *reinterpret_cast<const float4*>(o + 128 * j);
           else v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll 4
     for (int k = 0; k < cnt; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
-      if (wk == 0.f) continue;                    // alike in every lane
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at(i0 + k) * kT + lane * 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wk != 0.f) v = *reinterpret_cast<const float4*>(p.part_o + at(i0 + k) * kT + lane * 4);
       a.x = fmaf(wk, v.x, a.x);
       a.y = fmaf(wk, v.y, a.y);
       a.z = fmaf(wk, v.z, a.z);
