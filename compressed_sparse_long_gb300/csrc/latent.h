@@ -291,7 +291,7 @@ struct LatentWalk {
   __device__ __forceinline__ bool next(const LatentAttnParams& p, LatentPiece& w) {
     if (x >= x1) return false;
     LatentSeq s = latent_seq(p, b);
-    while (x >= base + s.pairs(U)) {
+    while (b + 1 < p.n_seq && x >= base + s.pairs(U)) {
       base += s.pairs(U);
       s = latent_seq(p, ++b);
     }

@@ -35,7 +35,7 @@ constexpr int kT = 128;                                          // a CTA's quer
 constexpr int kItem = 512;                                       // queries of an item
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;                                   // log2 units
-constexpr float kLimit = 1099511627776.0f;                       // 2^40
+constexpr float kLimit = 65536.0f;                               // of a tile's sum
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
@@ -131,8 +131,8 @@ __device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int
     tc::tmem_wait_ld();
     const int here = seen - t * kT;           // keys of the tile that this query sees
     // Weights are floating-point numbers, so the reference m need not be the maximum: a tile that
-    // every query of the warp sees whole is taken against m as it is, and only if a sum shows
-    // that a weight passed 2^kLimit is the tile done again with its maxima.
+    // every query of the warp sees whole is taken against m as it is, and only if a sum
+    // passes kLimit is the tile done again with its maxima.
     uint32_t pw[64];
     float sum = 0.f;
     bool slow = __any_sync(0xffffffffu, here < kT || m == -INFINITY);
@@ -249,7 +249,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const LatentExpandedParams& p, Piece& w) {
     if (x >= x1) return false;
     Seq s(p, b);
-    while (s.blocks == 0 || x >= base + s.steps(p) * p.H) {
+    while (b + 1 < p.n_seq && (s.blocks == 0 || x >= base + s.steps(p) * p.H)) {
       base += s.steps(p) * p.H;
       s = Seq(p, ++b);
       blk = -1;
@@ -259,7 +259,7 @@ struct Walk {
       blk_base = base;
     }
     int len = s.tiles(p, blk) + p.setup;
-    while (x >= blk_base + len * p.H) {
+    while (blk > 0 && x >= blk_base + len * p.H) {
       blk_base += len * p.H;
       len = s.tiles(p, --blk) + p.setup;
     }

@@ -18,7 +18,7 @@
 // Warps 0-7: softmax and output. A thread holds one key's 32 logits (warps 0-3 rows 0-31, warps
 // 4-7 rows 32-63 of the unit). A row's weights are taken against a reference, its maximum over
 // the first tile; maxima over the keys (redux, and through shared memory) are needed again only
-// where a tile is masked or a weight would pass 2^40, and then the reference is raised where it
+// where a tile is masked or a weight would pass 2^16, and then the reference is raised where it
 // is exceeded by more than 2^8 and the accumulator and sums rescaled. Warp 8: copies, with the
 // next tile requested into L2 a tile ahead. Warp 9: products.
 #include "kernels.h"
@@ -43,7 +43,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kKBlock, "the plan's prefix sums use a key block before its first copy");
 constexpr uint32_t kSCol = 0, kOCol = 64, kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.0f, kLimit = 40.0f;                   // log2 units
+constexpr float kRaise = 8.0f, kLimit = 16.0f;                   // log2 units
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;

@@ -64,8 +64,12 @@ def _stride(t, d):
 
 
 def _on(stream):
-    """Allocations of a call belong to the stream that it runs on."""
-    return nullcontext() if stream is None or isinstance(stream, int) else torch.cuda.stream(stream)
+    """Allocations of a call belong to the stream that it runs on (a torch stream or a handle)."""
+    if stream is None:
+        return nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _raw(stream, dev):

@@ -436,7 +436,126 @@ def test_expanded_peaked_and_two_streams():
     assert all(torch.equal(o, a) for o in outs)
 
 
+def _expanded(cfg, cuq, cuk, q, k, pe, v, causal=True, **kw):
+    lay = LatentLayer(cfg, None)
+    got = lay.attention_expanded(ints(cuq, torch.int32), ints(cuk, torch.int32), q, k, pe, v,
+                                 causal=causal, **kw)
+    ref, mag = O.attention_expanded(cuq, cuk, f64(q), f64(k), f64(pe), f64(v), cfg.softmax_scale,
+                                    causal)
+    lm = max(logit_bound(f64(q)[:, h], np.concatenate([f64(k)[:, h], f64(pe)], 1), cfg.softmax_scale)
+             for h in range(q.shape[1]))
+    return got, ref, attn_tolerance(BF, ref, mag, 192, len(k), lm)
+
+
+def test_expanded_heads_outermost_and_captured():
+    """Keys and values stored [H, n, d] (the token stride below the head stride), a call captured
+    into a graph and replayed on new inputs."""
+    rng = np.random.default_rng(23)
+    cfg = v4a.latent_cfg(v4a.BF16, 3, 512, v4a.rope_cfg(64))
+    k, v = rand(rng, BF, 3, 1500, 128).transpose(0, 1), rand(rng, BF, 3, 1500, 136).transpose(0, 1)[..., 8:]
+    q, pe = rand(rng, BF, 40, 3, 192), rand(rng, BF, 1500, 64)
+    got, ref, tol = _expanded(cfg, [0, 40], [0, 1500], q, k, pe, v)
+    check(got, ref, tol)
+    lay, cu, ck = LatentLayer(cfg, None), ints([0, 40], torch.int32), ints([0, 1500], torch.int32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = lay.attention_expanded(cu, ck, q, k, pe, v)
+    q.copy_(rand(rng, BF, 40, 3, 192))
+    g.replay()
+    torch.cuda.synchronize()
+    got, ref, tol = _expanded(cfg, [0, 40], [0, 1500], q, k, pe, v)
+    check(got, ref, tol)
+    assert torch.equal(out, got)
+
+
+def test_expanded_many_sequences_and_rows_of_none():
+    rng = np.random.default_rng(24)
+    nq = rng.integers(0, 4, 1024)
+    nk = nq + rng.integers(0, 150, 1024)
+    cuq, cuk = np.concatenate([[2], 2 + np.cumsum(nq)]), np.concatenate([[1], 1 + np.cumsum(nk)])
+    cfg = v4a.latent_cfg(v4a.BF16, 2, 512, v4a.rope_cfg(64))
+    q, kv, pe = (rand(rng, BF, int(cuq[-1]), 2, 192), rand(rng, BF, int(cuk[-1]), 2, 256),
+                 rand(rng, BF, int(cuk[-1]), 64))
+    out = torch.full((len(q), 2, 128), 3.0, dtype=BF, device="cuda")
+    got, ref, tol = _expanded(cfg, cuq, cuk, q, kv[..., :128], pe, kv[..., 128:], out=out)
+    assert (got[:2] == 3).all()                    # rows before the first sequence
+    check(got[2:], ref[2:], tol[2:])
+
+
+def test_large_values_and_rising_logits():
+    """Values near the type's limits under logits that jump from tile to tile: neither sums nor
+    weights overflow on the way."""
+    rng = np.random.default_rng(25)
+    cfg = v4a.latent_cfg(v4a.BF16, 2, 512, v4a.rope_cfg(64))
+    n = 700
+    rise = torch.linspace(0, 3, n, device="cuda")[:, None, None]
+    q, pe = rand(rng, BF, 150, 2, 192).abs(), rand(rng, BF, n, 64)
+    k, v = (rand(rng, F32, n, 2, 128) * 0.3 + rise).to(BF), 1e30 * rand(rng, BF, n, 2, 128)
+    got, ref, tol = _expanded(cfg, [0, 150], [0, n], q, k, pe, v)
+    check(got, ref, tol)
+    lay, bt = layer(rng, BF, 16, [n])
+    rows = [O.slot(bt, 0, x) for x in range(n)]
+    big = 1e15 * rand(rng, BF, n, 576)             # latents are keys too: 1e15 x 1e-15 logits
+    big[:, 512:] = (rise[:, :, 0] * 4 + 0.1 * rand(rng, F32, n, 64)).to(BF)
+    lay.pool.data[rows] = big
+    qa = rand(rng, BF, 3, 16, 576)
+    qa[..., :512] *= 1e-16
+    qa[..., 512:] = qa[..., 512:].abs()
+    got, ref, tol, flags = _attn(lay, bt, [n], [3], qa)
+    assert flags == 0
+    check(got, ref, tol)
+
+
+def test_raw_stream_handles():
+    rng = np.random.default_rng(26)
+    lay, bt = layer(rng, BF, 16, [3000])
+    cu, st, q = ints([0, 1], torch.int32), ints([2999], torch.int64), rand(rng, BF, 1, 16, 576)
+    ref = lay.attention(cu, st, 2999, q)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [lay.attention(cu, st, 2999, q, stream=h) for h in (s, s.cuda_stream, 0)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, ref) for g in got)
+
+
 # -------------------------------------------------------------------------- together
+def test_a_prompt_and_a_decode_step_on_tensor_cores():
+    """bf16, as a model would run them: a prompt through the expanded form on gathered rows, then
+    a decode step through the cache; each call against its definition on what it was given."""
+    rng = np.random.default_rng(27)
+    heads, dt = 16, BF
+    lay, bt = layer(rng, dt, heads, [520, 300], gamma=True, rope_kw=dict(layout=v4a.ROPE_HALF))
+    wkv = rand(rng, F32, 512, heads * 256) / 512 ** 0.5
+    rate, done = O.rates(64), [0, 0]
+    for new in ([519, 299], [1, 1]):
+        cu, _ = batch(new, new)
+        start, n = np.array(done), int(cu[-1])
+        pos = np.concatenate([start[b] + np.arange(new[b]) for b in range(2)])
+        cud, std, posd = ints(cu, torch.int32), ints(start, torch.int64), ints(pos, torch.int64)
+        x = rand(rng, dt, n, 576)
+        total = [d + m for d, m in zip(done, new)]
+        if new[0] > 1:
+            lay.insert(cud, std, x[:, :512], x[:, 512:])
+            cuk = np.array([0, total[0], sum(total)])
+            rows = lay.gather(ints(cuk, torch.int32), torch.zeros(2, dtype=torch.int64, device="cuda"),
+                              sum(total))
+            kv = (rows[:, :512].float() @ wkv).to(dt).view(-1, heads, 256)
+            q = rand(rng, dt, n, heads, 192)
+            rope(lay.cfg.rope, q[..., 128:], posd, out=q[..., 128:])
+            got, ref, tol = _expanded(lay.cfg, cu, cuk, q, kv[..., :128], rows[:, 512:], kv[..., 128:])
+        else:
+            q = rand(rng, dt, n, heads, 576)
+            before = f64(q[..., 512:])
+            got = lay.step(cud, std, max(total) - 1, posd, x[:, :512], x[:, 512:], q)
+            turned = O.rope(before, pos, rate, "half")
+            check(q[..., 512:], turned, _rope_tol(before, turned, dt, "half", 1.0))
+            ref, mag = O.attention(f64(lay.pool.data), bt, cu, start, f64(q), lay.cfg.softmax_scale, 512)
+            tol = attn_tolerance(dt, ref, mag, 576, max(total),
+                                 logit_bound(f64(q), f64(lay.pool.data), lay.cfg.softmax_scale))
+        check(got, ref, tol)
+        done = total
+
+
 def test_absorbed_and_expanded_forms_agree_through_the_cache():
     """A prompt in two chunks and a decode step: rows inserted, queries absorbed and attended
     over the pages, against the expanded form on the gathered rows' projections. In fp32, so
