@@ -111,11 +111,11 @@ static_assert((V4A_MAX_SEQ + 1) * 4 <= kStage, "the plan's prefix sums use a sta
 constexpr uint32_t kTmemCols = 512;
 
 // Softmax of a query's key tiles t0 .. t1 - 1 (t1 <= t0: none). S of a tile appears in tensor
-// memory at scol (sfull), P is written over it (arrive_p). A query sees the first `seen` keys; g
-// counts steps. Weights are taken against the reference m, and l is their sum. False when a wait
+// memory at scol (sfull), P is written over it (arrive_p). A query sees the first `seen` keys (a
+// thread without a query, row false, must not hold up its warp); g counts steps. Weights are taken against the reference m, and l is their sum. False when a wait
 // gave up.
 template <typename ArriveP>
-__device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int t0, int t1, int seen, uint32_t scol,
+__device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int t0, int t1, int seen, bool row, uint32_t scol,
                                               uint32_t ocol, uint64_t* sfull, int& g, float& m, float& l,
                                               volatile int* abort_flag, ArriveP arrive_p) {
   const float k2 = p.scale * kLog2e;
@@ -129,16 +129,16 @@ __device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int
 #pragma unroll
     for (int i = 0; i < 4; ++i) tc::tmem_ld32(scol + 32 * i, *reinterpret_cast<float(*)[32]>(&s[32 * i]));
     tc::tmem_wait_ld();
-    const int here = seen - t * kT;           // keys of the tile that this query sees
+    const int here = row ? seen - t * kT : kT;   // keys of the tile that this query sees
     // Weights are floating-point numbers, so the reference m need not be the maximum: a tile that
     // every query of the warp sees whole is taken against m as it is, and only if a sum
     // passes kLimit is the tile done again with its maxima.
     uint32_t pw[64];
     float sum = 0.f;
-    bool slow = __any_sync(0xffffffffu, here < kT || m == -INFINITY);
+    bool slow = __any_sync(0xffffffffu, row && (here < kT || m == -INFINITY));
     if (!slow) {
       sum = weights(s, k22, -m, pw);
-      slow = __any_sync(0xffffffffu, !(sum <= kLimit));
+      slow = __any_sync(0xffffffffu, row && !(sum <= kLimit));
       if (slow) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::tmem_ld32(scol + 32 * i, *reinterpret_cast<float(*)[32]>(&s[32 * i]));
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tc::tmem_alloc_pair(tmem_at, kTmemCols);
   pdl_wait();
   Walk walk;
-  Piece w;
+  Piece w{};
   {
     int32_t* pre = reinterpret_cast<int32_t*>(kvbuf);
     seq_prefix(p.n_seq, pre, warp_tot, [&](int b) { return Seq(p, b).steps(p) * p.H; });
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = tile * 256 + rank * kT + row, qi = w.q0 + mine;
       const bool any = w.end[tile] > w.t0, store = qi < w.nq;
       float m, l;
-      if (!softmax_steps(p, w.t0, w.end[tile], w.seen(p, qi), scol, ocol, sfull + tile, g, m, l, abort_flag,
+      if (!softmax_steps(p, w.t0, w.end[tile], w.seen(p, qi), store, scol, ocol, sfull + tile, g, m, l, abort_flag,
                          [&] { if (lane == 0) tc::mbar_arrive_cluster(p_at); }))
         break;
       if (any) {

@@ -193,7 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         vis = max((int64_t)0, min(pos, p.max_pos) + 1);
         if (quad == 0 && (pos > p.max_pos || pos < 0)) raise_err(p.err, V4A_DEV_BAD_POS);
       }
-      float m = -INFINITY;                        // row c's reference, log2 units
+      // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
+      // row that sees nothing (or is none) infinity
+      float m = -INFINITY;
+      const float none = vis > 0 ? 0.f : INFINITY;
+      __syncwarp();
+      mb[lane] = none;
+      __syncwarp();
       float l[32];                                // this key lane's sums, by row
 #pragma unroll
       for (int c = 0; c < 32; ++c) l[c] = 0.f;
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mt;
           }
           __syncwarp();
-          mb[lane] = m == -INFINITY ? 0.f : m;
+          mb[lane] = m == -INFINITY ? none : m;
           const bool raise = t > w.tile0 && __any_sync(0xffffffffu, corr != 1.f);
           __syncwarp();
           if (raise) {
