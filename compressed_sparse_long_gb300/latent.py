@@ -30,23 +30,29 @@ _TYPES = {BF16: torch.bfloat16, FP32: torch.float32}
 _KINDS = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
+# The stream that work goes to now, as a handle (the public call makes a Stream object first).
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _fits(t, dev, dtype, shape):
+    """t is a contiguous tensor of exactly this type and shape on device `dev`. (At decode sizes
+    a call is a few microseconds of GPU time: the usual case is checked in one expression, and
+    _need says what is wrong otherwise.)"""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous())
+
+
+def _rows(t, dev, dtype, shape):
+    """The same for rows that may lie apart: dense in the last dimension only."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.stride(-1) == 1)
+
+
 def _need(t, name, dev, dtype, shape, contiguous=True):
     """Check that t is a tensor of this type and shape (None: any size) on device `dev`, the
-    current one. (The calls here are a few microseconds of GPU time at decode sizes, so the
-    checks are kept as cheap as they can be.)"""
-    try:
-        if t.dtype is dtype and t.get_device() == dev:
-            sh = t.shape
-            if len(sh) == len(shape):
-                for w, g in zip(shape, sh):
-                    if w is not None and w != g:
-                        break
-                else:
-                    if t.is_contiguous() or not (contiguous or (t.numel() and t.stride(-1) != 1)):
-                        return
-    except AttributeError:
-        raise ValueError("%s: expected a CUDA tensor" % name) from None
-    if not t.is_cuda:
+    current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor" % name)
     if t.get_device() != dev:
         raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
@@ -54,8 +60,10 @@ def _need(t, name, dev, dtype, shape, contiguous=True):
         raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if len(t.shape) != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
         raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
-    raise ValueError("%s must be contiguous" % name if contiguous else
-                     "%s: its last dimension must have stride 1" % name)
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+        raise ValueError("%s: its last dimension must have stride 1" % name)
 
 
 def _stride(t, d):
@@ -74,7 +82,7 @@ def _on(stream):
 
 def _raw(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -97,19 +105,22 @@ def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | N
     """Rotate x [n, H, dim] or [n, dim] (bf16 or fp32, any strides with a dense last dimension:
     a slice of wider heads, say) at positions pos [n] int64. ``out`` is a new tensor unless
     given; ``out=x`` rotates in place. ``inverse`` turns back; it is also the gradient's map."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _KINDS or x.dim() not in (2, 3):
+    kind = _KINDS.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    shape = x.shape if kind is not None else ()
+    if len(shape) not in (2, 3):
         raise ValueError("x: expected a bfloat16 or float32 tensor [n, H, dim] or [n, dim]")
     dev = torch.cuda.current_device() if x.is_cuda else -2
-    shape = x.shape
-    _need(x, "x", dev, x.dtype, (None,) * (len(shape) - 1) + (cfg.dim,), contiguous=False)
-    _need(pos, "pos", dev, torch.int64, (shape[0],))
+    if not (shape[-1] == cfg.dim and _rows(x, dev, x.dtype, shape)
+            and _fits(pos, dev, torch.int64, shape[:1])):
+        _need(x, "x", dev, x.dtype, (None,) * (len(shape) - 1) + (cfg.dim,), contiguous=False)
+        _need(pos, "pos", dev, torch.int64, (shape[0],))
     if out is None:
-        out = _new(shape, x.dtype, x.device, stream)
-    else:
+        out = x.new_empty(shape) if stream is None else _new(shape, x.dtype, x.device, stream)
+    elif not _rows(out, dev, x.dtype, shape):
         _need(out, "out", dev, x.dtype, shape, contiguous=False)
     heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
     _check("v4a_rope", library().v4a_rope(
-        byref(cfg), _KINDS[x.dtype], shape[0], heads, pos.data_ptr(), x.data_ptr(), _stride(x, 0),
+        byref(cfg), kind, shape[0], heads, pos.data_ptr(), x.data_ptr(), _stride(x, 0),
         xh, out.data_ptr(), _stride(out, 0), oh, inverse, _word(dev_err, dev), _raw(stream, dev)))
     return out
 
@@ -156,11 +167,9 @@ class LatentLayer:
         """(device, sequences, cache descriptor) of a call over the cache."""
         dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
         d = self._describe(dev)
-        n_seq = cu.shape[0] - 1 if isinstance(cu, torch.Tensor) and cu.dim() == 1 else -1
-        if not (n_seq >= 0 and cu.dtype is torch.int32 and cu.get_device() == dev
-                and cu.is_contiguous() and start.dtype is torch.int64
-                and start.get_device() == dev and start.shape == (n_seq,)
-                and start.is_contiguous()):
+        n_seq = cu.numel() - 1 if isinstance(cu, torch.Tensor) else -1
+        if n_seq < 0 or not (_fits(cu, dev, torch.int32, (n_seq + 1,))
+                             and _fits(start, dev, torch.int64, (n_seq,))):
             _need(cu, "cu", dev, torch.int32, (None,))
             if n_seq < 0:
                 raise ValueError("cu: expected the sequences' first rows and the end")
@@ -177,7 +186,7 @@ class LatentLayer:
         with _on(stream):
             if torch.cuda.is_current_stream_capturing():
                 return torch.empty(nbytes, dtype=torch.uint8, device=device)
-            key = _raw(stream, device)
+            key = _raw(stream, device.index)
             ws = self._ws.get(key)
             if ws is None or ws.shape[0] < nbytes:
                 ws = self._ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -187,10 +196,13 @@ class LatentLayer:
         """Write the cache rows of new tokens: c [n, latent_dim], k_pe [n, rope dim] (rows may
         be strided: two slices of one projection's output)."""
         dev, n_seq, cache = self._batch(cu, start)
-        _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
-        _need(k_pe, "k_pe", dev, self.dtype, (c.shape[0], self.cfg.rope.dim), contiguous=False)
+        n = c.shape[0] if isinstance(c, torch.Tensor) and c.dim() else 0
+        if not (_rows(c, dev, self.dtype, (n, self.cfg.latent_dim))
+                and _rows(k_pe, dev, self.dtype, (n, self.cfg.rope.dim))):
+            _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
+            _need(k_pe, "k_pe", dev, self.dtype, (n, self.cfg.rope.dim), contiguous=False)
         _check("v4a_latent_insert", library().v4a_latent_insert(
-            byref(self.cfg), n_seq, c.shape[0], cu.data_ptr(), start.data_ptr(), c.data_ptr(),
+            byref(self.cfg), n_seq, n, cu.data_ptr(), start.data_ptr(), c.data_ptr(),
             _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),
             None if self.gamma is None else self.gamma.data_ptr(), byref(cache),
             _word(dev_err, dev), _raw(stream, dev)))
@@ -202,7 +214,7 @@ class LatentLayer:
         dev, n_seq, cache = self._batch(cu, start)
         if out is None:
             out = _new((n_rows, self.width), self.dtype, cu.device, stream)
-        else:
+        elif not _fits(out, dev, self.dtype, (n_rows, self.width)):
             _need(out, "out", dev, self.dtype, (n_rows, self.width))
         _check("v4a_latent_gather", library().v4a_latent_gather(
             byref(self.cfg), n_seq, n_rows, cu.data_ptr(), start.data_ptr(), byref(cache),
@@ -214,11 +226,12 @@ class LatentLayer:
         a sequence (decode) or chunks; returns [n, H, latent_dim]."""
         dev, n_seq, cache = self._batch(cu, start)
         h = self.cfg.n_heads
-        _need(q, "q", dev, self.dtype, (None, h, self.width))
-        n = q.shape[0]
+        n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+        if not _fits(q, dev, self.dtype, (n, h, self.width)):
+            _need(q, "q", dev, self.dtype, (None, h, self.width))
         if out is None:
             out = _new((n, h, self.cfg.latent_dim), self.dtype, q.device, stream)
-        else:
+        elif not _fits(out, dev, self.dtype, (n, h, self.cfg.latent_dim)):
             _need(out, "out", dev, self.dtype, (n, h, self.cfg.latent_dim))
         lib, cfg = library(), byref(self.cfg)
         nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
@@ -235,27 +248,34 @@ class LatentLayer:
         (shared by the heads), v [n_k, H, v_dim]; k, k_pe and v may be strided slices of wider
         rows. Returns [n_q, H, v_dim]."""
         c = self.cfg
-        dev = torch.cuda.current_device() if q.is_cuda else -2
-        _need(cu_q, "cu_q", dev, torch.int32, (None,))
-        n_seq = cu_q.shape[0] - 1
-        if n_seq < 0:
-            raise ValueError("cu_q: expected the sequences' first rows and the end")
-        _need(cu_k, "cu_k", dev, torch.int32, (n_seq + 1,))
-        _need(q, "q", dev, self.dtype, (None, c.n_heads, c.nope_dim + c.rope.dim))
-        _need(k, "k", dev, self.dtype, (None, c.n_heads, c.nope_dim), contiguous=False)
-        n_k = k.shape[0]
-        _need(k_pe, "k_pe", dev, self.dtype, (n_k, c.rope.dim), contiguous=False)
-        _need(v, "v", dev, self.dtype, (n_k, c.n_heads, c.v_dim), contiguous=False)
-        shape = (q.shape[0], c.n_heads, c.v_dim)
+        dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        n_seq = cu_q.numel() - 1 if isinstance(cu_q, torch.Tensor) else -1
+        n_q, n_k = (t.shape[0] if isinstance(t, torch.Tensor) and t.dim() else 0 for t in (q, k))
+        if n_seq < 0 or not (
+                _fits(cu_q, dev, torch.int32, (n_seq + 1,))
+                and _fits(cu_k, dev, torch.int32, (n_seq + 1,))
+                and _fits(q, dev, self.dtype, (n_q, c.n_heads, c.nope_dim + c.rope.dim))
+                and _rows(k, dev, self.dtype, (n_k, c.n_heads, c.nope_dim))
+                and _rows(k_pe, dev, self.dtype, (n_k, c.rope.dim))
+                and _rows(v, dev, self.dtype, (n_k, c.n_heads, c.v_dim))):
+            _need(cu_q, "cu_q", dev, torch.int32, (None,))
+            if n_seq < 0:
+                raise ValueError("cu_q: expected the sequences' first rows and the end")
+            _need(cu_k, "cu_k", dev, torch.int32, (n_seq + 1,))
+            _need(q, "q", dev, self.dtype, (None, c.n_heads, c.nope_dim + c.rope.dim))
+            _need(k, "k", dev, self.dtype, (None, c.n_heads, c.nope_dim), contiguous=False)
+            _need(k_pe, "k_pe", dev, self.dtype, (n_k, c.rope.dim), contiguous=False)
+            _need(v, "v", dev, self.dtype, (n_k, c.n_heads, c.v_dim), contiguous=False)
+        shape = (n_q, c.n_heads, c.v_dim)
         if out is None:
             out = _new(shape, self.dtype, q.device, stream)
-        else:
+        elif not _fits(out, dev, self.dtype, shape):
             _need(out, "out", dev, self.dtype, shape)
         lib, cfg = library(), byref(c)
-        nb = lib.v4a_latent_attn_expanded_workspace_size(cfg, n_seq, q.shape[0], n_k)
+        nb = lib.v4a_latent_attn_expanded_workspace_size(cfg, n_seq, n_q, n_k)
         ws = self._workspace(nb, q.device, stream)
         _check("v4a_latent_attn_expanded", lib.v4a_latent_attn_expanded(
-            cfg, n_seq, q.shape[0], cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
+            cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), _stride(k, 0), _stride(k, 1), k_pe.data_ptr(), _stride(k_pe, 0),
             v.data_ptr(), _stride(v, 0), _stride(v, 1), causal, out.data_ptr(),
             None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev), _raw(stream, dev)))
