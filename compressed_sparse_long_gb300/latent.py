@@ -115,7 +115,7 @@ def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | N
         _need(x, "x", dev, x.dtype, (None,) * (len(shape) - 1) + (cfg.dim,), contiguous=False)
         _need(pos, "pos", dev, torch.int64, (shape[0],))
     if out is None:
-        out = x.new_empty(shape) if stream is None else _new(shape, x.dtype, x.device, stream)
+        out = _new(shape, x.dtype, x.device, stream)
     elif not _rows(out, dev, x.dtype, shape):
         _need(out, "out", dev, x.dtype, shape, contiguous=False)
     heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
