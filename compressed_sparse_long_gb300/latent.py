@@ -71,6 +71,14 @@ def _stride(t, d):
     return t.stride(d) if t.shape[d] > 1 else -(-t.shape[-1] // 8) * 8
 
 
+def _strides(t):
+    """The same along the first two of three dimensions."""
+    n, h, _ = t.shape
+    if n > 1 and h > 1:
+        return t.stride()[:2]
+    return _stride(t, 0), _stride(t, 1)
+
+
 def _on(stream):
     """Allocations of a call belong to the stream that it runs on (a torch stream or a handle)."""
     if stream is None:
@@ -183,14 +191,16 @@ class LatentLayer:
         into a graph gets memory of that graph's own."""
         if nbytes == 0:
             return None
-        with _on(stream):
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(nbytes, dtype=torch.uint8, device=device)
-            key = _raw(stream, device.index)
-            ws = self._ws.get(key)
-            if ws is None or ws.shape[0] < nbytes:
-                ws = self._ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            return ws
+        if stream is not None:
+            with _on(stream):
+                return self._workspace(nbytes, device, None)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        key = _current_raw(device.index)
+        ws = self._ws.get(key)
+        if ws is None or ws.shape[0] < nbytes:
+            ws = self._ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws
 
     def insert(self, cu, start, c, k_pe, dev_err=None, stream=None):
         """Write the cache rows of new tokens: c [n, latent_dim], k_pe [n, rope dim] (rows may
@@ -250,7 +260,8 @@ class LatentLayer:
         c = self.cfg
         dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
         n_seq = cu_q.numel() - 1 if isinstance(cu_q, torch.Tensor) else -1
-        n_q, n_k = (t.shape[0] if isinstance(t, torch.Tensor) and t.dim() else 0 for t in (q, k))
+        n_q = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+        n_k = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
         if n_seq < 0 or not (
                 _fits(cu_q, dev, torch.int32, (n_seq + 1,))
                 and _fits(cu_k, dev, torch.int32, (n_seq + 1,))
@@ -276,8 +287,8 @@ class LatentLayer:
         ws = self._workspace(nb, q.device, stream)
         _check("v4a_latent_attn_expanded", lib.v4a_latent_attn_expanded(
             cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
-            k.data_ptr(), _stride(k, 0), _stride(k, 1), k_pe.data_ptr(), _stride(k_pe, 0),
-            v.data_ptr(), _stride(v, 0), _stride(v, 1), causal, out.data_ptr(),
+            k.data_ptr(), *_strides(k), k_pe.data_ptr(), _stride(k_pe, 0), v.data_ptr(),
+            *_strides(v), causal, out.data_ptr(),
             None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev), _raw(stream, dev)))
         return out
 
