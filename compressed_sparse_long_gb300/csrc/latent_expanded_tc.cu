@@ -11,15 +11,17 @@
 // 64 of the values' 128 dims), which the products read from both CTAs: per CTA half the copies
 // and 6 KB of shared-memory operands a product instead of 8. That is what one CTA's rate hangs
 // on: alone, S's 128 x 128 x 16 products take 96 cycles instead of the pipe's 64 (the same
-// kernel for single CTAs, 256 queries an item, ran an 8192-token prompt of 64 heads in 1102 us
-// against 927). Three stages of 40 KB keep copies two steps ahead.
+// kernel for single CTAs, 256 queries an item, ran an 8192-token prompt of 64 heads in 1102 us).
+// Three stages of 40 KB keep copies two steps ahead.
 //
-// Bound: the tensor pipe (40 MMAs a step of 512 queries x 128 keys), and the power it draws.
+// Bound: the tensor pipe (40 products a step of 512 queries x 128 keys, 2560 cycles; a step takes
+// 3050, a tile's chain of S, softmax and P V being a little longer) and, in long runs, the power
+// it draws: that prompt takes 832 us (1.65 PFLOP/s) in a short run and 910-920 in a long one.
 //
 // All (item, key tile) steps form one line, a sequence's blocks from the last (the longest, when
 // causal) to the first, heads within a block; each pair takes an equal part of it. An item whose
 // tiles fall to several pairs is left as partial results that a second kernel merges: without
-// that, a long sequence's few items would decide the time (ragged chunks: 391 us).
+// that, a long sequence's few items would decide the time (ragged chunks 391 us, now 184).
 //
 // Roles in each CTA: warps 0-7 softmax and output (tile 0 / 1), warp 8 copies, warp 11 watches
 // the copies land and reports to the CTA of rank 0, whose warp 9 issues the pair's products.
