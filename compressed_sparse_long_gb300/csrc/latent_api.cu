@@ -143,8 +143,8 @@ size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, 
 
 // Steps that starting an item counts for when the line is cut into equal parts. Its copies, first
 // logits and output take about two; counting four evens out the pairs that get many short items:
-// 8192-token prompt, 64 heads: 1190 us with 0, 973 with 2, 910 with 4, 916 with 6; ragged chunks
-// 220, 224, 228 and 239 us.
+// 8192-token prompt, 64 heads (long runs): 1190 us with 0, 973 with 2, 910 with 4, 916 with 6;
+// ragged chunks 220, 224, 228 and 239 us, before rows without a query were kept off the masked path.
 constexpr int kExpandedSetup = 4;
 
 // The plan of an expanded call (p->tc, pairs, split) and its workspace. False when the steps
