@@ -89,8 +89,6 @@ def _on(stream):
 
 
 def _raw(stream, dev):
-    if stream is None:
-        return _current_raw(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -102,8 +100,6 @@ def _new(shape, dtype, device, stream):
 
 
 def _word(dev_err, dev):
-    if dev_err is None:
-        return None
     _need(dev_err, "dev_err", dev, torch.int32, (1,))
     return dev_err.data_ptr()
 
@@ -129,7 +125,8 @@ def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | N
     heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
     _check("v4a_rope", library().v4a_rope(
         byref(cfg), kind, shape[0], heads, pos.data_ptr(), x.data_ptr(), _stride(x, 0),
-        xh, out.data_ptr(), _stride(out, 0), oh, inverse, _word(dev_err, dev), _raw(stream, dev)))
+        xh, out.data_ptr(), _stride(out, 0), oh, inverse, None if dev_err is None else _word(dev_err, dev),
+            _current_raw(dev) if stream is None else _raw(stream, dev)))
     return out
 
 
@@ -161,7 +158,8 @@ class LatentLayer:
             raise ValueError("this layer has no cache")
         data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
         d = self._desc
-        if d is None or d[0] is not data or d[1] is not bt or d[2] != rows or d[3] != data.data_ptr():
+        if (d is None or d[0] is not data or d[1] is not bt or d[2] != rows
+                or d[3] != data.data_ptr() or d[6].block_table != bt.data_ptr()):
             _need(data, "pool.data", dev, self.dtype, (None, self.width))
             _need(bt, "pool.block_table", dev, torch.int32, (None, None))
             c = Cache(data.data_ptr(), None, bt.data_ptr(), bt.shape[1], rows,
@@ -215,7 +213,8 @@ class LatentLayer:
             byref(self.cfg), n_seq, n, cu.data_ptr(), start.data_ptr(), c.data_ptr(),
             _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),
             None if self.gamma is None else self.gamma.data_ptr(), byref(cache),
-            _word(dev_err, dev), _raw(stream, dev)))
+            None if dev_err is None else _word(dev_err, dev),
+            _current_raw(dev) if stream is None else _raw(stream, dev)))
 
     def gather(self, cu, start, n_rows, out=None, dev_err=None, stream=None):
         """Copy cached rows out: sequence b's rows cu[b] .. cu[b+1]-1 of the result are its
@@ -228,7 +227,8 @@ class LatentLayer:
             _need(out, "out", dev, self.dtype, (n_rows, self.width))
         _check("v4a_latent_gather", library().v4a_latent_gather(
             byref(self.cfg), n_seq, n_rows, cu.data_ptr(), start.data_ptr(), byref(cache),
-            out.data_ptr(), _word(dev_err, dev), _raw(stream, dev)))
+            out.data_ptr(), None if dev_err is None else _word(dev_err, dev),
+            _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
     def attention(self, cu, start, max_pos, q, out=None, dev_err=None, stream=None):
@@ -248,8 +248,8 @@ class LatentLayer:
         ws = self._workspace(nb, q.device, stream)
         _check("v4a_latent_attn", lib.v4a_latent_attn(
             cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
-            out.data_ptr(), None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev),
-            _raw(stream, dev)))
+            out.data_ptr(), None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
+            _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
     def attention_expanded(self, cu_q, cu_k, q, k, k_pe, v, causal=True, out=None, dev_err=None,
@@ -289,7 +289,8 @@ class LatentLayer:
             cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), *_strides(k), k_pe.data_ptr(), _stride(k_pe, 0), v.data_ptr(),
             *_strides(v), causal, out.data_ptr(),
-            None if ws is None else ws.data_ptr(), nb, _word(dev_err, dev), _raw(stream, dev)))
+            None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
+            _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
     def step(self, cu, start, max_pos, pos, c, k_pe, q, out=None, dev_err=None, stream=None):

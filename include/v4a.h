@@ -467,7 +467,7 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
  * All pointers on 16-byte boundaries, strides positive multiples of 16 bytes.
  * Key and value rows at or behind cu_k[n_seq], and other sequences' rows, are not used,
  * whatever they hold. A value that is not finite may reach queries of its sequence that do
- * not see it.
+ * not see it. dev_err: V4A_DEV_TIMEOUT only (nothing here is looked up).
  * bf16 with nope = 128, rope.dim = 64 and v_dim = 128 runs on the tensor cores; other shapes
  * on CUDA cores.
  */

@@ -236,6 +236,7 @@ SHAPES = [
     (BF, 128, 512, 64, [300, 290], [290, 1]),
     (BF, 40, 512, 64, [256, 255], [2, 255]),
     (F32, 16, 64, 16, [1300], [1300]),
+    (BF, 300, 512, 64, [200, 3], [1, 2]),
 ]
 
 
@@ -518,6 +519,47 @@ def test_raw_stream_handles():
     assert all(torch.equal(g, ref) for g in got)
 
 
+def test_python_refusals():
+    """Types, shapes, strides and hosts that the layer does not take: refused before any launch."""
+    rng = np.random.default_rng(28)
+    lay, bt = layer(rng, BF, 16, [300, 20])
+    cu, st = ints([0, 1, 2], torch.int32), ints([299, 19], torch.int64)
+    q = rand(rng, BF, 2, 16, 576)
+    good = dict(cu=cu, start=st, max_pos=299, q=q)
+    assert lay.attention(**good).shape == (2, 16, 512)
+    for bad in (dict(q=q.float()), dict(q=q[..., :512]), dict(q=q[:, :8]), dict(q=q.cpu()),
+                dict(q=rand(rng, BF, 2, 16, 600)[..., :576]), dict(cu=cu.long()), dict(cu=cu[:0]),
+                dict(cu=ints([0, 1, 2, 2], torch.int32)), dict(start=st.int()), dict(start=st[:1]),
+                dict(start=[299, 19]), dict(cu=cu[None]), dict(out=torch.empty_like(q)),
+                dict(dev_err=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            lay.attention(**dict(good, **bad))
+    x = rand(rng, BF, 2, 576)
+    for c, pe in ((x[:, :512].float(), x[:, 512:]), (x[:, :500], x[:, 512:]), (x[:1, :512], x[:, 512:]),
+                  (rand(rng, BF, 512, 2).t(), x[:, 512:]), (x[:, :512], None)):
+        with pytest.raises(ValueError):
+            lay.insert(cu, st, c, pe)
+    with pytest.raises(v4a.V4AError):              # rows that do not start on 16 bytes
+        lay.insert(cu, st, rand(rng, BF, 2, 579)[:, 3:515], x[:, 512:])
+    with pytest.raises(ValueError):
+        lay.gather(cu, st, 2, out=torch.empty(2, 512, dtype=BF, device="cuda"))
+    kv, pe = rand(rng, BF, 4, 16, 256), rand(rng, BF, 4, 64)
+    qe, ce = rand(rng, BF, 2, 16, 192), ints([0, 2], torch.int32)
+    ok = dict(cu_q=ce, cu_k=ints([0, 4], torch.int32), q=qe, k=kv[..., :128], k_pe=pe, v=kv[..., 128:])
+    assert lay.attention_expanded(**ok).shape == (2, 16, 128)
+    for bad in (dict(k_pe=pe[:3]), dict(v=kv[:3, :, 128:]), dict(k=kv[..., :120]), dict(q=qe.float()),
+                dict(cu_k=ce[:1]), dict(v=None), dict(q=qe[..., ::2])):
+        with pytest.raises(ValueError):
+            lay.attention_expanded(**dict(ok, **bad))
+    with pytest.raises(v4a.V4AError):              # one key head for all: its stride is 0
+        lay.attention_expanded(**dict(ok, k=kv[:, :1, :128].expand(4, 16, 128)))
+    with pytest.raises(ValueError):
+        rope(lay.cfg.rope, q, ints([0, 1], torch.int64))
+    with pytest.raises(v4a.V4AError):              # rows of the result on top of each other
+        rope(lay.cfg.rope, rand(rng, BF, 2, 3, 64), ints([0, 1], torch.int64),
+             out=torch.empty(2, 1, 64, dtype=BF, device="cuda").expand(2, 3, 64))
+
+
 # -------------------------------------------------------------------------- together
 def test_a_prompt_and_a_decode_step_on_tensor_cores():
     """bf16, as a model would run them: a prompt through the expanded form on gathered rows, then
@@ -589,6 +631,27 @@ def test_absorbed_and_expanded_forms_agree_through_the_cache():
         # fp32 sums of at most 160 products and 333 weights on either side, values of order 1
         assert (absorbed - e.double()).abs().max() <= 1e-4
         done = total
+
+
+def test_expanded_offsets_pass_31_bits():
+    """Keys and values of more than 2^31 elements: the last heads of the last tokens."""
+    g = torch.Generator(device="cuda").manual_seed(29)
+    n, heads, nq = 140000, 64, 3
+    kv = torch.randn(n, heads, 256, generator=g, device="cuda", dtype=BF)
+    assert kv.numel() > 1 << 31
+    pe = torch.randn(n, 64, generator=g, device="cuda", dtype=BF)
+    q = torch.randn(nq, heads, 192, generator=g, device="cuda", dtype=BF)
+    lay = LatentLayer(v4a.latent_cfg(v4a.BF16, heads, 512, v4a.rope_cfg(64)), None)
+    got = lay.attention_expanded(ints([0, nq], torch.int32), ints([0, n], torch.int32), q,
+                                 kv[..., :128], pe, kv[..., 128:])
+    for h in (0, 63):
+        k = np.concatenate([f64(kv[:, h, :128]), f64(pe)], 1)
+        v = f64(kv[:, h, 128:])
+        for i in range(nq):
+            m = n - nq + i + 1
+            ref, mag = O.attend(f64(q)[i, h][None], k[:m], v[:m], lay.cfg.softmax_scale)
+            check(got[i, h][None], ref,
+                  attn_tolerance(BF, ref, mag, 192, n, logit_bound(f64(q)[i, h][None], k, lay.cfg.softmax_scale)))
 
 
 def test_long_cache_offsets_pass_31_bits():
