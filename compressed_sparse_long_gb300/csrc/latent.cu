@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
   int seq = 0, head = 0, item = blockIdx.x;
   bool posted = false;
   if constexpr (kPaged) {
-    walk.begin(p, pre, latent_prefix(p, pre, warp_tot), blockIdx.x);
+    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
   }
   for (;;) {
     // ---- the next unit: its query rows and its keys
@@ -663,7 +663,7 @@ cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
   cudaError_t e;
   if (p.plan.tc) {
-    e = p.plan.tc == 2 ? launch_latent_attn_pair(p, st) : launch_latent_attn_tc(p, st);
+    e = launch_latent_attn_tc(p, st);
   } else {
     e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, p.plan.ctas, st)
                           : run_gen<float, true>(p, p.C + p.R, p.C, p.plan.ctas, st);

@@ -65,9 +65,9 @@ struct LatentGatherParams {
 struct LatentPlan {
   int32_t NR, TK;
   int32_t max_U;
-  int32_t ctas;                       // a multiple of max_U (of pairs in the kernel for pairs)
+  int32_t ctas;                       // a multiple of max_U
   int32_t split;
-  int32_t tc;                         // 0: CUDA cores, 1: tensor cores, 2: the same by pairs of CTAs
+  int32_t tc;                         // tensor-core kernel
 };
 
 struct LatentAttnParams {
@@ -113,7 +113,6 @@ int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st);
-cudaError_t launch_latent_attn_pair(const LatentAttnParams& p, cudaStream_t st);
 cudaError_t launch_latent_expanded_tc(const LatentExpandedParams& p, cudaStream_t st);
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st);
 
@@ -262,9 +261,9 @@ struct LatentPiece {
 struct LatentWalk {
   int x, x1, cta, team, member, U, total, n;
   int b, base;      // current sequence and the pairs before it
-  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int U_, int cta_) {
+  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int U_) {
     U = U_;
-    cta = cta_;
+    cta = blockIdx.x;
     total = pre[p.n_seq];
     team = cta / U;
     member = cta % U;

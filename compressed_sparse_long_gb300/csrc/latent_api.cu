@@ -113,20 +113,17 @@ bool on_tensor_cores(const v4a_latent_cfg* c) {
 // The plan of an absorbed call. False when the tiles cannot be counted in 31 bits.
 bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t max_pos, LatentPlan* pl) {
   const bool tc = on_tensor_cores(c);
-  const int64_t rows = (int64_t)n_tokens * c->n_heads;
-  if (rows > INT32_MAX / 2) return false;
-  // pairs of CTAs take 128 rows, single ones 64
-  const bool pair = tc && rows / n_seq > 64;
-  pl->tc = pair ? 2 : tc ? 1 : 0;
-  pl->NR = pair ? 128 : tc ? 64 : 16;
+  pl->tc = tc;
+  pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
+  const int64_t rows = (int64_t)n_tokens * c->n_heads;
   const int64_t units = (rows + pl->NR - 1) / pl->NR + n_seq;   // at most, over the sequences
   const int64_t tiles = max_pos / pl->TK + 1;
+  if (rows > INT32_MAX / 2) return false;
   // sharing key tiles pays where an average sequence has several units (the device decides)
   pl->max_U = 1;
   while (tc && pl->max_U < 4 && rows / n_seq >= 2 * pl->max_U * pl->NR) pl->max_U *= 2;
-  const int sms = sm_count();
-  const int64_t most = pair ? sms / 2 / 4 * 4 : tc ? sms / 4 * 4 : 2 * sms;   // CTAs (pairs) at once
+  const int64_t most = tc ? sm_count() / 4 * 4 : 2 * sm_count();  // CTAs at once
   // Units are split along the keys where that fills the GPU (fewer than four a CTA) or evens
   // out sequences of different lengths (few new tokens each). Prompts, whose units' key counts
   // rise from one to the next, go as whole units, neighbours to neighbouring CTAs.

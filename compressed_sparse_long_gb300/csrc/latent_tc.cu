@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   LatentPiece w;
   {
     int32_t* pre = reinterpret_cast<int32_t*>(kbuf);
-    walk.begin(p, pre, latent_prefix(p, pre, warp_tot), blockIdx.x);
+    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
   }
   tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
   tc::fence_before_sync();
