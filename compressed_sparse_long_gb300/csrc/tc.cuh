@@ -219,7 +219,7 @@ __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 }
 constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // SBO 1024, 128B swizzle
 
-// mma_bf16 and mma_bf16_ta with descriptors of high word kSdescHi.
+// mma_bf16 with descriptors of high word kSdescHi.
 template <uint32_t kIdesc>
 __device__ __forceinline__ void mma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
   asm volatile(
@@ -228,15 +228,6 @@ __device__ __forceinline__ void mma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint
       "r"(a_lo), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
       : "memory");
 }
-template <uint32_t kIdesc>
-__device__ __forceinline__ void mma_bf16_ta_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; .reg .b64 b; mov.b64 b, {%2, %3}; setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "n"(kSdescHi), "n"(kIdesc), "r"(accumulate)
-      : "memory");
-}
-
 // ------------------------------------------------------------------------ CTA pairs
 // Two CTAs of a cluster work on one product (cta_group::2): the CTA of even rank issues it, each
 // CTA holds its half of the rows of A and D, and half of the columns of B.
