@@ -540,7 +540,8 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
 
 // ------------------------------------------------------------------------------ merge
 // The results of a unit whose tiles fell to several teams: out = sum_i w_i o_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max). Block (cta, rows) does the job that the CTA posted; a warp a row.
+// with w_i = 2^(m_i - max). Block (cta, rows, dims) does the job that the CTA posted; a warp
+// 256 dims of a row.
 // Bound: latency (job, statistics, partial results: three loads in a row).
 constexpr int kMergeWarps = 8;
 
@@ -551,61 +552,71 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
   const int4 job = *reinterpret_cast<const int4*>(p.part_job + 4 * blockIdx.x);
   const int r = blockIdx.y * kMergeWarps + warp, NR = p.plan.NR;
   if (r >= job.x) return;
-  const int U = job.w, g = blockIdx.x / U, member = blockIdx.x % U, last = job.z;
+  const int U = job.w, g = blockIdx.x / U, member = blockIdx.x % U, first = g - 1, last = job.z;
+  const int d0 = blockIdx.z * 256 + lane * 4;
   // team g - 1's piece begins the unit (slot 1), the others begin inside it (slot 0)
-  auto slot = [&](int i) { return (int64_t)(((i * U + member) << 1) + (i == g - 1 ? 1 : 0)) * NR + r; };
-  float m = -INFINITY;
-  for (int i = g - 1 + lane; i <= last; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2]);
+  auto slot = [&](int i) { return (int64_t)(((i * U + member) << 1) + (i == first ? 1 : 0)) * NR + r; };
+  auto load = [&](int i, float4 (&v)[2]) {
+    const float* o = p.part_o + slot(i) * p.C + d0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      v[j] = d0 + 128 * j < p.C ? *reinterpret_cast<const float4*>(o + 128 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  // the statistics, a lane a piece, and the first pieces' results are requested together (an
+  // empty range's result was not written: it is left out below)
+  float4 v[4][2];
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (first + lane <= last) ml = *reinterpret_cast<const float2*>(p.part_ml + slot(first + lane) * 2);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (first + k <= last) load(first + k, v[k]);
+  float m = ml.x;
+  for (int i = first + 32 + lane; i <= last; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2]);
   m = warp_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
-  T* out = reinterpret_cast<T*>(p.out) + (int64_t)(job.y + r) * p.C;
-  for (int d0 = 0; d0 < p.C; d0 += 512) {
-    float l = 0.f;
-    float4 a[4] = {};
-    for (int i0 = g - 1; i0 <= last; i0 += 32) {
-      // a lane a piece: its weight, 0 for a range without a key (whose o was not written)
-      const int i = i0 + lane;
-      float w = 0.f;
-      if (i <= last) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
-        if (ml.x != -INFINITY || ml.y != 0.f) w = exp2f(ml.x - ref);
-        l = fmaf(w, ml.y, l);
+  float l = 0.f;
+  float4 a[2] = {};
+  for (int i0 = first; i0 <= last; i0 += 32) {
+    if (i0 > first) ml = i0 + lane <= last ? *reinterpret_cast<const float2*>(p.part_ml + slot(i0 + lane) * 2)
+                                           : make_float2(-INFINITY, 0.f);
+    const float w = ml.x != -INFINITY || ml.y != 0.f ? exp2f(ml.x - ref) : 0.f;
+    l = fmaf(w, ml.y, l);
+    const int cnt = min(32, last - i0 + 1);
+    for (int k0 = 0; k0 < cnt; k0 += 4) {
+      if (k0 > 0 || i0 > first) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k0 + k < cnt) load(i0 + k0 + k, v[k]);
       }
-      const int cnt = min(32, last - i0 + 1);
-#pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* o = p.part_o + slot(i0 + k) * p.C + d0 + lane * 4;
-        float4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (wk != 0.f && d0 + lane * 4 + 128 * j < p.C) v[j] = *reinterpret_cast<const float4*>(o + 128 * j);
-          else v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < 4; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k >= cnt || wk == 0.f) continue;   // alike in every lane
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[j].x = fmaf(wk, v[j].x, a[j].x);
-          a[j].y = fmaf(wk, v[j].y, a[j].y);
-          a[j].z = fmaf(wk, v[j].z, a[j].z);
-          a[j].w = fmaf(wk, v[j].w, a[j].w);
+        for (int j = 0; j < 2; ++j) {
+          a[j].x = fmaf(wk, v[k][j].x, a[j].x);
+          a[j].y = fmaf(wk, v[k][j].y, a[j].y);
+          a[j].z = fmaf(wk, v[k][j].z, a[j].z);
+          a[j].w = fmaf(wk, v[k][j].w, a[j].w);
         }
       }
     }
-    l = warp_sum(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  }
+  l = warp_sum(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = reinterpret_cast<T*>(p.out) + (int64_t)(job.y + r) * p.C + d0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = d0 + lane * 4 + 128 * j;
-      if (d >= p.C) continue;
-      float f[4] = {a[j].x * inv, a[j].y * inv, a[j].z * inv, a[j].w * inv};
-      if constexpr (sizeof(T) == 4) {
-        store_pack<T, 4>(out + d, f);
-      } else {
-        uint2 u;
-        T* e = reinterpret_cast<T*>(&u);
+  for (int j = 0; j < 2; ++j) {
+    if (d0 + 128 * j >= p.C) continue;
+    float f[4] = {a[j].x * inv, a[j].y * inv, a[j].z * inv, a[j].w * inv};
+    if constexpr (sizeof(T) == 4) {
+      store_pack<T, 4>(out + 128 * j, f);
+    } else {
+      uint2 u;
+      T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = Elem<T>::from_f(f[k]);
-        *reinterpret_cast<uint2*>(out + d) = u;
-      }
+      for (int k = 0; k < 4; ++k) e[k] = Elem<T>::from_f(f[k]);
+      *reinterpret_cast<uint2*>(out + 128 * j) = u;
     }
   }
 }
@@ -655,7 +666,8 @@ int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
 
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st) {
   if (!p.plan.split) return cudaSuccess;
-  const dim3 grid((unsigned)p.plan.ctas, (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps));
+  const dim3 grid((unsigned)p.plan.ctas, (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps),
+                  (unsigned)((p.C + 255) / 256));
   return dtype == V4A_BF16 ? launch_pdl(latent_merge_kernel<__nv_bfloat16>, grid, dim3(32 * kMergeWarps), 0, st, p)
                            : launch_pdl(latent_merge_kernel<float>, grid, dim3(32 * kMergeWarps), 0, st, p);
 }
