@@ -236,13 +236,10 @@ __device__ __forceinline__ int latent_seq_at(const int32_t* pre, int n_seq, int 
   return lo;
 }
 
-// n teams share `total` pairs, team g taking [g * total / n, (g + 1) * total / n).
-__device__ __forceinline__ int latent_team_begin(int g, int total, int n) {
-  return (int)((int64_t)g * total / n);
-}
-__device__ __forceinline__ int latent_team_of(int x, int total, int n) {
-  return (int)((((int64_t)x + 1) * n - 1) / total);
-}
+// Team g takes pairs [g * per, (g + 1) * per) of a line of `total`, with the smallest per that n
+// teams can do with: no team more than in an even split, fewer teams where they suffice, and cuts
+// that fall together with those of equally long units where per divides their length.
+__device__ __forceinline__ int latent_per_team(int total, int n) { return n > 0 ? (total + n - 1) / n : 1; }
 
 // One piece of work of a CTA: a unit and a range of its key tiles.
 struct LatentPiece {
@@ -259,22 +256,22 @@ struct LatentPiece {
 // Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
 // the prefix sums are read in begin() only.
 struct LatentWalk {
-  int x, x1, cta, team, member, U, total, n;
+  int x, x1, cta, team, member, U, n, per;   // n: stride of whole shares; per: pairs of a team
   int b, base;      // current sequence and the pairs before it
   __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int U_) {
     U = U_;
     cta = blockIdx.x;
-    total = pre[p.n_seq];
+    const int total = pre[p.n_seq];
     team = cta / U;
     member = cta % U;
+    n = p.plan.ctas / U;
+    per = latent_per_team(total, n);
     if (!p.plan.split) {           // whole shares in turn, the teams striding over them
-      n = p.plan.ctas / U;
       x = team;
       x1 = total;
     } else {
-      n = min(p.plan.ctas / U, total);
-      x = team < n ? latent_team_begin(team, total, n) : 0;
-      x1 = team < n ? latent_team_begin(team + 1, total, n) : 0;
+      x = team < n ? min(team * per, total) : 0;
+      x1 = team < n ? min(x + per, total) : 0;
     }
     b = x < x1 ? latent_seq_at(pre, p.n_seq, x) : 0;
     base = x < x1 ? pre[b] : 0;
@@ -322,9 +319,9 @@ struct LatentWalk {
       // The team that holds the second piece of a unit posts the unit's merge: teams team - 1
       // to job_last hold its pieces, in slot 1 of the first and slot 0 of the others.
       const int x0 = x - t;
-      const bool second = t > 0 && latent_team_begin(team - 1, total, n) <= x0;
+      const bool second = t > 0 && (team - 1) * per <= x0;
       w.job_rows = second ? w.rows : 0;
-      w.job_last = second ? latent_team_of(x0 + s.tiles - 1, total, n) : 0;
+      w.job_last = second ? (x0 + s.tiles - 1) / per : 0;
       x += take;
     }
     return true;

@@ -110,7 +110,10 @@ bool on_tensor_cores(const v4a_latent_cfg* c) {
   return c->dtype == V4A_BF16 && c->latent_dim == 512 && c->rope.dim == 64;
 }
 
-// The plan of an absorbed call. False when the tiles cannot be counted in 31 bits.
+// The device counts the steps of a call in 31 bits, sums of two of them included.
+constexpr int64_t kMostSteps = (int64_t)1 << 30;
+
+// The plan of an absorbed call. False when there are too many steps.
 bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t max_pos, LatentPlan* pl) {
   const bool tc = on_tensor_cores(c);
   pl->tc = tc;
@@ -128,7 +131,7 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   // out sequences of different lengths (few new tokens each). Prompts, whose units' key counts
   // rise from one to the next, go as whole units, neighbours to neighbouring CTAs.
   pl->split = tiles > 1 && (units < 4 * most || n_tokens < 4 * (int64_t)n_seq);
-  if (pl->split && units * tiles >= INT32_MAX) return false;
+  if (pl->split && units * tiles >= kMostSteps) return false;
   const int64_t want = (pl->split ? units * tiles : units) + 3;
   pl->ctas = (int32_t)(want < most ? want / 4 * 4 : tc || pl->split ? most : want < 65536 ? want / 4 * 4 : 65536);
   return true;
@@ -147,8 +150,8 @@ size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, 
 // ragged chunks 220, 224, 228 and 239 us, before rows without a query were kept off the masked path.
 constexpr int kExpandedSetup = 4;
 
-// The plan of an expanded call (p->tc, pairs, split) and its workspace. False when the steps
-// cannot be counted in 31 bits.
+// The plan of an expanded call (p->tc, pairs, split) and its workspace. False when there are
+// too many steps.
 bool plan_expanded(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_q, int32_t n_k, LatentExpandedParams* p,
                    size_t* ml_at, size_t* job_at, size_t* bytes) {
   p->tc = c->dtype == V4A_BF16 && c->nope_dim == 128 && c->rope.dim == 64 && c->v_dim == 128;
@@ -157,7 +160,7 @@ bool plan_expanded(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_q, int32_t 
   if (!p->tc) return true;
   const int64_t items = ((int64_t)n_q / 512 + n_seq) * c->n_heads;                     // at most
   const int64_t tiles = (int64_t)n_k / 128 + 1 + kExpandedSetup;
-  if (items * tiles >= INT32_MAX) return false;
+  if (items * tiles >= kMostSteps) return false;
   const int64_t pairs = sm_count() / 2;
   p->pairs = (int32_t)(items * tiles < pairs ? items * tiles : pairs);
   p->split = n_k > 128;

@@ -234,15 +234,15 @@ struct Seq {
 
 // Walks a pair's part of the line.
 struct Walk {
-  int x, x1, pair, n, total;
+  int x, x1, pair, per;
   int b, base;                       // current sequence and the steps before it
   int blk, blk_base;                 // current block and the steps before it
   __device__ __forceinline__ void begin(const LatentExpandedParams& p, const int32_t* pre) {
-    total = pre[p.n_seq];
+    const int total = pre[p.n_seq];
     pair = blockIdx.x >> 1;
-    n = min(p.pairs, total);
-    x = pair < n ? latent_team_begin(pair, total, n) : 0;
-    x1 = pair < n ? latent_team_begin(pair + 1, total, n) : 0;
+    per = latent_per_team(total, p.pairs);
+    x = min(pair * per, total);
+    x1 = min(x + per, total);
     b = x < x1 ? latent_seq_at(pre, p.n_seq, x) : 0;
     base = x < x1 ? pre[b] : 0;
     blk = -1;
@@ -278,7 +278,7 @@ struct Walk {
     w.whole = take == len;
     w.slot = (pair << 1) + (from == 0 ? 1 : 0);
     const int x0 = x - from;
-    w.job_last = from > 0 && latent_team_begin(pair - 1, total, n) <= x0 ? latent_team_of(x0 + len - 1, total, n) : -1;
+    w.job_last = from > 0 && (pair - 1) * per <= x0 ? (x0 + len - 1) / per : -1;
     for (int i = 0; i < 2; ++i) {
       const int first = w.q0 + i * (kItem / 2), last = min(first + kItem / 2, w.nq) - 1;
       w.end[i] = last < first ? w.t0 : max(w.t0, min(w.t1, (w.seen(p, last) + kT - 1) / kT));
