@@ -99,6 +99,13 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _scratch(nbytes, device, stream):
+    """A call's workspace, held until the call has returned. It is the call's own: its kernels
+    meet in it, and calls of another thread, stream or graph may be enqueued among them. The
+    allocator hands the memory on in the stream's order, so a layer keeps none."""
+    return _new((nbytes,), torch.uint8, device, stream) if nbytes else None
+
+
 def _word(dev_err, dev):
     _need(dev_err, "dev_err", dev, torch.int32, (1,))
     return dev_err.data_ptr()
@@ -149,7 +156,7 @@ class LatentLayer:
             _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
         if gamma is not None:
             _need(gamma, "gamma", dev, torch.float32, (cfg.latent_dim,))
-        self._ws, self._desc = {}, None
+        self._desc = None
 
     def _describe(self, dev):
         """The C descriptor of the layer's own pool, made anew when the pool's tensors are."""
@@ -183,22 +190,6 @@ class LatentLayer:
         if n_seq > d[5]:
             raise ValueError("cu has %d sequences, the block table %d" % (n_seq, d[5]))
         return dev, n_seq, d[6]
-
-    def _workspace(self, nbytes, device, stream):
-        """Kept per stream, so calls on two streams never share one; a call being captured
-        into a graph gets memory of that graph's own."""
-        if nbytes == 0:
-            return None
-        if stream is not None:
-            with _on(stream):
-                return self._workspace(nbytes, device, None)
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        key = _current_raw(device.index)
-        ws = self._ws.get(key)
-        if ws is None or ws.shape[0] < nbytes:
-            ws = self._ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return ws
 
     def insert(self, cu, start, c, k_pe, dev_err=None, stream=None):
         """Write the cache rows of new tokens: c [n, latent_dim], k_pe [n, rope dim] (rows may
@@ -245,7 +236,7 @@ class LatentLayer:
             _need(out, "out", dev, self.dtype, (n, h, self.cfg.latent_dim))
         lib, cfg = library(), byref(self.cfg)
         nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
-        ws = self._workspace(nb, q.device, stream)
+        ws = _scratch(nb, q.device, stream)
         _check("v4a_latent_attn", lib.v4a_latent_attn(
             cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
             out.data_ptr(), None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
@@ -284,7 +275,7 @@ class LatentLayer:
             _need(out, "out", dev, self.dtype, shape)
         lib, cfg = library(), byref(c)
         nb = lib.v4a_latent_attn_expanded_workspace_size(cfg, n_seq, n_q, n_k)
-        ws = self._workspace(nb, q.device, stream)
+        ws = _scratch(nb, q.device, stream)
         _check("v4a_latent_attn_expanded", lib.v4a_latent_attn_expanded(
             cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), *_strides(k), k_pe.data_ptr(), _stride(k_pe, 0), v.data_ptr(),

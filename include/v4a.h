@@ -329,7 +329,10 @@ int v4a_slot_mapping(const v4a_cache* cache, int32_t n, const int32_t* seq,
  * cu is non-decreasing; rows at or behind cu[n_seq] belong to no sequence: inputs there are
  * not used and outputs there are left as they were. At most V4A_MAX_SEQ sequences a call.
  * Every call reads its inputs only after the kernels enqueued before it on the stream have
- * completed. Two calls that may overlap need workspaces of their own.
+ * completed. A call may enqueue several kernels that meet in its workspace: calls share a
+ * workspace only if they are on one stream and each is made after the one before it has
+ * returned. Calls on different streams, and calls that two threads make at once (on one
+ * stream too), need workspaces of their own.
  */
 #define V4A_MAX_SEQ 1024
 #define V4A_MAX_POS ((int64_t)1 << 36)  /* positions are below this */
