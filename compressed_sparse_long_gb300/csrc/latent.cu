@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
   int seq = 0, head = 0, item = blockIdx.x;
   bool posted = false;
   if constexpr (kPaged) {
-    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
+    walk.begin(p, pre, warp_tot);
   }
   for (;;) {
     // ---- the next unit: its query rows and its keys
@@ -665,8 +665,8 @@ int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st) {
-  if (!p.plan.split) return cudaSuccess;
-  const dim3 grid((unsigned)p.plan.ctas, (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps),
+  if (p.plan.split == kSplitNone) return cudaSuccess;
+  const dim3 grid((unsigned)p.plan.split_ctas, (unsigned)((p.plan.NR + kMergeWarps - 1) / kMergeWarps),
                   (unsigned)((p.C + 255) / 256));
   return dtype == V4A_BF16 ? launch_pdl(latent_merge_kernel<__nv_bfloat16>, grid, dim3(32 * kMergeWarps), 0, st, p)
                            : launch_pdl(latent_merge_kernel<float>, grid, dim3(32 * kMergeWarps), 0, st, p);

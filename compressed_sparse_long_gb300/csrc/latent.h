@@ -61,12 +61,17 @@ struct LatentGatherParams {
 // meet in L2), CTAs in teams of U take equal parts of all (share, tile) pairs in order. A unit
 // whose tiles fall to several teams is left as partial results that a second kernel merges.
 // U is 1, 2 or 4, at most max_U, the largest that costs no more than 1/8 in members without a
-// unit. Without split, whole units go to the CTAs in turn and nothing is merged.
+// unit. Without a split, whole units go to the CTAs in turn and nothing is merged: the host knows
+// that it has many units, but not whether one of them is as long as many others together, so
+// there the device decides.
+constexpr int32_t kSplitNone = 0, kSplitAll = 1, kSplitOnDevice = 2;
 struct LatentPlan {
   int32_t NR, TK;
   int32_t max_U;
-  int32_t ctas;                       // a multiple of max_U
-  int32_t split;
+  int32_t ctas;                       // of the launch, a multiple of max_U
+  int32_t split;                      // kSplit*; the workspace and the merge go with all but None
+  int32_t split_ctas;                 // the CTAs that work where units are split (<= ctas, a multiple
+                                      // of max_U): each may leave two partial results
   int32_t tc;                         // tensor-core kernel
 };
 
@@ -80,9 +85,9 @@ struct LatentAttnParams {
   void* out;
   CacheView cache;
   LatentPlan plan;
-  float* part_o;                      // [ctas][2][NR][C] unnormalised, fp32
-  float* part_ml;                     // [ctas][2][NR][2] reference (log2 units) and sum
-  int32_t* part_job;                  // [ctas][4] what to merge (LatentPiece::job)
+  float* part_o;                      // [split_ctas][2][NR][C] unnormalised, fp32
+  float* part_ml;                     // [split_ctas][2][NR][2] reference (log2 units) and sum
+  int32_t* part_job;                  // [split_ctas][4] what to merge (LatentWalk::post)
   int32_t* err;
 };
 
@@ -145,7 +150,7 @@ struct LatentSeq {
   __device__ __forceinline__ int pairs(int U) const { return shares(U) * tiles; }
 };
 
-__device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b) {
+__device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b, bool split) {
   LatentSeq s;
   const int a = cu_at(p.cu, b, p.n_tokens);
   const int n = max(cu_at(p.cu, b + 1, p.n_tokens) - a, 0);
@@ -154,7 +159,7 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b
   s.start = __ldg(p.start + b);
   s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
   const int64_t keys = min(s.start + n, p.max_pos + 1);
-  s.tiles = !p.plan.split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
+  s.tiles = !split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
   return s;
 }
 
@@ -192,13 +197,47 @@ __device__ __forceinline__ void seq_prefix(int n_seq, int32_t* pre, int32_t* war
   if (threadIdx.x == 0) pre[n_seq] = carry;
   __syncthreads();
 }
+// Whether the call's units are split along the keys, by the whole block (alike in every block).
+// Of many units, whole ones take an even part of the tiles that they see and about half the longest
+// unit more; split ones take an even part of a line in which every unit counts as long as its
+// sequence's last one (in prompts up to twice what they see). The shorter is taken. 64 heads, whole
+// and split: a 2,048-token prompt 429 and 680 us, 700 tokens 90 and 119; 1,000 tokens after 3,000
+// beside eight decode tokens on 20,000 each 944 and 701; 606 beside one on 100,000: 2151 and 137.
+__device__ __forceinline__ bool latent_split(const LatentAttnParams& p, int32_t* warp_tot) {
+  if (p.plan.split != kSplitOnDevice) return p.plan.split == kSplitAll;
+  int sees = 0, line = 0, longest = 0;
+  for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) {
+    const LatentSeq s = latent_seq(p, b, true);
+    if (s.units == 0) continue;
+    const int first = (int)((latent_visible(p, s, 0) + p.plan.TK - 1) / p.plan.TK);
+    sees += s.units * ((first + s.tiles + 1) / 2);
+    line += s.units * s.tiles;
+    longest = max(longest, s.tiles);
+  }
+  if (threadIdx.x < 3) warp_tot[threadIdx.x] = 0;
+  __syncthreads();
+  sees = __reduce_add_sync(0xffffffffu, sees);
+  line = __reduce_add_sync(0xffffffffu, line);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if ((threadIdx.x & 31) == 0 && longest > 0) {
+    atomicAdd(warp_tot, sees);
+    atomicAdd(warp_tot + 1, line);
+    atomicMax(warp_tot + 2, longest);
+  }
+  __syncthreads();
+  const bool split = 2 * (int64_t)warp_tot[0] + (int64_t)warp_tot[2] * p.plan.split_ctas > 2 * (int64_t)warp_tot[1];
+  __syncthreads();
+  return split;
+}
+
 // U and the (share, tile) pairs before each sequence of an absorbed call, by the whole block.
-__device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+__device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, bool split, int32_t* pre,
+                                             int32_t* warp_tot) {
   int U = p.plan.max_U;
   if (U > 1) {
     int c1 = 0, c2 = 0, c4 = 0;
     for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) {
-      const LatentSeq s = latent_seq(p, b);
+      const LatentSeq s = latent_seq(p, b, split);
       c1 += s.pairs(1);
       c2 += s.pairs(2);
       c4 += s.pairs(4);
@@ -222,7 +261,7 @@ __device__ __forceinline__ int latent_prefix(const LatentAttnParams& p, int32_t*
     if (U == 4 && (int64_t)c4 * 4 > most) U = 2;
     if (U == 2 && (int64_t)c2 * 2 > most) U = 1;
   }
-  seq_prefix(p.n_seq, pre, warp_tot, [&](int b) { return latent_seq(p, b).pairs(U); });
+  seq_prefix(p.n_seq, pre, warp_tot, [&](int b) { return latent_seq(p, b, split).pairs(U); });
   return U;
 }
 
@@ -256,30 +295,34 @@ struct LatentPiece {
 // Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
 // the prefix sums are read in begin() only.
 struct LatentWalk {
-  int x, x1, cta, team, member, U, n, per;   // n: stride of whole shares; per: pairs of a team
+  int x, x1, cta, team, member, U, n, per;   // n: stride of whole shares (0: split ones); per: pairs of a team
   int b, base;      // current sequence and the pairs before it
-  __device__ __forceinline__ void begin(const LatentAttnParams& p, const int32_t* pre, int U_) {
-    U = U_;
+  // The plan, in pre (shared memory) and here, by the whole block.
+  __device__ __forceinline__ void begin(const LatentAttnParams& p, int32_t* pre, int32_t* warp_tot) {
+    const bool split = latent_split(p, warp_tot);
+    U = latent_prefix(p, split, pre, warp_tot);
     cta = blockIdx.x;
     const int total = pre[p.n_seq];
     team = cta / U;
     member = cta % U;
-    n = p.plan.ctas / U;
-    per = latent_per_team(total, n);
-    if (!p.plan.split) {           // whole shares in turn, the teams striding over them
+    const int teams = (split ? p.plan.split_ctas : p.plan.ctas) / U;
+    per = latent_per_team(total, teams);
+    if (!split) {                  // whole shares in turn, the teams striding over them
+      n = teams;
       x = team;
       x1 = total;
     } else {
-      x = team < n ? min(team * per, total) : 0;
-      x1 = team < n ? min(x + per, total) : 0;
+      n = 0;
+      x = team < teams ? min(team * per, total) : 0;
+      x1 = team < teams ? min(x + per, total) : 0;
     }
     b = x < x1 ? latent_seq_at(pre, p.n_seq, x) : 0;
     base = x < x1 ? pre[b] : 0;
   }
   // A team's merge job, if any, is its first piece's: every team posts one, empty or not,
-  // before that piece's results.
+  // before that piece's results (an empty one too where the device decided against a split).
   __device__ __forceinline__ void post(const LatentAttnParams& p, const LatentPiece* w) const {
-    if (!p.plan.split) return;
+    if (p.plan.split == kSplitNone || cta >= p.plan.split_ctas) return;
     const int rows = w ? w->job_rows : 0;
     *reinterpret_cast<int4*>(p.part_job + 4 * cta) =
         make_int4(rows, rows > 0 ? w->row0 : 0, rows > 0 ? w->job_last : 0, U);
@@ -287,10 +330,10 @@ struct LatentWalk {
   // The next piece, or false. A piece may have no unit (rows == 0) or no keys.
   __device__ __forceinline__ bool next(const LatentAttnParams& p, LatentPiece& w) {
     if (x >= x1) return false;
-    LatentSeq s = latent_seq(p, b);
+    LatentSeq s = latent_seq(p, b, n == 0);
     while (b + 1 < p.n_seq && x >= base + s.pairs(U)) {
       base += s.pairs(U);
-      s = latent_seq(p, ++b);
+      s = latent_seq(p, ++b, n == 0);
     }
     const int r = x - base;
     const int share = r / s.tiles, t = r - share * s.tiles;
@@ -303,7 +346,7 @@ struct LatentWalk {
     w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
     w.keys0 = w.rows > 0 ? latent_visible(p, s, ur / p.H) : 0;
     const int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
-    if (!p.plan.split) {
+    if (n > 0) {
       w.tile0 = 0;
       w.tile1 = unit_tiles;
       w.whole = 1;

@@ -129,19 +129,25 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   const int64_t most = tc ? sm_count() / 4 * 4 : 2 * sm_count();  // CTAs at once
   // Units are split along the keys where that fills the GPU (fewer than four a CTA) or evens
   // out sequences of different lengths (few new tokens each). Prompts, whose units' key counts
-  // rise from one to the next, go as whole units, neighbours to neighbouring CTAs.
-  pl->split = tiles > 1 && (units < 4 * most || n_tokens < 4 * (int64_t)n_seq);
-  if (pl->split && units * tiles >= kMostSteps) return false;
-  const int64_t want = (pl->split ? units * tiles : units) + 3;
-  pl->ctas = (int32_t)(want < most ? want / 4 * 4 : tc || pl->split ? most : want < 65536 ? want / 4 * 4 : 65536);
+  // rise from one to the next, go as whole units, neighbours to neighbouring CTAs, unless single
+  // units are long beside a CTA's part of all: only the device sees that (latent_split).
+  const bool few = units < 4 * most || n_tokens < 4 * (int64_t)n_seq;
+  pl->split = tiles == 1 ? kSplitNone : few ? kSplitAll : kSplitOnDevice;
+  if (units * tiles >= kMostSteps) {
+    if (pl->split == kSplitAll) return false;
+    pl->split = kSplitNone;
+  }
+  const int64_t want = (pl->split == kSplitAll ? units * tiles : units) + 3;
+  pl->split_ctas = (int32_t)(want < most ? want / 4 * 4 : most);
+  pl->ctas = tc || pl->split == kSplitAll ? pl->split_ctas : (int32_t)(want < 65536 ? want / 4 * 4 : 65536);
   return true;
 }
 
 size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, size_t* job_at) {
-  const size_t slots = (size_t)pl.ctas * 2;
+  const size_t slots = (size_t)pl.split_ctas * 2;
   *ml_at = align_up(slots * pl.NR * c->latent_dim * sizeof(float), 256);
   *job_at = *ml_at + align_up(slots * pl.NR * 2 * sizeof(float), 256);
-  return pl.split ? *job_at + align_up(slots * 2 * sizeof(int32_t), 256) : 0;
+  return pl.split != kSplitNone ? *job_at + align_up(slots * 2 * sizeof(int32_t), 256) : 0;
 }
 
 // Steps that starting an item counts for when the line is cut into equal parts. Its copies, first

@@ -158,8 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   LatentWalk walk;
   LatentPiece w;
   {
-    int32_t* pre = reinterpret_cast<int32_t*>(kbuf);
-    walk.begin(p, pre, latent_prefix(p, pre, warp_tot));
+    walk.begin(p, reinterpret_cast<int32_t*>(kbuf), warp_tot);
   }
   tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
   tc::fence_before_sync();

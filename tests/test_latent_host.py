@@ -132,3 +132,15 @@ def test_a_layer_keeps_no_workspace(world, form):
     lay = world.layer(form)
     world.call(lay, form)
     assert world.scratch and all(r() is None for r in world.scratch)
+
+
+def test_long_sequences_beside_many_short_units_can_be_split():
+    """A 606-token chunk on a short context and one decode token on 100,000 cached ones, 64 heads:
+    more units than whole ones need, and one as long as 780 tiles. Splitting it needs a workspace."""
+    cfg = v4a.latent_cfg(v4a.BF16, 64, 512, v4a.rope_cfg(64))
+    for n_tokens in (600, 607, 5000):
+        assert v4a.v4a_latent_attn_workspace_size(cfg, 2, n_tokens, 99999) > 0
+    small = v4a.latent_cfg(v4a.FP32, 8, 128, v4a.rope_cfg(32))
+    assert v4a.v4a_latent_attn_workspace_size(small, 2, 5000, 99999) > 0
+    # steps past what the device counts in: whole units, as the host alone can have them
+    assert v4a.v4a_latent_attn_workspace_size(cfg, 2, 10000, (1 << 36) - 1) == 0
