@@ -36,8 +36,8 @@ constexpr int kThreads = 384, kStages = 3;
 constexpr int kT = 128;                                          // a CTA's queries of a tile; keys of a step
 constexpr int kItem = 512;                                       // queries of an item
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.0f;                                   // log2 units
-constexpr float kLimit = 65536.0f;                               // of a tile's sum
+constexpr float kRoom = 16.0f, kRaise = -8.0f;                   // log2 units: a reference above its maximum;
+                                                                 // a weight that raises it
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
@@ -132,15 +132,16 @@ __device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int
     for (int i = 0; i < 4; ++i) tc::tmem_ld32(scol + 32 * i, *reinterpret_cast<float(*)[32]>(&s[32 * i]));
     tc::tmem_wait_ld();
     const int here = row ? seen - t * kT : kT;   // keys of the tile that this query sees
-    // Weights are floating-point numbers, so the reference m need not be the maximum: a tile that
-    // every query of the warp sees whole is taken against m as it is, and only if a sum
-    // passes kLimit is the tile done again with its maxima.
+    // Weights are floating-point numbers, so the reference m need not be the maximum (it is set
+    // 2^16 above it): a tile that every query of the warp sees whole is taken against m as it is,
+    // and only if a sum passes 1 is the tile done again with its maxima. So no weight counts for
+    // more than 1, and sums overflow only where the plain softmax's would.
     uint32_t pw[64];
     float sum = 0.f;
     bool slow = __any_sync(0xffffffffu, row && (here < kT || m == -INFINITY));
     if (!slow) {
       sum = weights(s, k22, -m, pw);
-      slow = __any_sync(0xffffffffu, row && !(sum <= kLimit));
+      slow = __any_sync(0xffffffffu, row && !(sum <= 1.f));
       if (slow) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::tmem_ld32(scol + 32 * i, *reinterpret_cast<float(*)[32]>(&s[32 * i]));
@@ -159,10 +160,10 @@ __device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k2;
       float corr = 1.f;
       if (t == t0) {
-        m = mt;
+        m = mt + kRoom;
       } else if (mt > m + kRaise) {
-        corr = fast_exp2(m - mt);             // 0 from -inf
-        m = mt;
+        corr = fast_exp2(m - (mt + kRoom));   // 0 from -inf
+        m = mt + kRoom;
       }
       if (t > t0 && __any_sync(0xffffffffu, corr != 1.f)) {
         // S of this tile is done, and with it every product issued before it

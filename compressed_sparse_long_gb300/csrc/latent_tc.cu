@@ -20,10 +20,11 @@
 // 16 sequences of 4616-108051 tokens, 128 heads: 194 us, 835 TFLOP/s.
 //
 // Warps 0-7: softmax and output. A thread holds one key's 32 logits (warps 0-3 rows 0-31, warps
-// 4-7 rows 32-63 of the unit). A row's weights are taken against a reference, its maximum over
-// the first tile; maxima over the keys (redux, and through shared memory) are needed again only
-// where a tile is masked or a weight would pass 2^16, and then the reference is raised where it
-// is exceeded by more than 2^8 and the accumulator and sums rescaled. Warp 8: copies, with the
+// 4-7 rows 32-63 of the unit). A row's weights are taken against a reference, 2^16 times its
+// largest over the first tile; maxima over the keys (redux, and through shared memory) are needed
+// again only where a tile is masked or a weight would pass 1, and then the reference is raised
+// where a weight passes 2^-8 and the accumulator and sums rescaled. So no weight counts for more
+// than 1, and sums overflow only where the plain softmax's would. Warp 8: copies, with the
 // next tile requested into L2 a tile ahead. Warp 9: products.
 #include "kernels.h"
 #include "latent.h"
@@ -47,7 +48,8 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kKBlock, "the plan's prefix sums use a key block before its first copy");
 constexpr uint32_t kSCol = 0, kOCol = 64, kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.0f, kLimit = 16.0f;                   // log2 units
+constexpr float kRoom = 16.0f, kRaise = -8.0f;                   // log2 units: a reference above its maximum;
+                                                                 // a weight that raises it
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
@@ -212,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t x0 = (int64_t)t * kTK;
         const int valid = tile_ok[g & 1] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
         // A tile that every row sees whole, with every row's reference set: the weights are
-        // taken against the references as they are, unless one of them would pass 2^kLimit
-        // (weights and sums are floating-point numbers, so a reference need not be the
-        // maximum). The group agrees on that while it computes the exponentials.
+        // taken against the references as they are, unless one of them would pass 1 (weights
+        // and sums are floating-point numbers, so a reference need not be the maximum). The
+        // group agrees on that while it computes the exponentials.
         bool slow = valid < kTK || w.keys0 < x0 + kTK || __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
         float4 ref[8];
 #pragma unroll
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s[c + 3] = fmaf(s[c + 3], k2, -mv.w);
             top = fmaxf(top, fmaxf(fmaxf(s[c], s[c + 1]), fmaxf(s[c + 2], s[c + 3])));
           }
-          const bool over = __any_sync(0xffffffffu, top > kLimit);
+          const bool over = __any_sync(0xffffffffu, top > 0.f);
           if (lane == 0) {
             if (over) raised[half * 2 + (g & 1)] = g + 1;
             tc::mbar_arrive(redb + half);
@@ -266,10 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * k2;
           float corr = 1.f;
           if (t == w.tile0) {
-            m = mt;
+            m = mt + kRoom;
           } else if (mt > m + kRaise) {
-            corr = fast_exp2(m - mt);             // 0 from -inf
-            m = mt;
+            corr = fast_exp2(m - (mt + kRoom));   // 0 from -inf
+            m = mt + kRoom;
           }
           __syncwarp();
           mb[lane] = m == -INFINITY ? none : m;

@@ -333,6 +333,9 @@ int v4a_slot_mapping(const v4a_cache* cache, int32_t n, const int32_t* seq,
  * workspace only if they are on one stream and each is made after the one before it has
  * returned. Calls on different streams, and calls that two threads make at once (on one
  * stream too), need workspaces of their own.
+ * Attention forms sum w v with weights w of at most 1, divided at the end by sum w: a result
+ * is lost to overflow only where such a sum in 32 bits is (|v| above 2^128 / keys), and values
+ * below 2^-110 may be lost beside 0.
  */
 #define V4A_MAX_SEQ 1024
 #define V4A_MAX_POS ((int64_t)1 << 36)  /* positions are below this */

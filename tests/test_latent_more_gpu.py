@@ -1,10 +1,14 @@
-"""GPU: latent attention and rotary positions at the ends of their ranges: lengths
-that differ widely. Tolerances as in latent_helpers."""
+"""GPU: latent attention at the ends of its ranges: large and small values, lengths that differ
+widely. Tolerances as in latent_helpers."""
 import numpy as np
 import pytest
 import torch
 
-from latent_helpers import BF, F32, batch, check, f64, ints, layer, rand
+import compressed_sparse_long_gb300 as v4a
+from compressed_sparse_long_gb300.latent import LatentLayer
+from latent_helpers import (BF, F32, attn_tolerance, batch, check, f64, ints, layer, logit_bound,
+                            rand)
+from oracle import latent_oracle as O
 from test_latent_gpu import _attn
 
 pytestmark = pytest.mark.gpu
@@ -17,6 +21,53 @@ def _cuda():
     torch.cuda.synchronize()
     yield
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------------ ranges
+# Values of 1e35 under 700 keys: the weighted sum in 32 bits, with weights of at most 1, reaches
+# 7e37 at most, so the softmax's definition is computable and its result is of order 1e35. The
+# keys behind the first tile weigh up to 2^15 of those in it: no weight may count for more than 1.
+@pytest.mark.parametrize("size", [1e35, 1e-28])
+def test_expanded_values_near_the_ends_of_the_type(size):
+    rng = np.random.default_rng(40)
+    heads, n, nq = 64, 700, 3                      # a pair of CTAs walks several tiles of an item
+    cfg = v4a.latent_cfg(v4a.BF16, heads, 512, v4a.rope_cfg(64))
+    q, pe = torch.ones(nq, heads, 192, device="cuda", dtype=BF), torch.zeros(n, 64, device="cuda", dtype=BF)
+    k = torch.zeros(n, heads, 128, device="cuda", dtype=BF)
+    k[128:] = 0.6377                               # 8.5 in log2 units above the first tile
+    v = (size * rand(rng, torch.float32, n, heads, 128).abs()).to(BF)
+    cu = [0, nq], [0, n]
+    got = LatentLayer(cfg, None).attention_expanded(ints(cu[0], torch.int32), ints(cu[1], torch.int32),
+                                                    q, k, pe, v)
+    vs = f64(v) / size                             # the tolerance's absolute part is for values of order 1
+    ref, mag = O.attention_expanded(*cu, f64(q), f64(k), f64(pe), vs, cfg.softmax_scale, True)
+    lm = logit_bound(f64(q)[:, 0], np.concatenate([f64(k)[:, 0], f64(pe)], 1), cfg.softmax_scale)
+    check(got.double() / size, ref, attn_tolerance(BF, ref, mag, 192, n, lm))
+
+
+@pytest.mark.parametrize("size", [1e35, 1e-28])
+def test_absorbed_values_near_the_ends_of_the_type(size):
+    """1024 heads, so that a CTA walks several tiles of a sequence from the first on."""
+    rng = np.random.default_rng(41)
+    heads, total = 1024, [700] * 4
+    lay, bt = layer(rng, BF, heads, total)
+    for b in range(4):
+        rows = [O.slot(bt, b, x) for x in range(700)]
+        lay.pool.data[rows, :512] = (size * rand(rng, torch.float32, 700, 512).abs()).to(BF)
+        lay.pool.data[rows, 512:] = 0
+        lay.pool.data[rows[128:], 512:] = 2.25     # 15 in log2 units above the first tile
+    q = torch.zeros(4, heads, 576, device="cuda", dtype=BF)
+    q[..., 512:] = 1
+    cu, start = [0, 1, 2, 3, 4], [699] * 4
+    got = lay.attention(ints(cu, torch.int32), ints(start, torch.int64), 699, q)
+    # every head's query is the same
+    pool, q1 = f64(lay.pool.data), f64(q)[:, :1]
+    pool[:, :512] /= size
+    ref, mag = O.attention(pool, bt, cu, start, q1, lay.cfg.softmax_scale, 512)
+    used = pool[[O.slot(bt, b, x) for b in range(4) for x in range(700)]]
+    tol = attn_tolerance(BF, ref, mag, 576, 700, logit_bound(q1, used, lay.cfg.softmax_scale))
+    assert all(torch.equal(got[:, :1], got[:, h:h + 1]) for h in range(1, heads))
+    check(got[:, :1].double() / size, ref, tol)
 
 
 # -------------------------------------------------------------------- uneven batches
