@@ -99,6 +99,11 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeros(shape, dtype, device, stream):
+    with _on(stream):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+
 def _scratch(nbytes, device, stream):
     """A call's workspace, held until the call has returned. It is the call's own: its kernels
     meet in it, and calls of another thread, stream or graph may be enqueued among them. The
@@ -111,11 +116,8 @@ def _word(dev_err, dev):
     return dev_err.data_ptr()
 
 
-def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
-         inverse: bool = False, dev_err=None, stream=None) -> torch.Tensor:
-    """Rotate x [n, H, dim] or [n, dim] (bf16 or fp32, any strides with a dense last dimension:
-    a slice of wider heads, say) at positions pos [n] int64. ``out`` is a new tensor unless
-    given; ``out=x`` rotates in place. ``inverse`` turns back; it is also the gradient's map."""
+def _rope(cfg, x, pos, out, inverse, dev_err, stream, new=_new):
+    """rope() without a graph; `new` makes the result where none is given."""
     kind = _KINDS.get(x.dtype) if isinstance(x, torch.Tensor) else None
     shape = x.shape if kind is not None else ()
     if len(shape) not in (2, 3):
@@ -126,7 +128,7 @@ def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | N
         _need(x, "x", dev, x.dtype, (None,) * (len(shape) - 1) + (cfg.dim,), contiguous=False)
         _need(pos, "pos", dev, torch.int64, (shape[0],))
     if out is None:
-        out = _new(shape, x.dtype, x.device, stream)
+        out = new(shape, x.dtype, x.device, stream)
     elif not _rows(out, dev, x.dtype, shape):
         _need(out, "out", dev, x.dtype, shape, contiguous=False)
     heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
@@ -137,8 +139,41 @@ def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | N
     return out
 
 
+class _Rope(torch.autograd.Function):
+    """A recorded call: its gradient is the turn the other way, itself such a call."""
+
+    @staticmethod
+    def forward(ctx, x, pos, cfg, inverse, dev_err, stream):
+        # a token at a bad position is not written: its result and its gradient are zeros here
+        y = _rope(cfg, x, pos, None, inverse, dev_err, stream, _zeros)
+        ctx.save_for_backward(pos)
+        ctx.cfg, ctx.inverse = RopeCfg.from_buffer_copy(cfg), inverse
+        return y
+
+    @staticmethod
+    def backward(ctx, g):
+        g = g if g.stride(-1) == 1 else g.contiguous()
+        turned = _Rope.apply(g, ctx.saved_tensors[0], ctx.cfg, not ctx.inverse, None, None)
+        return turned, None, None, None, None, None
+
+
+def rope(cfg: RopeCfg, x: torch.Tensor, pos: torch.Tensor, out: torch.Tensor | None = None,
+         inverse: bool = False, dev_err=None, stream=None) -> torch.Tensor:
+    """Rotate x [n, H, dim] or [n, dim] (bf16 or fp32, any strides with a dense last dimension:
+    a slice of wider heads, say) at positions pos [n] int64. ``out`` is a new tensor unless
+    given; ``out=x`` rotates in place. ``inverse`` turns back; it is also the gradient's map,
+    and the gradient of a call without ``out`` on an x that requires grad."""
+    if isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out: a call that writes it is not recorded, but x requires grad")
+        return _Rope.apply(x, pos, cfg, inverse, dev_err, stream)
+    return _rope(cfg, x, pos, out, inverse, dev_err, stream)
+
+
 class LatentLayer:
     """A latent-attention layer's configuration, cache and norm weight.
+
+    Forward only: the methods' results are outside any graph, whatever their inputs require.
 
     pool: PagedPool of [n_pages * 256, latent_dim + rope dim] rows, or None for a layer that
     is only used in the expanded form; gamma: fp32 [latent_dim] or None (no norm at insert).
@@ -289,5 +324,5 @@ class LatentLayer:
         place (pos [n]: the new tokens' positions), attend."""
         self.insert(cu, start, c, k_pe, dev_err, stream)
         rot = q[..., self.cfg.latent_dim:]
-        rope(self.cfg.rope, rot, pos, out=rot, dev_err=dev_err, stream=stream)
+        _rope(self.cfg.rope, rot, pos, rot, False, dev_err, stream)
         return self.attention(cu, start, max_pos, q, out=out, dev_err=dev_err, stream=stream)

@@ -1,15 +1,15 @@
-"""GPU: latent attention at the ends of its ranges: large and small values, lengths that differ
-widely. Tolerances as in latent_helpers."""
+"""GPU: gradients of the rotation, and latent attention at the ends of its ranges: large and small
+values, lengths that differ widely. Tolerances as in latent_helpers."""
 import numpy as np
 import pytest
 import torch
 
 import compressed_sparse_long_gb300 as v4a
-from compressed_sparse_long_gb300.latent import LatentLayer
-from latent_helpers import (BF, F32, attn_tolerance, batch, check, f64, ints, layer, logit_bound,
-                            rand)
+from compressed_sparse_long_gb300.latent import LatentLayer, rope
+from latent_helpers import (BF, F32, attn_tolerance, batch, check, f64, half_step, ints, layer,
+                            logit_bound, rand)
 from oracle import latent_oracle as O
-from test_latent_gpu import _attn
+from test_latent_gpu import _attn, _rope_case, _rope_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +21,96 @@ def _cuda():
     torch.cuda.synchronize()
     yield
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------------------- gradients
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["pairs", "half"])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_records_its_gradient(dtype, layout, inverse):
+    """An x that requires grad gets the formula's gradient, J^T g with J the rotation, through a
+    slice of wider heads; a plain call's bytes are the same."""
+    rng = np.random.default_rng(44)
+    cfg, rate = _rope_case(64, layout, "yarn", 1.1)
+    q = rand(rng, dtype, 9, 4, 80).requires_grad_()
+    p = rng.integers(0, 100000, 9)
+    pos, g = ints(p, torch.int64), rand(rng, dtype, 9, 4, 64)
+    y = rope(cfg, q[..., 8:72], pos, inverse=inverse)
+    assert y.requires_grad
+    with torch.no_grad():
+        plain = rope(cfg, q[..., 8:72], pos, inverse=inverse)
+    assert not plain.requires_grad and torch.equal(plain, y)
+    (y * g).sum().backward()
+    ref = O.rope(f64(g), p, rate, layout, 1.1, not inverse)
+    check(q.grad[..., 8:72], ref, _rope_tol(f64(g), ref, dtype, layout, 1.1))
+    assert (q.grad[..., :8] == 0).all() and (q.grad[..., 72:] == 0).all()
+    # by differences of the 64-bit form, along one direction
+    dx, step = rng.standard_normal((9, 4, 64)), 1e-6
+    x = f64(q)[..., 8:72]
+    dy = (O.rope(x + step * dx, p, rate, layout, 1.1, inverse) -
+          O.rope(x - step * dx, p, rate, layout, 1.1, inverse)) / (2 * step)
+    lhs, rhs = float((f64(g) * dy).sum()), float((f64(q.grad)[..., 8:72] * dx).sum())
+    size = float(((np.abs(f64(q.grad))[..., 8:72] + 4) * np.abs(dx)).sum())
+    assert abs(lhs - rhs) <= (1e-5 + half_step(dtype)) * size
+
+
+def test_rope_gradient_of_a_gradient_shared_heads_and_sums():
+    rng = np.random.default_rng(45)
+    cfg, _ = _rope_case(32, "half", "none")
+    pos = ints(rng.integers(0, 9000, 5), torch.int64)
+    x = rand(rng, F32, 5, 1, 32).requires_grad_()
+    y = rope(cfg, x.expand(5, 3, 32), pos)         # one row for three heads: their gradients add
+    (gx,) = torch.autograd.grad(y.sum(), x, create_graph=True)   # of a sum: an expanded scalar
+    one = rope(cfg, torch.ones(5, 1, 32, device="cuda"), pos, inverse=True)
+    # each rotated 1 is a sum of two products of cosine and sine, all three alike
+    assert (gx - 3 * one).abs().max() <= 3 * 4 * 2.0 ** -23 * 2
+    w = rand(rng, F32, 5, 3, 32).requires_grad_()
+    (gx,) = torch.autograd.grad((rope(cfg, x.expand(5, 3, 32), pos) * w).sum(), x, create_graph=True)
+    (gw,) = torch.autograd.grad(gx.sum(), w)       # d/dw of 1 . J^T w is J 1
+    assert torch.equal(gw, rope(cfg, torch.ones(5, 3, 32, device="cuda"), pos))
+
+
+def test_rope_recorded_calls_of_bad_positions_configurations_and_graphs():
+    rng = np.random.default_rng(46)
+    cfg, _ = _rope_case(64, "pairs", "none")
+    x, pos = rand(rng, F32, 4, 2, 64).requires_grad_(), ints([3, -1, 1 << 36, 9], torch.int64)
+    y = rope(cfg, x, pos)
+    cfg.base = 500.0                               # the call's configuration was taken with it
+    y.sum().backward()
+    assert (y[1:3] == 0).all() and (x.grad[1:3] == 0).all()
+    cfg.base = 10000.0
+    assert torch.equal(x.grad[0], rope(cfg, torch.ones(4, 2, 64, device="cuda"), pos, inverse=True)[0])
+    # writing a given tensor is not recorded: refused where a gradient is asked for
+    with pytest.raises(ValueError):
+        rope(cfg, x, pos, out=torch.empty_like(x))
+    with torch.no_grad():
+        rope(cfg, x, pos, out=torch.empty_like(x))
+    # forward and backward captured and replayed on other values
+    leaf, pos = rand(rng, BF, 6, 3, 64).requires_grad_(), ints([0, 5, 70, 800, 9000, 7], torch.int64)
+    w = rand(rng, BF, 6, 3, 64)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.autograd.grad((rope(cfg, leaf, pos) * w).sum(), leaf)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (grad,) = torch.autograd.grad((rope(cfg, leaf, pos) * w).sum(), leaf)
+    w.copy_(rand(rng, BF, 6, 3, 64))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(grad, rope(cfg, w, pos, inverse=True))
+
+
+def test_a_step_on_queries_that_require_grad_runs_as_it_is():
+    """Inference without no_grad on a model's own outputs: the layer is forward only."""
+    rng = np.random.default_rng(47)
+    lay, bt = layer(rng, BF, 16, [300])
+    q, x = rand(rng, BF, 1, 16, 576), rand(rng, BF, 1, 576)
+    args = (ints([0, 1], torch.int32), ints([299], torch.int64), 299, ints([299], torch.int64), x[:, :512], x[:, 512:])
+    ref = lay.step(*args, q.clone())
+    q.requires_grad_()
+    out = lay.step(*args, q * 1)
+    assert torch.equal(out, ref) and not out.requires_grad
 
 
 # ------------------------------------------------------------------------------ ranges
