@@ -391,7 +391,9 @@ typedef struct v4a_latent_cfg {
  * amplitude the gradient of the forward call with respect to x.
  * The rotated part of a wider head is given by its pointer and strides.
  *
- * dtype: V4A_FP32 or V4A_BF16 (computed in fp32, the angle reduced exactly, rounded once)
+ * dtype: V4A_FP32 or V4A_BF16 (computed in fp32, the angle reduced exactly, rounded once).
+ *        Cosine and sine are good to a few 2^-24 for positions below 2^28; beyond, the rates,
+ *        64-bit numbers, add up to pos * 2^-49
  * pos:   device int64 [n_tokens], each in [0, V4A_MAX_POS); a token outside it is left
  *        unwritten and sets V4A_DEV_BAD_POS
  * x, y:  device, element (t, h, d) at t * token_stride + h * head_stride + d (strides in

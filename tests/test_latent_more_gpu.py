@@ -1,5 +1,8 @@
-"""GPU: gradients of the rotation, and latent attention at the ends of its ranges: large and small
+"""GPU: gradients of the rotation and far positions, and latent attention at the ends of its ranges: large and small
 values, lengths that differ widely. Tolerances as in latent_helpers."""
+import decimal
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -21,6 +24,49 @@ def _cuda():
     torch.cuda.synchronize()
     yield
     torch.cuda.synchronize()
+
+
+# ----------------------------------------------------------------------- far positions
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def _turn(dim, scaling, pos):
+    """Angles below one turn of exact positions, from rates in 60 digits."""
+    with decimal.localcontext(decimal.Context(prec=60)):
+        out = []
+        for i in range(dim // 2):
+            keep = decimal.Decimal(1)
+            if scaling == "yarn":
+                def pair(t):
+                    return dim * math.log(4096 / (t * 2 * math.pi)) / (2 * math.log(10000))
+                a, b = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), dim - 1)
+                keep -= min(decimal.Decimal(1), max(decimal.Decimal(0), decimal.Decimal(i - a) / (b - a)))
+            theta = decimal.Decimal(10000) ** (decimal.Decimal(-2 * i) / dim)
+            theta *= keep + (1 - keep) / 8
+            out.append([float(p * theta % (2 * PI)) for p in pos])
+    return np.array(out).T
+
+
+@pytest.mark.parametrize("layout", ["pairs", "half"])
+@pytest.mark.parametrize("scaling", ["none", "yarn"])
+def test_rope_far_positions(layout, scaling):
+    """The rates are 64-bit numbers of a few roundings (two powers, a product, the scaling, the
+    division by 2 pi: at most 12 2^-53 in all, and no rate is above 1), so an angle is off by up to
+    12 2^-53 of its position, beside the 4 2^-23 of near ones."""
+    rng = np.random.default_rng(48)
+    dim, far = 64, [2 ** 21 + 1, 2 ** 24 - 1, 2 ** 24 + 12345, 2 ** 28 + 77, 2 ** 30 - 3, 2 ** 32 + 999, 2 ** 36 - 1]
+    cfg, _ = _rope_case(dim, layout, scaling)
+    x = rand(rng, F32, len(far), 2, dim)
+    got, ang, xs = rope(cfg, x, ints(far, torch.int64)), _turn(dim, scaling, far), f64(x)
+    a, b = (xs[..., :32], xs[..., 32:]) if layout == "half" else (xs[..., ::2], xs[..., 1::2])
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    r0, r1, size = a * c - b * s, a * s + b * c, np.abs(a) + np.abs(b)
+    if layout == "half":
+        ref, size = np.concatenate([r0, r1], -1), np.concatenate([size, size], -1)
+    else:
+        ref, size = np.stack([r0, r1], -1).reshape(xs.shape), np.repeat(size, 2, -1)
+    off = 4 * 2.0 ** -23 + 12 * 2.0 ** -53 * np.array(far, np.float64)[:, None, None]
+    check(got, ref, off * size)
 
 
 # --------------------------------------------------------------------------- gradients
