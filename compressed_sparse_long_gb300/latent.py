@@ -191,30 +191,23 @@ class LatentLayer:
             _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
         if gamma is not None:
             _need(gamma, "gamma", dev, torch.float32, (cfg.latent_dim,))
-        self._desc = None
 
     def _describe(self, dev):
-        """The C descriptor of the layer's own pool, made anew when the pool's tensors are."""
+        """(sequences of the block table, C descriptor) of the layer's pool as it is now."""
         pool = self.pool
         if pool is None:
             raise ValueError("this layer has no cache")
         data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
-        d = self._desc
-        if (d is None or d[0] is not data or d[1] is not bt or d[2] != rows
-                or d[3] != data.data_ptr() or d[6].block_table != bt.data_ptr()):
+        n, (b, m) = data.shape[0], bt.shape if bt.dim() == 2 else (0, 0)
+        if not (_fits(data, dev, self.dtype, (n, self.width)) and _fits(bt, dev, torch.int32, (b, m))):
             _need(data, "pool.data", dev, self.dtype, (None, self.width))
             _need(bt, "pool.block_table", dev, torch.int32, (None, None))
-            c = Cache(data.data_ptr(), None, bt.data_ptr(), bt.shape[1], rows,
-                      data.shape[0] // rows, self.width, 0)
-            d = self._desc = (data, bt, rows, data.data_ptr(), data.get_device(), bt.shape[0], c)
-        if d[4] != dev:
-            raise ValueError("pool.data is on cuda:%d, the current device is cuda:%d" % (d[4], dev))
-        return d
+        return b, Cache(data.data_ptr(), None, bt.data_ptr(), m, rows, n // rows, self.width, 0)
 
     def _batch(self, cu, start):
         """(device, sequences, cache descriptor) of a call over the cache."""
         dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-        d = self._describe(dev)
+        known, cache = self._describe(dev)
         n_seq = cu.numel() - 1 if isinstance(cu, torch.Tensor) else -1
         if n_seq < 0 or not (_fits(cu, dev, torch.int32, (n_seq + 1,))
                              and _fits(start, dev, torch.int64, (n_seq,))):
@@ -222,9 +215,9 @@ class LatentLayer:
             if n_seq < 0:
                 raise ValueError("cu: expected the sequences' first rows and the end")
             _need(start, "start", dev, torch.int64, (n_seq,))
-        if n_seq > d[5]:
-            raise ValueError("cu has %d sequences, the block table %d" % (n_seq, d[5]))
-        return dev, n_seq, d[6]
+        if n_seq > known:
+            raise ValueError("cu has %d sequences, the block table %d" % (n_seq, known))
+        return dev, n_seq, cache
 
     def insert(self, cu, start, c, k_pe, dev_err=None, stream=None):
         """Write the cache rows of new tokens: c [n, latent_dim], k_pe [n, rope dim] (rows may
@@ -235,6 +228,8 @@ class LatentLayer:
                 and _rows(k_pe, dev, self.dtype, (n, self.cfg.rope.dim))):
             _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
             _need(k_pe, "k_pe", dev, self.dtype, (n, self.cfg.rope.dim), contiguous=False)
+        if self.gamma is not None and not _fits(self.gamma, dev, torch.float32, (self.cfg.latent_dim,)):
+            _need(self.gamma, "gamma", dev, torch.float32, (self.cfg.latent_dim,))
         _check("v4a_latent_insert", library().v4a_latent_insert(
             byref(self.cfg), n_seq, n, cu.data_ptr(), start.data_ptr(), c.data_ptr(),
             _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),

@@ -134,6 +134,42 @@ def test_a_layer_keeps_no_workspace(world, form):
     assert world.scratch and all(r() is None for r in world.scratch)
 
 
+def test_a_pool_changed_in_place_is_described_as_it_is(world):
+    """Tables and pools that change under the same tensors, and tensors that replace others."""
+    lay, seen = world.layer("absorbed"), []
+    lay.pool.block_table = world.zeros(3, 8, dtype=I32)
+
+    def call(n_seq):
+        z = world.zeros
+        lay.attention(z(n_seq + 1, dtype=I32), z(n_seq, dtype=I64), 5000, z(3, 4, 576))
+        return seen.pop()
+    world.lib.during = lambda ws: None
+    take, lib = world.lib.v4a_latent_attn, world.lib
+    lib.v4a_latent_attn = lambda *a: (seen.append(a[7]._obj), take(*a))[1]
+    first = call(3)
+    assert (first.max_blocks, first.n_pages) == (8, 2)
+    lay.pool.block_table.resize_(3, 5)             # same tensor, same address
+    lay.pool.data.resize_(256, 576)
+    assert lay.pool.block_table.data_ptr() == first.block_table
+    cache = call(3)
+    assert (cache.max_blocks, cache.n_pages) == (5, 1)
+    lay.pool.block_table.resize_(2, 5)
+    with pytest.raises(ValueError):
+        call(3)
+    for bad in (dict(data=world.zeros(512, 575)), dict(data=world.zeros(512, 576, dtype=torch.float32)),
+                dict(data=torch.zeros(512, 576, dtype=BF)), dict(block_table=world.zeros(8, dtype=I32)),
+                dict(block_table=world.zeros(3, 8, dtype=I64)), dict(block_table=world.zeros(8, 3, dtype=I32).t())):
+        kept = lay.pool
+        lay.pool = PagedPool(**dict(dict(data=kept.data, scale=None, block_table=kept.block_table,
+                                         rows_per_block=256), **bad))
+        with pytest.raises(ValueError):
+            call(1)
+        lay.pool = kept
+    lay.gamma = torch.ones(512)                    # on the host
+    with pytest.raises(ValueError):
+        lay.insert(world.zeros(2, dtype=I32), world.zeros(1, dtype=I64), world.zeros(1, 512), world.zeros(1, 64))
+
+
 def test_long_sequences_beside_many_short_units_can_be_split():
     """A 606-token chunk on a short context and one decode token on 100,000 cached ones, 64 heads:
     more units than whole ones need, and one as long as 780 tiles. Splitting it needs a workspace."""
