@@ -18,21 +18,15 @@ Prompts, after a cached prefix or none (expanded form)::
 """
 from __future__ import annotations
 
-from contextlib import nullcontext
 from ctypes import byref
 
 import torch
 
 from . import (BF16, FP32, Cache, LatentCfg, RopeCfg, _check, library)
-from .layer import PagedPool
+from .layer import PagedPool, current_raw as _current_raw, on_stream, scratch
 
 _TYPES = {BF16: torch.bfloat16, FP32: torch.float32}
 _KINDS = {torch.bfloat16: BF16, torch.float32: FP32}
-
-
-# The stream that work goes to now, as a handle (the public call makes a Stream object first).
-_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
-                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _fits(t, dev, dtype, shape):
@@ -79,15 +73,6 @@ def _strides(t):
     return _stride(t, 0), _stride(t, 1)
 
 
-def _on(stream):
-    """Allocations of a call belong to the stream that it runs on (a torch stream or a handle)."""
-    if stream is None:
-        return nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
 def _raw(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -95,20 +80,13 @@ def _raw(stream, dev):
 def _new(shape, dtype, device, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with _on(stream):
+    with on_stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _zeros(shape, dtype, device, stream):
-    with _on(stream):
+    with on_stream(stream):
         return torch.zeros(shape, dtype=dtype, device=device)
-
-
-def _scratch(nbytes, device, stream):
-    """A call's workspace, held until the call has returned. It is the call's own: its kernels
-    meet in it, and calls of another thread, stream or graph may be enqueued among them. The
-    allocator hands the memory on in the stream's order, so a layer keeps none."""
-    return _new((nbytes,), torch.uint8, device, stream) if nbytes else None
 
 
 def _word(dev_err, dev):
@@ -266,7 +244,7 @@ class LatentLayer:
             _need(out, "out", dev, self.dtype, (n, h, self.cfg.latent_dim))
         lib, cfg = library(), byref(self.cfg)
         nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
-        ws = _scratch(nb, q.device, stream)
+        ws = scratch(nb, q.device, stream)
         _check("v4a_latent_attn", lib.v4a_latent_attn(
             cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
             out.data_ptr(), None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
@@ -305,7 +283,7 @@ class LatentLayer:
             _need(out, "out", dev, self.dtype, shape)
         lib, cfg = library(), byref(c)
         nb = lib.v4a_latent_attn_expanded_workspace_size(cfg, n_seq, n_q, n_k)
-        ws = _scratch(nb, q.device, stream)
+        ws = scratch(nb, q.device, stream)
         _check("v4a_latent_attn_expanded", lib.v4a_latent_attn_expanded(
             cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), *_strides(k), k_pe.data_ptr(), _stride(k_pe, 0), v.data_ptr(),

@@ -6,6 +6,7 @@ describing a layer's parameters and pools to the device.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import numpy as np
@@ -22,6 +23,34 @@ from . import (BF16_FP8, C4A, C128A, FP32, IDX_DEFAULT, IDX_FP4, cache, layer_cf
 
 def _t(x, dtype, device):
     return torch.from_numpy(np.ascontiguousarray(x)).to(device=device, dtype=dtype)
+
+
+# The stream that work goes to now, as a handle (the public call makes a Stream object first).
+current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def on_stream(stream):
+    """Allocations of a call belong to the stream that it runs on (a torch stream or a handle)."""
+    if stream is None:
+        return nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def scratch(nbytes, device, stream=None):
+    """A call's workspace, held until the call has returned (None where it needs none). It is the
+    call's own: its kernels meet in it, and calls of another thread, stream or graph may be
+    enqueued among them. The allocator hands the memory on in the stream's order, so a layer
+    keeps none."""
+    if not nbytes:
+        return None
+    handle = getattr(stream, "cuda_stream", stream)
+    if stream is None or handle == current_raw(device.index):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with on_stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 @dataclass
@@ -61,7 +90,6 @@ class Layer:
         self.attn, self.idx, self.swa, self.state = attn, idx, swa, state
         self.top_k = top_k
         self.in_dtype = torch.bfloat16 if cfg.dtype == BF16_FP8 else torch.float32
-        self._ws = {}
 
     @staticmethod
     def from_host(h, device="cuda") -> "Layer":
@@ -86,13 +114,6 @@ class Layer:
         return Layer(self.cfg, self.bias, self.gamma, self.ibias, self.attn.clone(),
                      None if self.idx is None else self.idx.clone(), self.swa.clone(),
                      self.state.clone(), self.top_k)
-
-    def workspace(self, key, nbytes, device) -> torch.Tensor:
-        ws = self._ws.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            self._ws[key] = ws
-        return ws
 
     # -------------------------------------------------------------- library calls
     def compress_insert(self, cu, start, kv, s, ik=None, is_=None, dev_err=None, stream=None):
@@ -121,7 +142,7 @@ class Layer:
         if out is None:
             out = torch.empty((n_q, k), dtype=torch.int32, device=q_seq.device)
         nb = v4a_index_topk_workspace_size(self.cfg, n_q, max_pos)
-        ws = self.workspace("index", nb, q_seq.device)
+        ws = scratch(nb, q_seq.device, stream)
         v4a_index_topk(self.cfg, n_q, q_seq, q_pos, max_pos, q_idx, w, self.idx.c, k, out, ws,
                        dev_err, stream)
         return out
@@ -144,7 +165,7 @@ class Layer:
         k = k if topk is None else topk.shape[1]
         nb = v4a_attn_workspace_size(self.cfg, n_q, max_pos, k if topk is not None else 0,
                                      prefill)
-        ws = self.workspace("attn_p" if prefill else "attn_d", nb, q_seq.device)
+        ws = scratch(nb, q_seq.device, stream)
         fn = v4a_attn_prefill if prefill else v4a_attn_decode
         fn(self.cfg, n_q, q_seq, q_pos, max_pos, q, topk, k, self.attn.c, self.swa.c, out, ws,
            dev_err, stream)
@@ -157,7 +178,7 @@ class Layer:
         codes = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
         scale = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         nb = v4a_attn_q8_workspace_size(self.cfg, n_q, max_pos, k if topk is not None else 0)
-        ws = self.workspace("attn_q8", nb, q_seq.device)
+        ws = scratch(nb, q_seq.device, stream)
         v4a_attn_decode_q8(self.cfg, n_q, q_seq, q_pos, max_pos, q, topk, k, self.attn.c,
                            self.swa.c, codes, scale, ws, dev_err, stream)
         return codes, scale
