@@ -163,6 +163,7 @@ class LatentLayer:
         self.cfg, self.pool, self.gamma = cfg, pool, gamma
         self.dtype = _TYPES[cfg.dtype]
         self.width = cfg.latent_dim + cfg.rope.dim
+        self._desc = None, None
         dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
         if pool is not None:
             _need(pool.data, "pool.data", dev, self.dtype, (None, self.width))
@@ -176,11 +177,19 @@ class LatentLayer:
         if pool is None:
             raise ValueError("this layer has no cache")
         data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
-        n, (b, m) = data.shape[0], bt.shape if bt.dim() == 2 else (0, 0)
-        if not (_fits(data, dev, self.dtype, (n, self.width)) and _fits(bt, dev, torch.int32, (b, m))):
+        shape, table = data.shape, bt.shape
+        if not (data.dtype is self.dtype and bt.dtype is torch.int32 and len(shape) == len(table) == 2
+                and shape[1] == self.width and data.get_device() == dev == bt.get_device()
+                and data.is_contiguous() and bt.is_contiguous()):
             _need(data, "pool.data", dev, self.dtype, (None, self.width))
             _need(bt, "pool.block_table", dev, torch.int32, (None, None))
-        return b, Cache(data.data_ptr(), None, bt.data_ptr(), m, rows, n // rows, self.width, 0)
+        # (the structure is kept for as long as a new one would say the same)
+        key = (data.data_ptr(), bt.data_ptr(), table[1], rows, shape[0])
+        d = self._desc
+        if d[0] != key:
+            d = self._desc = key, Cache(key[0], None, key[1], table[1], rows, shape[0] // rows,
+                                        self.width, 0)
+        return table[0], d[1]
 
     def _batch(self, cu, start):
         """(device, sequences, cache descriptor) of a call over the cache."""

@@ -46,8 +46,7 @@ def scratch(nbytes, device, stream=None):
     keeps none."""
     if not nbytes:
         return None
-    handle = getattr(stream, "cuda_stream", stream)
-    if stream is None or handle == current_raw(device.index):
+    if stream is None or getattr(stream, "cuda_stream", stream) == current_raw(device.index):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with on_stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
