@@ -644,8 +644,9 @@ int launch_rope(const RopeParams& p, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st) {
+  const int sms = sm_count();
   int tokens = kInsertTokens;                    // fewer a block while that leaves SMs without one
-  while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * 152) tokens /= 2;
+  while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * sms) tokens /= 2;
   const dim3 grid((unsigned)((p.n_tokens + (int64_t)tokens - 1) / tokens)), block(32 * kInsertWarps);
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, block, 0, st, p, tokens) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
@@ -657,8 +658,9 @@ int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st
 
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st) {
   // fewer rows a block while that leaves SMs without one
+  const int sms = sm_count();
   int rows = kGatherRows;
-  while (rows > 8 && (int64_t)p.n_rows < (int64_t)rows * 2 * 152) rows /= 2;
+  while (rows > 8 && (int64_t)p.n_rows < (int64_t)rows * 2 * sms) rows /= 2;
   const dim3 grid((unsigned)(((int64_t)p.n_rows + rows - 1) / rows));
   return launch_pdl(latent_gather_kernel, grid, dim3(kGatherThreads), 0, st, p, rows) == cudaSuccess ? V4A_OK
                                                                                                    : V4A_ERR_CUDA;

@@ -112,6 +112,8 @@ struct LatentExpandedParams {
   int32_t* err;
 };
 
+// SMs of the current device (152, a GB300's, where there is none to ask).
+int sm_count();
 int launch_rope(const RopeParams& p, int dtype, cudaStream_t st);
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st);
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);

@@ -8,6 +8,14 @@
 
 using namespace v4a;
 
+int v4a::sm_count() {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+    return v;
+  return 152;
+}
+
 namespace {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -96,14 +104,6 @@ int check_batch(int32_t n_seq, int32_t n, const int32_t* cu, const int64_t* star
   if (n_seq > V4A_MAX_SEQ) return V4A_ERR_UNSUPPORTED;
   if (n == 0 || n_seq == 0) return V4A_OK;
   return cu && start ? V4A_OK : V4A_ERR_ARG;
-}
-
-int sm_count() {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-    return v;
-  return 152;
 }
 
 bool on_tensor_cores(const v4a_latent_cfg* c) {
