@@ -361,7 +361,7 @@ __device__ __forceinline__ void load_row_f(float* dst, const T* src, int n, int 
 // kNV: 32-dim groups of the output. kPaged: absorbed form (V = the row's first dims).
 template <typename T, int kNV, bool kPaged, typename P>
 __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_constant__ P p) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];   // read as float4
   __shared__ int32_t pre[kPaged ? V4A_MAX_SEQ + 1 : 1];
   __shared__ int32_t warp_tot[kGenThreads / 32];
   __shared__ uint8_t kvalid[kGenKeys];
