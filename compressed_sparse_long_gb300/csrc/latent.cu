@@ -432,9 +432,8 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
       const int r = 2 * warp + i;
       if constexpr (kPaged) {
         const int tok = (w.row0 + r - w.seq_row0) / p.H;
-        vis[i] = r < rows ? max((int64_t)0, min(w.start + tok, p.max_pos) + 1) : 0;
-        if (r < rows && lane == 0 && (w.start + tok > p.max_pos || w.start + tok < 0))
-          raise_err(p.err, V4A_DEV_BAD_POS);
+        vis[i] = r < rows ? latent_visible(p, w.start + tok) : 0;
+        if (r < rows && lane == 0) latent_report_pos(p, w.start + tok);
       } else {
         vis[i] = r >= rows ? 0 : p.causal ? max(0, nk - nq + seq + r + 1) : nk;
       }

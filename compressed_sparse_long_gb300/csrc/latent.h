@@ -79,6 +79,7 @@ struct LatentAttnParams {
   int32_t n_seq, n_tokens, H, C, R;   // R = rotary dims
   float scale;
   int64_t max_pos;
+  int64_t end;                        // no key is at or behind it: max_pos + 1 and the table's reach
   const int32_t* cu;
   const int64_t* start;
   const void* q;
@@ -160,14 +161,24 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b
   s.rows = n * p.H;
   s.start = __ldg(p.start + b);
   s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
-  const int64_t keys = min(s.start + n, p.max_pos + 1);
+  const int64_t keys = min(s.start + n, p.end);
   s.tiles = !split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
   return s;
 }
 
-// Keys that token i of a sequence sees (0 for a position below 0, capped at max_pos + 1).
+// Keys that a token at pos sees (0 for a position below 0).
+__device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, int64_t pos) {
+  return max((int64_t)0, min(pos, p.end - 1) + 1);
+}
+// What is to be reported of a token's position. (Positions that the block table does not reach are
+// blocks without a page; only the table's are walked.)
+__device__ __forceinline__ void latent_report_pos(const LatentAttnParams& p, int64_t pos) {
+  if (pos > p.max_pos || pos < 0) raise_err(p.err, V4A_DEV_BAD_POS);
+  if (min(pos, p.max_pos) >= p.end) raise_err(p.err, V4A_DEV_MISSING_PAGE);
+}
+// The same for token i of a sequence.
 __device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, const LatentSeq& s, int i) {
-  return max((int64_t)0, min(s.start + i, p.max_pos) + 1);
+  return latent_visible(p, s.start + i);
 }
 
 // Exclusive prefix sums of weight(b) over the sequences into pre[0 .. n_seq] (shared memory),

@@ -299,6 +299,8 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, 
   p.R = cfg->rope.dim;
   p.scale = cfg->softmax_scale;
   p.max_pos = max_pos;
+  const int64_t reach = (int64_t)cache->max_blocks * kBlock;
+  p.end = max_pos + 1 < reach ? max_pos + 1 : reach;
   p.cu = cu_tokens;
   p.start = start_pos;
   p.q = q;

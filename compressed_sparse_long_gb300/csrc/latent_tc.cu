@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t vis = 0;
       if (my_row < w.rows) {
         const int64_t pos = w.start + (w.row0 + my_row - w.seq_row0) / p.H;
-        vis = max((int64_t)0, min(pos, p.max_pos) + 1);
-        if (quad == 0 && (pos > p.max_pos || pos < 0)) raise_err(p.err, V4A_DEV_BAD_POS);
+        vis = latent_visible(p, pos);
+        if (quad == 0) latent_report_pos(p, pos);
       }
       // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
       // row that sees nothing (or is none) infinity

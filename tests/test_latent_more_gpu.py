@@ -1,5 +1,6 @@
-"""GPU: gradients of the rotation and far positions, and latent attention at the ends of its ranges: large and small
-values, lengths that differ widely. Tolerances as in latent_helpers."""
+"""GPU: the rotation's gradients and far positions, and latent attention at the ends of its ranges:
+large and small values, lengths that differ widely, positions past the block table. Tolerances as
+in latent_helpers."""
 import decimal
 import math
 
@@ -9,10 +10,10 @@ import torch
 
 import compressed_sparse_long_gb300 as v4a
 from compressed_sparse_long_gb300.latent import LatentLayer, rope
-from latent_helpers import (BF, F32, attn_tolerance, batch, check, f64, half_step, ints, layer,
-                            logit_bound, rand)
+from latent_helpers import (BF, F32, attn_tolerance, batch, check, err_word, f64, half_step, ints,
+                            layer, logit_bound, rand)
 from oracle import latent_oracle as O
-from test_latent_gpu import _attn, _rope_case, _rope_tol
+from test_latent_gpu import _attn, _expanded, _rope_case, _rope_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -244,6 +245,16 @@ def test_many_units_beside_long_ones(dtype, heads, latent, dim, total, new):
         check(got, ref, tol)
 
 
+def test_expanded_items_over_many_pairs_of_ctas():
+    """One head and 5,000 keys: an item's 40 key tiles fall to more pairs than a warp has lanes."""
+    rng = np.random.default_rng(50)
+    cfg = v4a.latent_cfg(v4a.BF16, 1, 512, v4a.rope_cfg(64))
+    for nq in (1, 300, 513):
+        q, kv, pe = rand(rng, BF, nq, 1, 192), rand(rng, BF, 5000, 1, 256), rand(rng, BF, 5000, 64)
+        got, ref, tol = _expanded(cfg, [0, nq], [0, 5000], q, kv[..., :128], pe, kv[..., 128:])
+        check(got, ref, tol)
+
+
 def test_a_sequence_alone_and_in_a_batch():
     """The others in a batch move the cuts along the keys, and with them the order of sums, but
     nothing else: each sequence alone is within the definition's bounds of itself in the batch."""
@@ -261,3 +272,28 @@ def test_a_sequence_alone_and_in_a_batch():
         one = lay.attention(ints([0, new[b]], torch.int32), ints(start[b:b + 1], torch.int64),
                             total[b] - 1, q[part].contiguous())
         check(one, f64(got)[part], 2 * tol[part])        # either is within tol of the definition
+
+
+@pytest.mark.parametrize("dtype,heads", [(BF, 64), (BF, 16), (F32, 4)])
+def test_positions_past_the_block_table(dtype, heads):
+    """Keys that the table does not reach are left out like any block without a page, and not
+    walked: a call whose positions run into the billions takes no longer than its table."""
+    rng = np.random.default_rng(49)
+    total, new = [500, 700], [1, 2]
+    lay, bt = layer(rng, dtype, heads, total)
+    q = rand(rng, dtype, 3, heads, 576)
+    got, ref, tol, flags = _attn(lay, bt, total, new, q, start=[4000, 699], max_pos=4500)
+    assert flags == v4a.DEV_MISSING_PAGE
+    check(got, ref, tol)
+    cu = ints([0, 1, 3], torch.int32)
+    for start, max_pos, want in (([1 << 31, (1 << 31) - 7], 1 << 32, v4a.DEV_MISSING_PAGE),
+                                 ([(1 << 63) - 9, 1 << 31], 1 << 32, v4a.DEV_MISSING_PAGE | v4a.DEV_BAD_POS)):
+        e = err_word()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        far = lay.attention(cu, ints(start, torch.int64), max_pos, q, dev_err=e)
+        b.record()
+        assert v4a.v4a_get_error(e) == want
+        near, ref, tol, _ = _attn(lay, bt, total, new, q, start=[767, 767], max_pos=767)
+        check(far, ref, tol)                         # every key of either table
+        assert a.elapsed_time(b) < 1000              # (tiles of 2^31 keys would take half a minute)
