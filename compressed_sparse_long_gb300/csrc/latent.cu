@@ -328,7 +328,10 @@ __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __g
 // A unit of 16 query rows against tiles of 32 keys, in fp32. Warp w holds rows 2w, 2w + 1;
 // lane x computes their products with key x of the tile (the key tile's rows are padded by one
 // word, so the lanes' reads fall in different banks), the softmax statistics go by shuffles,
-// and lane l accumulates output dims l, l + 32, .. . Bound: shared-memory reads and fp32 FMA.
+// and lane l accumulates output dims l, l + 32, .. . Bound: shared-memory reads (a word a product)
+// and fp32 FMA: absorbed 14-17 TFLOP/s with 512 or 256 latent dims (8 sequences x 8,192 tokens, 64
+// heads, 512 + 64, fp32: 538 us), 6 with 128; expanded 5-9 (2,048-token prompt, 16 heads, fp32,
+// 128 + 64 / 128: 2.5 ms). The tensor-core kernels take 33 and 44 us at these sizes.
 constexpr int kGenRows = 16, kGenKeys = 32, kGenThreads = 256;
 
 struct RowState {
@@ -464,9 +467,11 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
           if constexpr (kPaged) {
             load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.cache.data) + g * (int64_t)DK, DK, lane);
           } else {
-            load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.k) + g * p.k_ts + (int64_t)head * p.k_hs, p.DN, lane);
+            const T* key = reinterpret_cast<const T*>(p.k) + g * p.k_ts + (int64_t)head * p.k_hs;
+            const T* value = reinterpret_cast<const T*>(p.v) + g * p.v_ts + (int64_t)head * p.v_hs;
+            load_row_f<T>(ks + k * KS, key, p.DN, lane);
             load_row_f<T>(ks + k * KS + p.DN, reinterpret_cast<const T*>(p.k_pe) + g * p.pe_ts, p.DR, lane);
-            load_row_f<T>(vs + k * VS, reinterpret_cast<const T*>(p.v) + g * p.v_ts + (int64_t)head * p.v_hs, DV, lane);
+            load_row_f<T>(vs + k * VS, value, DV, lane);
           }
         } else {
           for (int d = lane; d < DK; d += 32) ks[k * KS + d] = 0.f;

@@ -238,7 +238,8 @@ __device__ __forceinline__ bool latent_split(const LatentAttnParams& p, int32_t*
     atomicMax(warp_tot + 2, longest);
   }
   __syncthreads();
-  const bool split = 2 * (int64_t)warp_tot[0] + (int64_t)warp_tot[2] * p.plan.split_ctas > 2 * (int64_t)warp_tot[1];
+  const int64_t whole2 = 2 * (int64_t)warp_tot[0] + (int64_t)warp_tot[2] * p.plan.split_ctas;
+  const bool split = whole2 > 2 * (int64_t)warp_tot[1];
   __syncthreads();
   return split;
 }

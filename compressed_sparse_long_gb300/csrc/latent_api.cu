@@ -151,9 +151,10 @@ size_t part_bytes(const v4a_latent_cfg* c, const LatentPlan& pl, size_t* ml_at, 
 }
 
 // Steps that starting an item counts for when the line is cut into equal parts. Its copies, first
-// logits and output take about two; counting four evens out the pairs that get many short items:
-// 8192-token prompt, 64 heads (long runs): 1190 us with 0, 973 with 2, 910 with 4, 916 with 6;
-// ragged chunks 220, 224, 228 and 239 us, before rows without a query were kept off the masked path.
+// logits and output take about two; counting more evens out the pairs that get many short items.
+// us on the device with 0, 2, 4 and 6: 8,192-token prompt, 64 heads 1159, 975, 861, 880; 4,096
+// tokens, 32 heads 211, 169, 162, 160; five ragged chunks, 16 heads 337, 307, 288, 279; four, 32
+// heads 213, 161, 156, 154; four, 8 heads 123, 96, 83, 85.
 constexpr int kExpandedSetup = 4;
 
 // The plan of an expanded call (p->tc, pairs, split) and its workspace. False when there are

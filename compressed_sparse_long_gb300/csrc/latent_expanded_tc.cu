@@ -16,12 +16,13 @@
 //
 // Bound: the tensor pipe (40 products a step of 512 queries x 128 keys, 2560 cycles; a step takes
 // 3050, a tile's chain of S, softmax and P V being a little longer) and, in long runs, the power
-// it draws: that prompt takes 832 us (1.65 PFLOP/s) in a short run and 910-920 in a long one.
+// it draws: that prompt takes 850-930 us in runs of milliseconds and 920-945 (1.45-1.5 PFLOP/s) in
+// longer ones.
 //
 // All (item, key tile) steps form one line, a sequence's blocks from the last (the longest, when
 // causal) to the first, heads within a block; each pair takes an equal part of it. An item whose
 // tiles fall to several pairs is left as partial results that a second kernel merges: without
-// that, a long sequence's few items would decide the time (ragged chunks 391 us, now 184).
+// that, a long sequence's few items would decide the time (ragged chunks 391 us, now 190).
 //
 // Roles in each CTA: warps 0-7 softmax and output (tile 0 / 1), warp 8 copies, warp 11 watches
 // the copies land and reports to the CTA of rank 0, whose warp 9 issues the pair's products.
@@ -114,12 +115,12 @@ constexpr uint32_t kTmemCols = 512;
 
 // Softmax of a query's key tiles t0 .. t1 - 1 (t1 <= t0: none). S of a tile appears in tensor
 // memory at scol (sfull), P is written over it (arrive_p). A query sees the first `seen` keys (a
-// thread without a query, row false, must not hold up its warp); g counts steps. Weights are taken against the reference m, and l is their sum. False when a wait
-// gave up.
+// thread without a query, row false, must not hold up its warp); g counts steps. Weights are taken
+// against the reference m, and l is their sum. False when a wait gave up.
 template <typename ArriveP>
-__device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int t0, int t1, int seen, bool row, uint32_t scol,
-                                              uint32_t ocol, uint64_t* sfull, int& g, float& m, float& l,
-                                              volatile int* abort_flag, ArriveP arrive_p) {
+__device__ __forceinline__ bool softmax_steps(const LatentExpandedParams& p, int t0, int t1, int seen, bool row,
+                                              uint32_t scol, uint32_t ocol, uint64_t* sfull, int& g, float& m,
+                                              float& l, volatile int* abort_flag, ArriveP arrive_p) {
   const float k2 = p.scale * kLog2e;
   const uint64_t k22 = pack2(k2, k2);
   m = -INFINITY;
@@ -221,8 +222,8 @@ struct Seq {
     const int seen = p.causal ? max(0, min(nk, nk - nq + last + 1)) : nk;
     return max(1, (seen + kT - 1) / kT);
   }
-  // Steps of one head, p.setup a block included (what starting an item is worth): the last block, and before it blocks whose tiles
-  // fall by kItem / kT each until they reach one.
+  // Steps of one head, p.setup a block included (what starting an item is worth): the last block,
+  // and before it blocks whose tiles fall by kItem / kT each until they reach one.
   __device__ __forceinline__ int steps(const LatentExpandedParams& p) const {
     if (blocks == 0) return 0;
     const int last = tiles(p, blocks - 1), full = blocks - 1;

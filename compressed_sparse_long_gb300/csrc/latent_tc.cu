@@ -15,9 +15,10 @@
 // Bound: HBM for decode with up to 64 heads (1152 bytes a key for 2 * 64 * 1088 flop); for 128
 // heads and chunks the operands' shared-memory reads: an M = 128, N = 64 product reads 6 KB and
 // takes 54 (O^T) to 60 (S^T) cycles where the pipe would need 32. A tile then takes 5400 cycles:
-// S^T 2160, softmax 930 with 560 of signalling, O^T 1730. (One CTA cannot take 128 rows: O^T would
-// fill the tensor memory.) 32 sequences x 32768 tokens, 64 heads: 196 us with the merge, 6.2 TB/s;
-// 16 sequences of 4616-108051 tokens, 128 heads: 194 us, 835 TFLOP/s.
+// S^T 2160, softmax 930 with 560 of signalling, O^T 1730 (clock marks in a copy of the kernel).
+// (One CTA cannot take 128 rows: O^T would fill the tensor memory.) 32 sequences x 32768 tokens, 64
+// heads: 197 us with the merge, 6.1 TB/s; 16 sequences of 4616-108051 tokens, 128 heads: 195 us,
+// 830 TFLOP/s.
 //
 // Warps 0-7: softmax and output. A thread holds one key's 32 logits (warps 0-3 rows 0-31, warps
 // 4-7 rows 32-63 of the unit). A row's weights are taken against a reference, 2^16 times its

@@ -112,8 +112,9 @@ def _rope(cfg, x, pos, out, inverse, dev_err, stream, new=_new):
     heads, xh, oh = (1, 0, 0) if len(shape) == 2 else (shape[1], _stride(x, 1), _stride(out, 1))
     _check("v4a_rope", library().v4a_rope(
         byref(cfg), kind, shape[0], heads, pos.data_ptr(), x.data_ptr(), _stride(x, 0),
-        xh, out.data_ptr(), _stride(out, 0), oh, inverse, None if dev_err is None else _word(dev_err, dev),
-            _current_raw(dev) if stream is None else _raw(stream, dev)))
+        xh, out.data_ptr(), _stride(out, 0), oh, inverse,
+        None if dev_err is None else _word(dev_err, dev),
+        _current_raw(dev) if stream is None else _raw(stream, dev)))
     return out
 
 
@@ -178,8 +179,9 @@ class LatentLayer:
             raise ValueError("this layer has no cache")
         data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
         shape, table = data.shape, bt.shape
-        if not (data.dtype is self.dtype and bt.dtype is torch.int32 and len(shape) == len(table) == 2
-                and shape[1] == self.width and data.get_device() == dev == bt.get_device()
+        if not (data.dtype is self.dtype and bt.dtype is torch.int32
+                and len(shape) == len(table) == 2 and shape[1] == self.width
+                and data.get_device() == dev == bt.get_device()
                 and data.is_contiguous() and bt.is_contiguous()):
             _need(data, "pool.data", dev, self.dtype, (None, self.width))
             _need(bt, "pool.block_table", dev, torch.int32, (None, None))
@@ -215,12 +217,13 @@ class LatentLayer:
                 and _rows(k_pe, dev, self.dtype, (n, self.cfg.rope.dim))):
             _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
             _need(k_pe, "k_pe", dev, self.dtype, (n, self.cfg.rope.dim), contiguous=False)
-        if self.gamma is not None and not _fits(self.gamma, dev, torch.float32, (self.cfg.latent_dim,)):
-            _need(self.gamma, "gamma", dev, torch.float32, (self.cfg.latent_dim,))
+        gamma, shape = self.gamma, (self.cfg.latent_dim,)
+        if gamma is not None and not _fits(gamma, dev, torch.float32, shape):
+            _need(gamma, "gamma", dev, torch.float32, shape)
         _check("v4a_latent_insert", library().v4a_latent_insert(
             byref(self.cfg), n_seq, n, cu.data_ptr(), start.data_ptr(), c.data_ptr(),
             _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),
-            None if self.gamma is None else self.gamma.data_ptr(), byref(cache),
+            None if gamma is None else gamma.data_ptr(), byref(cache),
             None if dev_err is None else _word(dev_err, dev),
             _current_raw(dev) if stream is None else _raw(stream, dev)))
 
@@ -256,7 +259,8 @@ class LatentLayer:
         ws = scratch(nb, q.device, stream)
         _check("v4a_latent_attn", lib.v4a_latent_attn(
             cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
-            out.data_ptr(), None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
+            out.data_ptr(), None if ws is None else ws.data_ptr(), nb,
+            None if dev_err is None else _word(dev_err, dev),
             _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
@@ -297,7 +301,8 @@ class LatentLayer:
             cfg, n_seq, n_q, cu_q.data_ptr(), n_k, cu_k.data_ptr(), q.data_ptr(),
             k.data_ptr(), *_strides(k), k_pe.data_ptr(), _stride(k_pe, 0), v.data_ptr(),
             *_strides(v), causal, out.data_ptr(),
-            None if ws is None else ws.data_ptr(), nb, None if dev_err is None else _word(dev_err, dev),
+            None if ws is None else ws.data_ptr(), nb,
+            None if dev_err is None else _word(dev_err, dev),
             _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
