@@ -198,8 +198,12 @@ class LatentLayer:
         dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
         known, cache = self._describe(dev)
         n_seq = cu.numel() - 1 if isinstance(cu, torch.Tensor) else -1
-        if n_seq < 0 or not (_fits(cu, dev, torch.int32, (n_seq + 1,))
-                             and _fits(start, dev, torch.int64, (n_seq,))):
+        # (_fits of both, written out)
+        if n_seq < 0 or not (isinstance(start, torch.Tensor)
+                             and cu.dtype is torch.int32 and start.dtype is torch.int64
+                             and cu.dim() == 1 and start.shape == (n_seq,)
+                             and cu.get_device() == dev == start.get_device()
+                             and cu.is_contiguous() and start.is_contiguous()):
             _need(cu, "cu", dev, torch.int32, (None,))
             if n_seq < 0:
                 raise ValueError("cu: expected the sequences' first rows and the end")
@@ -213,17 +217,16 @@ class LatentLayer:
         be strided: two slices of one projection's output)."""
         dev, n_seq, cache = self._batch(cu, start)
         n = c.shape[0] if isinstance(c, torch.Tensor) and c.dim() else 0
-        if not (_rows(c, dev, self.dtype, (n, self.cfg.latent_dim))
-                and _rows(k_pe, dev, self.dtype, (n, self.cfg.rope.dim))):
-            _need(c, "c", dev, self.dtype, (None, self.cfg.latent_dim), contiguous=False)
-            _need(k_pe, "k_pe", dev, self.dtype, (n, self.cfg.rope.dim), contiguous=False)
-        gamma, shape = self.gamma, (self.cfg.latent_dim,)
-        if gamma is not None and not _fits(gamma, dev, torch.float32, shape):
-            _need(gamma, "gamma", dev, torch.float32, shape)
+        dc, dr, gamma = self.cfg.latent_dim, self.cfg.rope.dim, self.gamma
+        if not (_rows(c, dev, self.dtype, (n, dc)) and _rows(k_pe, dev, self.dtype, (n, dr))):
+            _need(c, "c", dev, self.dtype, (None, dc), contiguous=False)
+            _need(k_pe, "k_pe", dev, self.dtype, (n, dr), contiguous=False)
+        if gamma is not None and not _fits(gamma, dev, torch.float32, (dc,)):
+            _need(gamma, "gamma", dev, torch.float32, (dc,))
+        cs, ks = (c.stride(0), k_pe.stride(0)) if n > 1 else (dc, dr)
         _check("v4a_latent_insert", library().v4a_latent_insert(
             byref(self.cfg), n_seq, n, cu.data_ptr(), start.data_ptr(), c.data_ptr(),
-            _stride(c, 0), k_pe.data_ptr(), _stride(k_pe, 0),
-            None if gamma is None else gamma.data_ptr(), byref(cache),
+            cs, k_pe.data_ptr(), ks, None if gamma is None else gamma.data_ptr(), byref(cache),
             None if dev_err is None else _word(dev_err, dev),
             _current_raw(dev) if stream is None else _raw(stream, dev)))
 
