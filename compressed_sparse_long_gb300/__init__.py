@@ -23,9 +23,13 @@ __all__ = [
     "RopeCfg", "LatentCfg", "rope_cfg", "latent_cfg", "v4a_rope", "v4a_latent_insert",
     "v4a_latent_gather", "v4a_latent_attn", "v4a_latent_attn_workspace_size",
     "v4a_latent_attn_expanded", "v4a_latent_attn_expanded_workspace_size",
+    "v4a_latent_attn_window", "v4a_latent_attn_window_workspace_size",
+    "PageTableDesc", "Pool", "v4a_pages_workspace_size", "v4a_pages_free", "v4a_pages_grow",
+    "v4a_pages_fork", "v4a_pages_copy", "v4a_pages_compact",
     "v4a_get_error", "v4a_version",
     "BF16", "ROPE_INTERLEAVED", "ROPE_HALF", "ROPE_SCALE_NONE", "ROPE_SCALE_LINEAR",
-    "ROPE_SCALE_BY_PARTS", "ROPE_SCALE_YARN", "MAX_SEQ",
+    "ROPE_SCALE_BY_PARTS", "ROPE_SCALE_YARN", "MAX_SEQ", "LATENT_PLAIN", "LATENT_FP4", "MAX_POOLS",
+    "DEV_NO_PAGE", "latent_row_bytes",
     "C4A", "C128A", "FP32", "BF16_FP8", "IDX_DEFAULT", "IDX_FP4", "DEV_MISSING_PAGE", "DEV_BAD_PAGE", "DEV_BAD_INDEX", "DEV_BAD_POS",
 ]
 
@@ -35,10 +39,12 @@ C4A, C128A = 0, 1
 FP32, BF16_FP8, BF16 = 0, 1, 2
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BY_PARTS, ROPE_SCALE_YARN = 0, 1, 2, 3
-MAX_SEQ = 1024
+MAX_SEQ, MAX_POOLS = 1024, 64
+LATENT_PLAIN, LATENT_FP4 = 0, 1
 IDX_DEFAULT, IDX_FP4 = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE, ERR_TOO_LARGE = 0, -1, -2, -3, -4, -5
 DEV_MISSING_PAGE, DEV_BAD_PAGE, DEV_BAD_INDEX, DEV_BAD_POS = 1, 2, 4, 8
+DEV_NO_PAGE = 32
 _NAMES = {ERR_ARG: "V4A_ERR_ARG", ERR_UNSUPPORTED: "V4A_ERR_UNSUPPORTED",
           ERR_CUDA: "V4A_ERR_CUDA", ERR_DEVICE: "V4A_ERR_DEVICE",
           ERR_TOO_LARGE: "V4A_ERR_TOO_LARGE"}
@@ -80,15 +86,28 @@ class RopeCfg(ctypes.Structure):
 class LatentCfg(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
                 ("latent_dim", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
-                ("v_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("cache_format", ctypes.c_int32),
                 ("rms_eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
                 ("rope", RopeCfg)]
+
+
+class PageTableDesc(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("row_bytes", ctypes.c_int64), ("rows_per_block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFG, _CACHE = ctypes.POINTER(LayerCfg), ctypes.POINTER(Cache)
 _ROPE, _LATENT = ctypes.POINTER(RopeCfg), ctypes.POINTER(LatentCfg)
+_TABLE, _POOLS = ctypes.POINTER(PageTableDesc), ctypes.POINTER(Pool)
 
 _SIGS = {
     "v4a_version": (_I32, []),
@@ -125,6 +144,15 @@ _SIGS = {
     "v4a_latent_attn_workspace_size": (_SZ, [_LATENT, _I32, _I32, _I64]),
     "v4a_latent_attn": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _P, _I64, _P, _CACHE, _P, _P, _SZ,
                                        _P, _P]),
+    "v4a_latent_attn_window_workspace_size": (_SZ, [_LATENT, _I32, _I32, _I64, _I64, _I64]),
+    "v4a_latent_attn_window": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _P, _I64, _I64, _I64, _P,
+                                              _CACHE, _P, _P, _SZ, _P, _P]),
+    "v4a_pages_workspace_size": (_SZ, [_TABLE]),
+    "v4a_pages_free": (ctypes.c_int, [_TABLE, _P, _P, _P, _P]),
+    "v4a_pages_grow": (ctypes.c_int, [_TABLE, _P, _P, _P, _SZ, _P, _P]),
+    "v4a_pages_fork": (ctypes.c_int, [_TABLE, _POOLS, _I32, _I32, _P, _P, _P, _P, _SZ, _P, _P]),
+    "v4a_pages_copy": (ctypes.c_int, [_TABLE, _POOLS, _I32, _I32, _P, _P, _P, _P]),
+    "v4a_pages_compact": (ctypes.c_int, [_TABLE, _POOLS, _I32, _P, _P, _P, _SZ, _P, _P]),
     "v4a_latent_attn_expanded": (ctypes.c_int, [_LATENT, _I32, _I32, _P, _I32, _P, _P, _P, _I64,
                                                 _I64, _P, _I64, _P, _I64, _I64, _I32, _P, _P,
                                                 _SZ, _P, _P]),
@@ -317,11 +345,19 @@ def rope_cfg(dim: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0,
 
 
 def latent_cfg(dtype: int, n_heads: int, latent_dim: int, rope: RopeCfg, nope_dim: int = 128,
-               v_dim: int = 128, rms_eps: float = 1e-6,
-               softmax_scale: float | None = None) -> LatentCfg:
-    """A latent-attention layer; the softmax scale defaults to the expanded key's width ^ -1/2."""
-    return LatentCfg(dtype, n_heads, latent_dim, nope_dim, v_dim, 0, rms_eps,
+               v_dim: int = 128, rms_eps: float = 1e-6, softmax_scale: float | None = None,
+               cache_format: int = LATENT_PLAIN) -> LatentCfg:
+    """A latent-attention layer; the softmax scale defaults to the expanded key's width ^ -1/2.
+    cache_format: LATENT_PLAIN, or LATENT_FP4 for a cache in 4 bits (see include/v4a.h)."""
+    return LatentCfg(dtype, n_heads, latent_dim, nope_dim, v_dim, cache_format, rms_eps,
                      softmax_scale if softmax_scale else (nope_dim + rope.dim) ** -0.5, rope)
+
+
+def latent_row_bytes(cfg: LatentCfg) -> int:
+    """Bytes of a row of the layer's pool (an FP4 row's scale besides)."""
+    if cfg.cache_format == LATENT_FP4:
+        return -(-(cfg.latent_dim // 2 + 2 * cfg.rope.dim + cfg.latent_dim // 16) // 16) * 16
+    return (cfg.latent_dim + cfg.rope.dim) * (2 if cfg.dtype == BF16 else 4)
 
 
 def v4a_rope(rope, dtype, n_tokens, n_heads, pos, x, x_token_stride, x_head_stride, y,
@@ -359,6 +395,20 @@ def v4a_latent_attn(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, q, cach
         _stream(stream)))
 
 
+def v4a_latent_attn_window_workspace_size(cfg, n_seq, n_tokens, max_pos, window, sinks) -> int:
+    return library().v4a_latent_attn_window_workspace_size(ctypes.byref(cfg), n_seq, n_tokens,
+                                                           max_pos, window, sinks)
+
+
+def v4a_latent_attn_window(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, window, sinks, q,
+                           cache, out, workspace, dev_err=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("v4a_latent_attn_window", library().v4a_latent_attn_window(
+        ctypes.byref(cfg), n_seq, n_tokens, _ptr(cu_tokens), _ptr(start_pos), max_pos, window,
+        sinks, _ptr(q), ctypes.byref(cache), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_err),
+        _stream(stream)))
+
+
 def v4a_latent_attn_expanded(cfg, n_seq, n_q, cu_q, n_k, cu_k, q, k, k_token_stride,
                              k_head_stride, k_pe, k_pe_stride, v, v_token_stride, v_head_stride,
                              causal, out, workspace, dev_err=None, stream=None):
@@ -372,6 +422,48 @@ def v4a_latent_attn_expanded(cfg, n_seq, n_q, cu_q, n_k, cu_k, q, k, k_token_str
 
 def v4a_latent_attn_expanded_workspace_size(cfg, n_seq, n_q, n_k) -> int:
     return library().v4a_latent_attn_expanded_workspace_size(ctypes.byref(cfg), n_seq, n_q, n_k)
+
+
+def _pools(pools):
+    return (Pool * len(pools))(*pools) if pools else None
+
+
+def _bytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def v4a_pages_workspace_size(table) -> int:
+    return library().v4a_pages_workspace_size(ctypes.byref(table))
+
+
+def v4a_pages_free(table, first, last, dev_err=None, stream=None):
+    _check("v4a_pages_free", library().v4a_pages_free(
+        ctypes.byref(table), _ptr(first), _ptr(last), _ptr(dev_err), _stream(stream)))
+
+
+def v4a_pages_grow(table, first, last, workspace, dev_err=None, stream=None):
+    _check("v4a_pages_grow", library().v4a_pages_grow(
+        ctypes.byref(table), _ptr(first), _ptr(last), _ptr(workspace), _bytes(workspace),
+        _ptr(dev_err), _stream(stream)))
+
+
+def v4a_pages_fork(table, pools, n, src, dst, length, workspace, dev_err=None, stream=None):
+    """pools: a sequence of Pool."""
+    _check("v4a_pages_fork", library().v4a_pages_fork(
+        ctypes.byref(table), _pools(pools), len(pools), n, _ptr(src), _ptr(dst), _ptr(length),
+        _ptr(workspace), _bytes(workspace), _ptr(dev_err), _stream(stream)))
+
+
+def v4a_pages_copy(table, pools, n, src, dst, dev_err=None, stream=None):
+    _check("v4a_pages_copy", library().v4a_pages_copy(
+        ctypes.byref(table), _pools(pools), len(pools), n, _ptr(src), _ptr(dst), _ptr(dev_err),
+        _stream(stream)))
+
+
+def v4a_pages_compact(table, pools, n_used, moved, workspace, dev_err=None, stream=None):
+    _check("v4a_pages_compact", library().v4a_pages_compact(
+        ctypes.byref(table), _pools(pools), len(pools), _ptr(n_used), _ptr(moved),
+        _ptr(workspace), _bytes(workspace), _ptr(dev_err), _stream(stream)))
 
 
 def v4a_get_error(dev_err, stream=None) -> int:

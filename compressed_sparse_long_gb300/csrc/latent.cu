@@ -17,46 +17,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A kernel parameter array read with an index of each thread's own: through its address, as
-// ordinary memory. (From the constant bank the lanes' different words come one at a time.)
-__device__ __forceinline__ const float* by_address(const float* v) {
-  const float* q;
-  asm volatile("mov.b64 %0, %1;" : "=l"(q) : "l"(v));
-  return q;
-}
-
 // ------------------------------------------------------------------------------- rope
 // Bound: HBM for many tokens (8192 x 64 heads x 64 dims fp32: 44 us, 6.1 TB/s), latency for few
 // (4.3 us). A thread takes `VEC` consecutive elements of
 // each half (half layout) or 2 VEC consecutive ones (interleaved): VEC pairs. The block's
 // tokens' cosines and sines are computed once, into shared memory, for all heads.
-template <typename T, int N> struct Pack { T v[N]; };
-template <typename T, int N>
-__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
-  if constexpr (N * sizeof(T) == 16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(p[i]);
-  }
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
-  if constexpr (N * sizeof(T) == 16) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = Elem<T>::from_f(f[i]);
-    *reinterpret_cast<uint4*>(p) = u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = Elem<T>::from_f(f[i]);
-  }
-}
-
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 2048;   // cosine/sine pairs of a block's tokens
 
@@ -361,8 +326,23 @@ __device__ __forceinline__ void load_row_f(float* dst, const T* src, int n, int 
   }
 }
 
-// kNV: 32-dim groups of the output. kPaged: absorbed form (V = the row's first dims).
-template <typename T, int kNV, bool kPaged, typename P>
+// The same of an FP4 row, as the values that it stands for: a lane a block of 16.
+__device__ __forceinline__ void load_row_fp4(float* dst, const LatentAttnParams& p, int64_t slot, int lane) {
+  const uint8_t* row = reinterpret_cast<const uint8_t*>(p.cache.data) + slot * p.cache.width;
+  const float scale = __ldg(p.cache.scale + slot);
+  for (int b = lane; b < p.C / 16; b += 32) {
+    float f[16];
+    fp4_block(row, p.C, p.R, b, scale, f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) dst[16 * b + k] = f[k];
+  }
+  const __half* h = reinterpret_cast<const __half*>(row + p.C / 2);
+  for (int d = lane; d < p.R; d += 32) dst[p.C + d] = scale * __half2float(h[d]);
+}
+
+// kNV: 32-dim groups of the output. kPaged: absorbed form (V = the row's first dims), kFp4: of an
+// FP4 cache.
+template <typename T, int kNV, bool kPaged, bool kFp4, typename P>
 __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_constant__ P p) {
   extern __shared__ __align__(16) float sm[];   // read as float4
   __shared__ int32_t pre[kPaged ? V4A_MAX_SEQ + 1 : 1];
@@ -427,7 +407,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
       if (r < rows) load_row_f<T>(qs + r * DK, reinterpret_cast<const T*>(p.q) + row * DK, DK, lane);
       else for (int d = lane; d < DK; d += 32) qs[r * DK + d] = 0.f;
     }
-    int64_t vis[2];
+    int64_t vis[2], from[2] = {0, 0}, sinks = 0;   // a row sees [0, sinks) and [from, vis)
     RowState st[2];
     float o[2][kNV];
 #pragma unroll
@@ -437,6 +417,10 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
         const int tok = (w.row0 + r - w.seq_row0) / p.H;
         vis[i] = r < rows ? latent_visible(p, w.start + tok) : 0;
         if (r < rows && lane == 0) latent_report_pos(p, w.start + tok);
+        if (p.window > 0) {
+          from[i] = latent_from(p, w.start + tok);
+          sinks = p.sinks;
+        }
       } else {
         vis[i] = r >= rows ? 0 : p.causal ? max(0, nk - nq + seq + r + 1) : nk;
       }
@@ -445,8 +429,10 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
 #pragma unroll
       for (int d = 0; d < kNV; ++d) o[i][d] = 0.f;
     }
+    auto sees = [&](int i, int64_t x) { return x < vis[i] && (x >= from[i] || x < sinks); };
     for (int t = t0; t < t1; ++t) {
-      const int64_t x0 = (int64_t)t * kGenKeys;
+      int64_t x0 = (int64_t)t * kGenKeys;
+      if constexpr (kPaged) x0 = w.tile_at<true>(t) * kGenKeys;
       __syncthreads();
       // lane k resolves key k's row; a warp then copies four rows
       int64_t at = -1;
@@ -464,7 +450,9 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
         const int k = warp * (kGenKeys / 8) + i;
         const int64_t g = __shfl_sync(0xffffffffu, at, k);
         if (g >= 0) {
-          if constexpr (kPaged) {
+          if constexpr (kPaged && kFp4) {
+            load_row_fp4(ks + k * KS, p, g, lane);
+          } else if constexpr (kPaged) {
             load_row_f<T>(ks + k * KS, reinterpret_cast<const T*>(p.cache.data) + g * (int64_t)DK, DK, lane);
           } else {
             const T* key = reinterpret_cast<const T*>(p.k) + g * p.k_ts + (int64_t)head * p.k_hs;
@@ -492,8 +480,8 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
       }
       const float k2e = p.scale * kLog2e;
       const bool ok = kvalid[lane];
-      s0 = ok && x0 + lane < vis[0] ? s0 * k2e : -INFINITY;
-      s1 = ok && x0 + lane < vis[1] ? s1 * k2e : -INFINITY;
+      s0 = ok && sees(0, x0 + lane) ? s0 * k2e : -INFINITY;
+      s1 = ok && sees(1, x0 + lane) ? s1 * k2e : -INFINITY;
       float c0, c1;
       const float p0 = softmax_step(s0, st[0], c0), p1 = softmax_step(s1, st[1], c1);
 #pragma unroll
@@ -503,13 +491,14 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
       }
       for (int k = 0; k < kGenKeys; ++k) {
         const float a = __shfl_sync(0xffffffffu, p0, k), b = __shfl_sync(0xffffffffu, p1, k);
-        if (x0 + k >= vis[0] && x0 + k >= vis[1]) continue;   // alike in every lane
+        const bool sees0 = sees(0, x0 + k), sees1 = sees(1, x0 + k);   // alike in every lane
+        if (!sees0 && !sees1) continue;
         const float* v = vs + k * VS + lane;
 #pragma unroll
         for (int d = 0; d < kNV; ++d) {
           const float x = lane + 32 * d < DV ? v[32 * d] : 0.f;
-          if (x0 + k < vis[0]) o[0][d] = fmaf(a, x, o[0][d]);
-          if (x0 + k < vis[1]) o[1][d] = fmaf(b, x, o[1][d]);
+          if (sees0) o[0][d] = fmaf(a, x, o[0][d]);
+          if (sees1) o[1][d] = fmaf(b, x, o[1][d]);
         }
       }
     }
@@ -625,7 +614,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
   }
 }
 
-template <typename T, bool kPaged, typename P>
+template <typename T, bool kPaged, bool kFp4, typename P>
 cudaError_t run_gen(const P& p, int DK, int DV, int64_t grid, cudaStream_t st) {
   const size_t smem = sizeof(float) * ((size_t)kGenRows * DK + (size_t)kGenKeys * (DK + 1) +
                                        (kPaged ? 0 : (size_t)kGenKeys * DV));
@@ -635,10 +624,10 @@ cudaError_t run_gen(const P& p, int DK, int DV, int64_t grid, cudaStream_t st) {
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kGenThreads), smem, st, p);
   };
   if constexpr (kPaged) {
-    if (DV > 512) return go(latent_attn_gen<T, 32, kPaged, P>);
-    if (DV > 256) return go(latent_attn_gen<T, 16, kPaged, P>);
+    if (DV > 512) return go(latent_attn_gen<T, 32, kPaged, kFp4, P>);
+    if (DV > 256) return go(latent_attn_gen<T, 16, kPaged, kFp4, P>);
   }
-  return go(latent_attn_gen<T, 8, kPaged, P>);   // an expanded value has at most 256 dims
+  return go(latent_attn_gen<T, 8, kPaged, kFp4, P>);   // an expanded value has at most 256 dims
 }
 
 }  // namespace
@@ -648,6 +637,7 @@ int launch_rope(const RopeParams& p, int dtype, cudaStream_t st) {
 }
 
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st) {
+  if (p.fp4) return launch_latent_insert_fp4(p, dtype, st);
   const int sms = sm_count();
   int tokens = kInsertTokens;                    // fewer a block while that leaves SMs without one
   while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * sms) tokens /= 2;
@@ -682,9 +672,12 @@ int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
   cudaError_t e;
   if (p.plan.tc) {
     e = launch_latent_attn_tc(p, st);
+  } else if (p.fp4) {
+    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true, true>(p, p.C + p.R, p.C, p.plan.ctas, st)
+                          : run_gen<float, true, true>(p, p.C + p.R, p.C, p.plan.ctas, st);
   } else {
-    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true>(p, p.C + p.R, p.C, p.plan.ctas, st)
-                          : run_gen<float, true>(p, p.C + p.R, p.C, p.plan.ctas, st);
+    e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true, false>(p, p.C + p.R, p.C, p.plan.ctas, st)
+                          : run_gen<float, true, false>(p, p.C + p.R, p.C, p.plan.ctas, st);
   }
   if (e == cudaSuccess) e = launch_latent_merge(p, dtype, st);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
@@ -694,8 +687,8 @@ int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_
   if (p.tc) return launch_latent_expanded_tc(p, st) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
   int64_t grid = ((int64_t)p.n_q / kGenRows + p.n_seq) * p.H;
   if (grid > 65536) grid = 65536;
-  const cudaError_t e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, false>(p, p.DN + p.DR, p.DV, grid, st)
-                                          : run_gen<float, false>(p, p.DN + p.DR, p.DV, grid, st);
+  const cudaError_t e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, false, false>(p, p.DN + p.DR, p.DV, grid, st)
+                                          : run_gen<float, false, false>(p, p.DN + p.DR, p.DV, grid, st);
   return e == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace v4a {
@@ -40,13 +42,15 @@ struct LatentInsertParams {
   int64_t c_stride, k_stride;
   const float* gamma;
   float eps;
-  CacheView cache;
+  CacheView cache;                    // FP4: its width is a row's bytes
+  int32_t fp4;
   int32_t* err;
   RotTab rot;
 };
 
 struct LatentGatherParams {
-  int32_t n_seq, n_rows, row_bytes;
+  int32_t n_seq, n_rows, row_bytes;   // row_bytes: of a row of out
+  int32_t C, R, fp4;
   const int32_t* cu;
   const int64_t* start;
   CacheView cache;
@@ -80,6 +84,9 @@ struct LatentAttnParams {
   float scale;
   int64_t max_pos;
   int64_t end;                        // no key is at or behind it: max_pos + 1 and the table's reach
+  int64_t window, sinks;              // of the keys up to its own a token sees the last `window` and
+                                      // the first `sinks` (window 0: all)
+  int32_t fp4;                        // rows in 4 bits; the cache's width is a row's bytes
   const int32_t* cu;
   const int64_t* start;
   const void* q;
@@ -118,6 +125,8 @@ int sm_count();
 int launch_rope(const RopeParams& p, int dtype, cudaStream_t st);
 int launch_latent_insert(const LatentInsertParams& p, int dtype, cudaStream_t st);
 int launch_latent_gather(const LatentGatherParams& p, cudaStream_t st);
+int launch_latent_insert_fp4(const LatentInsertParams& p, int dtype, cudaStream_t st);
+int launch_latent_gather_fp4(const LatentGatherParams& p, int dtype, cudaStream_t st);
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st);
@@ -126,6 +135,82 @@ cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream
 
 // ------------------------------------------------------------------ device-side plan
 #ifdef __CUDACC__
+
+// A kernel parameter array read with an index of each thread's own: through its address, as
+// ordinary memory. (From the constant bank the lanes' different words come one at a time.)
+__device__ __forceinline__ const float* by_address(const float* v) {
+  const float* q;
+  asm volatile("mov.b64 %0, %1;" : "=l"(q) : "l"(v));
+  return q;
+}
+
+// N elements, as one 16-byte access where they are as many bytes.
+template <typename T, int N>
+__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
+  if constexpr (N * sizeof(T) == 16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(p[i]);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
+  if constexpr (N * sizeof(T) == 16) {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = Elem<T>::from_f(f[i]);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = Elem<T>::from_f(f[i]);
+  }
+}
+
+// Eight e2m1 codes (code k in bits 4k .. 4k + 3) as four pairs of f16, in order.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{ .reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Eight values (even ones first in each byte) as e2m1 codes, to nearest even, saturating.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&v)[8]) {
+  uint32_t w;
+  asm("{ .reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3}; }"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+__device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+}
+// Block b (16 values) of an FP4 row: scale (B code); the inner product is exact.
+__device__ __forceinline__ void fp4_block(const uint8_t* row, int C, int R, int b, float scale, float (&f)[16]) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(row) + b);
+  const float block = e4m3_to_f32(__ldg(row + C / 2 + 2 * R + b));
+  uint32_t h[8];
+  e2m1x8_to_f16(w.x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
+  e2m1x8_to_f16(w.y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    f[2 * i] = scale * (block * v.x);
+    f[2 * i + 1] = scale * (block * v.y);
+  }
+}
 
 // Rows of a packed batch that belong to sequence b, inside [0, n) whatever cu holds.
 __device__ __forceinline__ int cu_at(const int32_t* cu, int i, int n) {
@@ -142,12 +227,29 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n_seq, int t) {
   return t >= __ldg(cu + lo) && t < __ldg(cu + lo + 1) ? lo : -1;
 }
 
+// The key behind the last one that a token at pos sees (0 for a position below 0), and, under a
+// window, the first one that it sees besides the sinks.
+__device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, int64_t pos) {
+  return max((int64_t)0, min(pos, p.end - 1) + 1);
+}
+__device__ __forceinline__ int64_t latent_from(const LatentAttnParams& p, int64_t pos) {
+  return max((int64_t)0, pos + 1 - p.window);
+}
+
+// Tiles of the sinks, and the most of them that any unit walks under a window: its tokens' windows
+// together, wherever they begin. (Also on the host, where the workspace is sized.)
+__host__ __device__ __forceinline__ int64_t window_tiles(int64_t window, int64_t sinks, int NR, int TK, int H) {
+  const int64_t tokens = (NR + H - 2) / H + 1;
+  return (sinks + TK - 1) / TK + (window + tokens + TK - 3) / TK + 1;
+}
+
 // One sequence's part of the plan.
 struct LatentSeq {
   int row0;          // first row of the batch's (token, head) rows
   int rows;          // rows of the sequence
   int units;         // units of NR rows
-  int tiles;         // key tiles of the whole sequence (1 in whole-unit plans)
+  int tiles;         // key tiles of the whole sequence, at most those of any unit's windows (1 in
+                     // whole-unit plans)
   int64_t start;     // position of its first new token
   __device__ __forceinline__ int shares(int U) const { return (units + U - 1) / U; }
   __device__ __forceinline__ int pairs(int U) const { return shares(U) * tiles; }
@@ -163,13 +265,11 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b
   s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
   const int64_t keys = min(s.start + n, p.end);
   s.tiles = !split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
+  if (p.window > 0 && s.tiles > 1)
+    s.tiles = (int)min((int64_t)s.tiles, window_tiles(p.window, min(p.sinks, keys), p.plan.NR, p.plan.TK, p.H));
   return s;
 }
 
-// Keys that a token at pos sees (0 for a position below 0).
-__device__ __forceinline__ int64_t latent_visible(const LatentAttnParams& p, int64_t pos) {
-  return max((int64_t)0, min(pos, p.end - 1) + 1);
-}
 // What is to be reported of a token's position. (Positions that the block table does not reach are
 // blocks without a page; only the table's are walked.)
 __device__ __forceinline__ void latent_report_pos(const LatentAttnParams& p, int64_t pos) {
@@ -222,7 +322,7 @@ __device__ __forceinline__ bool latent_split(const LatentAttnParams& p, int32_t*
   for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) {
     const LatentSeq s = latent_seq(p, b, true);
     if (s.units == 0) continue;
-    const int first = (int)((latent_visible(p, s, 0) + p.plan.TK - 1) / p.plan.TK);
+    const int first = (int)min((int64_t)s.tiles, (latent_visible(p, s, 0) + p.plan.TK - 1) / p.plan.TK);
     sees += s.units * ((first + s.tiles + 1) / 2);
     line += s.units * s.tiles;
     longest = max(longest, s.tiles);
@@ -297,13 +397,18 @@ __device__ __forceinline__ int latent_per_team(int total, int n) { return n > 0 
 // One piece of work of a CTA: a unit and a range of its key tiles.
 struct LatentPiece {
   int seq, row0, rows;         // row0: first row of the unit in q; rows <= NR
-  int tile0, tile1;            // key tiles of the sequence
+  int tile0, tile1;            // key tiles of the sequence (under a window, of those that it walks)
+  int sink_tiles, skip;        // under a window: the first sink_tiles tiles, then those `skip` further on
   int64_t keys, keys0;         // keys that the unit's last and first rows see
   int64_t start;               // position of the sequence's first token
   int seq_row0;                // first row of the sequence
   int whole;                   // the piece holds every tile of the unit: write the result
   int slot;                    // where its partial result goes otherwise
   int job_rows, job_last;      // set where the piece is the second of its unit's pieces (see below)
+  template <bool kWindow>
+  __device__ __forceinline__ int64_t tile_at(int t) const {
+    return kWindow && t >= sink_tiles ? (int64_t)t + skip : t;
+  }
 };
 
 // Walks a CTA's pieces, forward through the sequences. All threads of a role call it alike;
@@ -359,7 +464,14 @@ struct LatentWalk {
     w.rows = max(0, min(p.plan.NR, s.rows - ur));
     w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
     w.keys0 = w.rows > 0 ? latent_visible(p, s, ur / p.H) : 0;
-    const int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
+    int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
+    w.sink_tiles = w.skip = 0;
+    if (p.window > 0) {
+      const int64_t from = latent_from(p, s.start + ur / p.H) / p.plan.TK;
+      w.sink_tiles = (int)((min(p.sinks, w.keys) + p.plan.TK - 1) / p.plan.TK);
+      w.skip = (int)max((int64_t)0, min(from, (int64_t)unit_tiles) - w.sink_tiles);
+      unit_tiles -= w.skip;
+    }
     if (n > 0) {
       w.tile0 = 0;
       w.tile1 = unit_tiles;

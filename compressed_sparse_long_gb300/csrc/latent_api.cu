@@ -83,8 +83,10 @@ int check_latent(const v4a_latent_cfg* c) {
   if (!known_type(c->dtype)) return V4A_ERR_UNSUPPORTED;
   const int rc = check_rope(&c->rope);
   if (rc) return rc;
-  if (c->reserved != 0 || c->n_heads <= 0 || c->n_heads > 1024) return V4A_ERR_ARG;
+  if (c->cache_format != V4A_LATENT_PLAIN && c->cache_format != V4A_LATENT_FP4) return V4A_ERR_UNSUPPORTED;
+  if (c->n_heads <= 0 || c->n_heads > 1024) return V4A_ERR_ARG;
   if (c->latent_dim < 8 || c->latent_dim % 8 || c->latent_dim > 1024) return V4A_ERR_UNSUPPORTED;
+  if (c->cache_format == V4A_LATENT_FP4 && c->latent_dim % 32) return V4A_ERR_UNSUPPORTED;
   if (c->rope.dim % 8 || c->rope.dim > 128) return V4A_ERR_UNSUPPORTED;
   if (c->nope_dim < 0 || c->nope_dim % 8 || c->nope_dim > 256) return V4A_ERR_UNSUPPORTED;
   if (c->v_dim < 8 || c->v_dim % 8 || c->v_dim > 256) return V4A_ERR_UNSUPPORTED;
@@ -92,8 +94,17 @@ int check_latent(const v4a_latent_cfg* c) {
   return V4A_OK;
 }
 
+bool is_fp4(const v4a_latent_cfg* c) { return c->cache_format == V4A_LATENT_FP4; }
+
+// The cache as the kernels see it: an FP4 row's width in bytes.
+CacheView latent_view(const v4a_latent_cfg* c, const v4a_cache* cache) {
+  CacheView v = view_of(cache);
+  if (is_fp4(c)) v.width = V4A_LATENT_FP4_ROW_BYTES(c->latent_dim, c->rope.dim);
+  return v;
+}
+
 int check_latent_cache(const v4a_latent_cfg* c, const v4a_cache* cache) {
-  const int rc = check_cache(cache, kBlock, c->latent_dim + c->rope.dim, false);
+  const int rc = check_cache(cache, kBlock, c->latent_dim + c->rope.dim, is_fp4(c));
   if (rc) return rc;
   // tensor maps count pool rows in 31 bits
   return cache->n_pages * kBlock > INT32_MAX ? V4A_ERR_UNSUPPORTED : V4A_OK;
@@ -107,22 +118,30 @@ int check_batch(int32_t n_seq, int32_t n, const int32_t* cu, const int64_t* star
 }
 
 bool on_tensor_cores(const v4a_latent_cfg* c) {
-  return c->dtype == V4A_BF16 && c->latent_dim == 512 && c->rope.dim == 64;
+  return c->dtype == V4A_BF16 && c->latent_dim == 512 && c->rope.dim == 64 && !is_fp4(c);
 }
 
 // The device counts the steps of a call in 31 bits, sums of two of them included.
 constexpr int64_t kMostSteps = (int64_t)1 << 30;
 
 // The plan of an absorbed call. False when there are too many steps.
-bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t max_pos, LatentPlan* pl) {
+// window 0: every token sees all keys up to its own.
+bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t max_pos, int64_t window,
+               int64_t sinks, LatentPlan* pl) {
   const bool tc = on_tensor_cores(c);
   pl->tc = tc;
   pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
   const int64_t rows = (int64_t)n_tokens * c->n_heads;
   const int64_t units = (rows + pl->NR - 1) / pl->NR + n_seq;   // at most, over the sequences
-  const int64_t tiles = max_pos / pl->TK + 1;
+  int64_t tiles = max_pos / pl->TK + 1;
   if (rows > INT32_MAX / 2) return false;
+  if (window > 0) {
+    if (tiles >= kMostSteps) return false;       // tiles are numbered in 31 bits
+    const int64_t walked = window_tiles(window < max_pos ? window : max_pos, sinks < max_pos ? sinks : max_pos,
+                                        pl->NR, pl->TK, c->n_heads);
+    if (walked < tiles) tiles = walked;
+  }
   // sharing key tiles pays where an average sequence has several units (the device decides)
   pl->max_U = 1;
   while (tc && pl->max_U < 4 && rows / n_seq >= 2 * pl->max_U * pl->NR) pl->max_U *= 2;
@@ -179,6 +198,56 @@ bool plan_expanded(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_q, int32_t 
     *bytes = *job_at + align_up((size_t)p->pairs * 8 * sizeof(int32_t), 256);
   }
   return true;
+}
+
+size_t attn_workspace(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, int64_t max_pos, int64_t window,
+                      int64_t sinks) {
+  LatentPlan pl;
+  size_t ml_at, job_at;
+  if (check_latent(cfg) || n_seq < 0 || n_seq > V4A_MAX_SEQ || n_tokens < 0 || max_pos < 0 ||
+      max_pos >= V4A_MAX_POS || n_tokens == 0 || n_seq == 0)
+    return 0;
+  return make_plan(cfg, n_seq, n_tokens, max_pos, window, sinks, &pl) ? part_bytes(cfg, pl, &ml_at, &job_at) : 0;
+}
+
+int attn_call(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, const int32_t* cu_tokens,
+              const int64_t* start_pos, int64_t max_pos, int64_t window, int64_t sinks, const void* q,
+              const v4a_cache* cache, void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+              v4a_stream_t stream) {
+  int rc = check_latent(cfg);
+  if (rc) return rc;
+  if ((rc = check_batch(n_seq, n_tokens, cu_tokens, start_pos))) return rc;
+  if (max_pos < 0 || max_pos >= V4A_MAX_POS) return V4A_ERR_ARG;
+  if (n_seq == 0 || n_tokens == 0) return V4A_OK;
+  if ((rc = check_latent_cache(cfg, cache))) return rc;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return V4A_ERR_ARG;
+  LatentAttnParams p{};
+  if (!make_plan(cfg, n_seq, n_tokens, max_pos, window, sinks, &p.plan)) return V4A_ERR_UNSUPPORTED;
+  size_t ml_at = 0, job_at = 0;
+  const size_t need = part_bytes(cfg, p.plan, &ml_at, &job_at);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return V4A_ERR_ARG;
+  p.n_seq = n_seq;
+  p.n_tokens = n_tokens;
+  p.H = cfg->n_heads;
+  p.C = cfg->latent_dim;
+  p.R = cfg->rope.dim;
+  p.scale = cfg->softmax_scale;
+  p.max_pos = max_pos;
+  p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
+  p.fp4 = is_fp4(cfg);
+  const int64_t reach = (int64_t)cache->max_blocks * kBlock;
+  p.end = max_pos + 1 < reach ? max_pos + 1 : reach;
+  p.cu = cu_tokens;
+  p.start = start_pos;
+  p.q = q;
+  p.out = out;
+  p.cache = latent_view(cfg, cache);
+  p.part_o = reinterpret_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + ml_at);
+  p.part_job = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + job_at);
+  p.err = dev_err;
+  return launch_latent_attn(p, cfg->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -241,7 +310,8 @@ int v4a_latent_insert(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens
   p.k_stride = k_stride;
   p.gamma = gamma;
   p.eps = cfg->rms_eps;
-  p.cache = view_of(cache);
+  p.cache = latent_view(cfg, cache);
+  p.fp4 = is_fp4(cfg);
   p.err = dev_err;
   p.rot = make_rot(&cfg->rope);
   return launch_latent_insert(p, cfg->dtype, reinterpret_cast<cudaStream_t>(stream));
@@ -260,58 +330,46 @@ int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows, 
   p.n_seq = n_seq;
   p.n_rows = n_rows;
   p.row_bytes = (int32_t)((cfg->latent_dim + cfg->rope.dim) * elem_size(cfg->dtype));
+  p.C = cfg->latent_dim;
+  p.R = cfg->rope.dim;
+  p.fp4 = is_fp4(cfg);
   p.cu = cu_rows;
   p.start = start_pos;
-  p.cache = view_of(cache);
+  p.cache = latent_view(cfg, cache);
   p.out = out;
   p.err = dev_err;
-  return launch_latent_gather(p, reinterpret_cast<cudaStream_t>(stream));
+  return p.fp4 ? launch_latent_gather_fp4(p, cfg->dtype, reinterpret_cast<cudaStream_t>(stream))
+               : launch_latent_gather(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                                       int64_t max_pos) {
-  LatentPlan pl;
-  size_t ml_at, job_at;
-  if (check_latent(cfg) || n_seq < 0 || n_seq > V4A_MAX_SEQ || n_tokens < 0 || max_pos < 0 ||
-      max_pos >= V4A_MAX_POS || n_tokens == 0 || n_seq == 0)
-    return 0;
-  return make_plan(cfg, n_seq, n_tokens, max_pos, &pl) ? part_bytes(cfg, pl, &ml_at, &job_at) : 0;
+  return attn_workspace(cfg, n_seq, n_tokens, max_pos, 0, 0);
 }
 
 int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, const int32_t* cu_tokens,
                     const int64_t* start_pos, int64_t max_pos, const void* q, const v4a_cache* cache, void* out,
                     void* workspace, size_t workspace_bytes, int32_t* dev_err, v4a_stream_t stream) {
-  int rc = check_latent(cfg);
+  return attn_call(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, 0, 0, q, cache, out, workspace,
+                   workspace_bytes, dev_err, stream);
+}
+
+size_t v4a_latent_attn_window_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                                             int64_t max_pos, int64_t window, int64_t sinks) {
+  if (window < 1 || sinks < 0) return 0;
+  return attn_workspace(cfg, n_seq, n_tokens, max_pos, window > max_pos ? 0 : window, sinks);
+}
+
+int v4a_latent_attn_window(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, const int32_t* cu_tokens,
+                           const int64_t* start_pos, int64_t max_pos, int64_t window, int64_t sinks, const void* q,
+                           const v4a_cache* cache, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_err, v4a_stream_t stream) {
+  const int rc = check_latent(cfg);
   if (rc) return rc;
-  if ((rc = check_batch(n_seq, n_tokens, cu_tokens, start_pos))) return rc;
-  if (max_pos < 0 || max_pos >= V4A_MAX_POS) return V4A_ERR_ARG;
-  if (n_seq == 0 || n_tokens == 0) return V4A_OK;
-  if ((rc = check_latent_cache(cfg, cache))) return rc;
-  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return V4A_ERR_ARG;
-  LatentAttnParams p{};
-  if (!make_plan(cfg, n_seq, n_tokens, max_pos, &p.plan)) return V4A_ERR_UNSUPPORTED;
-  size_t ml_at = 0, job_at = 0;
-  const size_t need = part_bytes(cfg, p.plan, &ml_at, &job_at);
-  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return V4A_ERR_ARG;
-  p.n_seq = n_seq;
-  p.n_tokens = n_tokens;
-  p.H = cfg->n_heads;
-  p.C = cfg->latent_dim;
-  p.R = cfg->rope.dim;
-  p.scale = cfg->softmax_scale;
-  p.max_pos = max_pos;
-  const int64_t reach = (int64_t)cache->max_blocks * kBlock;
-  p.end = max_pos + 1 < reach ? max_pos + 1 : reach;
-  p.cu = cu_tokens;
-  p.start = start_pos;
-  p.q = q;
-  p.out = out;
-  p.cache = view_of(cache);
-  p.part_o = reinterpret_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + ml_at);
-  p.part_job = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + job_at);
-  p.err = dev_err;
-  return launch_latent_attn(p, cfg->dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (window < 1 || sinks < 0) return V4A_ERR_ARG;
+  // (a window that reaches behind every position's beginning hides nothing)
+  return attn_call(cfg, n_seq, n_tokens, cu_tokens, start_pos, max_pos, window > max_pos ? 0 : window, sinks, q,
+                   cache, out, workspace, workspace_bytes, dev_err, stream);
 }
 
 size_t v4a_latent_attn_expanded_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_q, int32_t n_k) {

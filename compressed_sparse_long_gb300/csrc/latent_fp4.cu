@@ -1,0 +1,278 @@
+// The latent cache in 4 bits: insert and gather of FP4 rows (the format is stated in include/v4a.h at
+// V4A_LATENT_FP4).
+//
+//   z = gamma c, r = 1 / sqrt(mean c^2 + eps), k = rope(k_pe)
+//   row scale s = r max|z| / 2688 (more where the rotary part or 2^-100 asks for it), u = s / r
+//   block of 16: B = e4m3(max|z / u| / 6), code = e2m1(z / (u B));  h = f16(k / s)
+//
+// Codes and block scales come from products of z with one number each, in the order that the header
+// gives (no fused multiply-add), so they are the same whatever sums the mean square. Each rounding to
+// fewer bits is the format's own.
+#include "kernels.h"
+#include "latent.h"
+
+namespace v4a {
+namespace {
+
+// The larger one, or NaN where either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ----------------------------------------------------------------------------- insert
+// As the kernel for plain rows: a block looks the pool rows of up to 32 tokens up, a thread a token,
+// then a warp takes one token after the other, the next one's row requested ahead. A lane holds whole
+// blocks of 16 values (blocks lane, lane + 32), so that a block's maximum needs no other lane, and
+// pairs lane, lane + 32 of the rotary part.
+constexpr int kInsertWarps = 8, kInsertTokens = 32;
+
+template <typename T, int kBlocks>
+struct Fp4Row {
+  static constexpr int kV = 16 / (int)sizeof(T), kVec = 16 / kV;   // vectors of a block
+  uint4 v[kBlocks][kVec];
+  T x0[2], x1[2];
+  __device__ __forceinline__ void load(const LatentInsertParams& p, int64_t t, int lane) {
+    const T* c = reinterpret_cast<const T*>(p.c) + t * p.c_stride;
+    const T* k = reinterpret_cast<const T*>(p.k_pe) + t * p.k_stride;
+    const int np = p.rot.dim / 2;
+    const bool half = p.rot.layout == V4A_ROPE_HALF;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+      if (lane + 32 * i < p.C / 16)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[i][j] = *reinterpret_cast<const uint4*>(c + (lane + 32 * i) * 16 + j * kV);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (i < np) {
+        x0[j] = k[half ? i : 2 * i];
+        x1[j] = k[half ? i + np : 2 * i + 1];
+      }
+    }
+  }
+};
+
+template <typename T, int kBlocks>
+__global__ void __launch_bounds__(32 * kInsertWarps, 2)
+    latent_insert_fp4_kernel(const __grid_constant__ LatentInsertParams p, int tokens) {
+  using Row = Fp4Row<T, kBlocks>;
+  constexpr int kV = Row::kV;
+  __shared__ int64_t slots[kInsertTokens], at[kInsertTokens];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int np = p.rot.dim / 2, nb = p.C / 16;
+  const int t0 = blockIdx.x * tokens, nt = min(tokens, p.n_tokens - t0);
+  float rate[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = min(lane + 32 * j, np - 1);
+    rate[j][0] = by_address(p.rot.phi_hi)[i];
+    rate[j][1] = by_address(p.rot.phi_lo)[i];
+    rate[j][2] = by_address(p.rot.psi_hi)[i];
+    rate[j][3] = by_address(p.rot.psi_lo)[i];
+  }
+  pdl_wait();
+  Row next;
+  if (warp < nt) next.load(p, t0 + warp, lane);
+  if (threadIdx.x < nt) {
+    const int t = t0 + threadIdx.x, b = find_seq(p.cu, p.n_seq, t);
+    int64_t slot = -1, pos = 0;
+    if (b >= 0) {
+      pos = __ldg(p.start + b) + (t - __ldg(p.cu + b));
+      if (pos < 0 || pos >= V4A_MAX_POS) {
+        raise_err(p.err, V4A_DEV_BAD_POS);
+      } else {
+        slot = slot_of(p.cache, b, pos);
+        slot_ok(slot, p.err);
+      }
+    }
+    slots[threadIdx.x] = slot;
+    at[threadIdx.x] = pos;
+  }
+  __syncthreads();
+  const bool half = p.rot.layout == V4A_ROPE_HALF;
+  for (int k = warp; k < nt; k += kInsertWarps) {
+    const Row in = next;
+    if (k + kInsertWarps < nt) next.load(p, t0 + k + kInsertWarps, lane);
+    const int64_t slot = slots[k], pos = at[k];
+    if (slot < 0) continue;
+    float z[kBlocks][16], ss = 0.f, zmax = 0.f, kmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int b = lane + 32 * i;
+      if (b >= nb) continue;
+      const T* e = reinterpret_cast<const T*>(&in.v[i][0]);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        z[i][q] = Elem<T>::to_f(e[q]);
+        ss = fmaf(z[i][q], z[i][q], ss);
+      }
+      if (p.gamma) {
+#pragma unroll
+        for (int q = 0; q < 16; q += 4) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>(p.gamma + 16 * b + q));
+          z[i][q] *= g.x;
+          z[i][q + 1] *= g.y;
+          z[i][q + 2] *= g.z;
+          z[i][q + 3] *= g.w;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) zmax = max_nan(zmax, fabsf(z[i][q]));
+    }
+    float y0[2] = {0.f, 0.f}, y1[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (lane + 32 * j >= np) continue;
+      float cc, sn;
+      rot_cs(pos, rate[j][0], rate[j][1], rate[j][2], rate[j][3], cc, sn);
+      cc *= p.rot.amp;
+      sn *= p.rot.amp;
+      const float a = Elem<T>::to_f(in.x0[j]), b = Elem<T>::to_f(in.x1[j]);
+      y0[j] = a * cc - b * sn;
+      y1[j] = a * sn + b * cc;
+      kmax = max_nan(kmax, max_nan(fabsf(y0[j]), fabsf(y1[j])));
+    }
+    const float r = p.gamma ? 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps) : 1.f;
+    zmax = warp_max_nan(zmax);
+    kmax = warp_max_nan(kmax);
+    float u = __fmul_rn(zmax, 1.0f / 2688.0f), s = __fmul_rn(r, u);
+    const float least = max_nan(__fmul_rn(kmax, 1.0f / 32768.0f), 0x1p-100f);
+    if (!(s >= least)) {
+      u = least / r;
+      s = s != s ? s : least;          // (NaN stays)
+    }
+    const float iu = 1.0f / u, is = 1.0f / s;
+    uint8_t* row = reinterpret_cast<uint8_t*>(p.cache.data) + slot * (int64_t)p.cache.width;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int b = lane + 32 * i;
+      if (b >= nb) continue;
+      float m = 0.f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        z[i][q] = __fmul_rn(z[i][q], iu);
+        m = fmaxf(m, fabsf(z[i][q]));
+      }
+      const __nv_fp8_storage_t code = __nv_cvt_float_to_fp8(__fmul_rn(m, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
+      const float block = e4m3_to_f32(code), ib = block > 0.f ? 1.0f / block : 0.f;
+      float a[8], c[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        a[q] = __fmul_rn(z[i][q], ib);
+        c[q] = __fmul_rn(z[i][q + 8], ib);
+      }
+      reinterpret_cast<uint2*>(row)[b] = make_uint2(f32x8_to_e2m1(a), f32x8_to_e2m1(c));
+      row[p.C / 2 + 2 * p.rot.dim + b] = code;
+    }
+    __half* h = reinterpret_cast<__half*>(row + p.C / 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (i >= np) continue;
+      h[half ? i : 2 * i] = __float2half_rn(__fmul_rn(y0[j], is));
+      h[half ? i + np : 2 * i + 1] = __float2half_rn(__fmul_rn(y1[j], is));
+    }
+    if (lane == 0) p.cache.scale[slot] = s;
+  }
+}
+
+// ----------------------------------------------------------------------------- gather
+// A block takes `rows` rows: their pool rows are looked up first, a thread a row; then a thread takes
+// a block of 16 latent values (8 bytes of codes, one block scale) or 16 rotary ones at a time.
+constexpr int kGatherRows = 64, kGatherThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kGatherThreads)
+    latent_gather_fp4_kernel(const __grid_constant__ LatentGatherParams p, int rows) {
+  constexpr int kV = 16 / (int)sizeof(T);
+  __shared__ int64_t slots[kGatherRows];   // pool row, -1: zeros, -2: no row of the batch
+  __shared__ float scales[kGatherRows];
+  const int r0 = blockIdx.x * rows, nr = min(rows, p.n_rows - r0);
+  pdl_wait();
+  if (threadIdx.x < nr) {
+    const int t = r0 + threadIdx.x;
+    const int b = find_seq(p.cu, p.n_seq, t);
+    int64_t s = -2;
+    if (b >= 0) {
+      s = slot_of(p.cache, b, __ldg(p.start + b) + (t - __ldg(p.cu + b)));
+      if (!slot_ok(s, p.err)) s = -1;
+    }
+    slots[threadIdx.x] = s;
+    scales[threadIdx.x] = s >= 0 ? __ldg(p.cache.scale + s) : 0.f;
+  }
+  __syncthreads();
+  const int lat = p.C / 16, items = lat + (p.R + 15) / 16, width = p.C + p.R;
+  for (int k = threadIdx.x; k < nr * items; k += kGatherThreads) {
+    const int r = k / items, i = k - r * items;
+    const int64_t s = slots[r];
+    if (s == -2) continue;
+    float f[16] = {};
+    int n = 16;
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(p.cache.data) + s * (int64_t)p.cache.width;
+    if (i < lat) {
+      if (s >= 0) fp4_block(row, p.C, p.R, i, scales[r], f);
+    } else {
+      const int d = (i - lat) * 16;
+      n = min(16, p.R - d);                    // 8 or 16
+      if (s >= 0) {
+        const uint4* h = reinterpret_cast<const uint4*>(row + p.C / 2 + 2 * d);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (8 * j >= n) continue;
+          const uint4 w = __ldg(h + j);
+          const __half2* v = reinterpret_cast<const __half2*>(&w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 x = __half22float2(v[q]);
+            f[8 * j + 2 * q] = scales[r] * x.x;
+            f[8 * j + 2 * q + 1] = scales[r] * x.y;
+          }
+        }
+      }
+    }
+    T* out = reinterpret_cast<T*>(p.out) + (int64_t)(r0 + r) * width + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 16 / kV; ++j) {
+      if (j * kV >= n) continue;
+      float g[kV];
+#pragma unroll
+      for (int q = 0; q < kV; ++q) g[q] = f[j * kV + q];
+      store_pack<T, kV>(out + j * kV, g);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_latent_insert_fp4(const LatentInsertParams& p, int dtype, cudaStream_t st) {
+  const int sms = sm_count();
+  int tokens = kInsertTokens;                    // fewer a block while that leaves SMs without one
+  while (tokens > kInsertWarps && (int64_t)p.n_tokens < (int64_t)tokens * 2 * sms) tokens /= 2;
+  const dim3 grid((unsigned)((p.n_tokens + (int64_t)tokens - 1) / tokens)), block(32 * kInsertWarps);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, st, p, tokens) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  };
+  if (dtype == V4A_BF16)
+    return p.C <= 512 ? go(latent_insert_fp4_kernel<__nv_bfloat16, 1>) : go(latent_insert_fp4_kernel<__nv_bfloat16, 2>);
+  return p.C <= 512 ? go(latent_insert_fp4_kernel<float, 1>) : go(latent_insert_fp4_kernel<float, 2>);
+}
+
+int launch_latent_gather_fp4(const LatentGatherParams& p, int dtype, cudaStream_t st) {
+  const int sms = sm_count();
+  int rows = kGatherRows;
+  while (rows > 8 && (int64_t)p.n_rows < (int64_t)rows * 2 * sms) rows /= 2;
+  const dim3 grid((unsigned)(((int64_t)p.n_rows + rows - 1) / rows));
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(kGatherThreads), 0, st, p, rows) == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  };
+  return dtype == V4A_BF16 ? go(latent_gather_fp4_kernel<__nv_bfloat16>) : go(latent_gather_fp4_kernel<float>);
+}
+
+}  // namespace v4a

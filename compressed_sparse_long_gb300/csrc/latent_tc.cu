@@ -99,10 +99,12 @@ __device__ __forceinline__ float reduce_scatter_sum(const float (&v)[32]) {
 }
 
 // Pool row of the first key of a tile, or a negative number when its page is missing or bad.
-__device__ __forceinline__ int64_t tile_slot(const LatentAttnParams& p, int seq, int tile) {
-  return slot_of(p.cache, seq, (int64_t)tile * kTK);
+__device__ __forceinline__ int64_t tile_slot(const LatentAttnParams& p, int seq, int64_t tile) {
+  return slot_of(p.cache, seq, tile * kTK);
 }
 
+// kWindow: tokens see a window and the first keys (p.window, p.sinks).
+template <bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_attn_tc(const __grid_constant__ LatentAttnParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap) {
@@ -193,12 +195,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.rows == 0) continue;
       // lane c: row c of this half, the keys it sees
       const int my_row = half * 32 + lane;
-      int64_t vis = 0;
+      int64_t vis = 0, from = 0;
       if (my_row < w.rows) {
         const int64_t pos = w.start + (w.row0 + my_row - w.seq_row0) / p.H;
         vis = latent_visible(p, pos);
+        if (kWindow) from = latent_from(p, pos);
         if (quad == 0) latent_report_pos(p, pos);
       }
+      // where the first row's window begins, and the last one's: keys before the one are seen as sinks
+      // only, keys behind the other by every row
+      const int64_t first_from = kWindow ? latent_from(p, w.start + (w.row0 - w.seq_row0) / p.H) : 0;
+      const int64_t all_from = kWindow ? latent_from(p, w.start + (w.row0 + w.rows - 1 - w.seq_row0) / p.H) : 0;
       // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
       // row that sees nothing (or is none) infinity
       float m = -INFINITY;
@@ -212,13 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         // (the tile's last copy is complete before its products are)
         if (!tc::mbar_wait(xfull, g & 1, abort_flag, p.err)) { ok = false; break; }
-        const int64_t x0 = (int64_t)t * kTK;
+        const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
         const int valid = tile_ok[g & 1] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
         // A tile that every row sees whole, with every row's reference set: the weights are
         // taken against the references as they are, unless one of them would pass 1 (weights
         // and sums are floating-point numbers, so a reference need not be the maximum). The
         // group agrees on that while it computes the exponentials.
-        bool slow = valid < kTK || w.keys0 < x0 + kTK || __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
+        bool slow = valid < kTK || w.keys0 < x0 + kTK || (kWindow && x0 < all_from && x0 + kTK > p.sinks) ||
+                    __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
         float4 ref[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) ref[c] = *reinterpret_cast<const float4*>(mb + 4 * c);
@@ -258,6 +266,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
+          if (kWindow) {
+            const int begin = (int)max((int64_t)0, min(from - x0, (int64_t)kTK));
+            const bool sink = x0 + row < p.sinks;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
+          }
           float* rb = red_max + (ru & 1) * 256 + half * 128;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -309,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(xbuf + tc::sw128_off(row, half * 4 + i)) =
               make_uint4(pack_bf16(s[8 * i], s[8 * i + 1]), pack_bf16(s[8 * i + 2], s[8 * i + 3]),
                          pack_bf16(s[8 * i + 4], s[8 * i + 5]), pack_bf16(s[8 * i + 6], s[8 * i + 7]));
-        if (row >= valid) {                       // 0 times whatever lies behind the keys must be 0
+        // 0 times whatever lies behind the keys, or between sinks and windows, must be 0
+        if (row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks)) {
 #pragma unroll 1
           for (int b = half * 4; b < half * 4 + 4; ++b)
 #pragma unroll
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
         for (int b = 0; b < 9; ++b) tma_2d(qbuf + b * kQBlock, &qmap, b * 128, w.row0, qfull);
         for (int t = w.tile0; t < w.tile1; ++t, ++g) {
-          const int64_t slot = tile_slot(p, w.seq, t);
+          const int64_t slot = tile_slot(p, w.seq, w.tile_at<kWindow>(t));
           const bool have = slot >= 0;
           if (!have) slot_ok(slot, p.err);
 #pragma unroll
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive(xfull);
           }
           if (t + 1 < w.tile1) {             // the next tile's rows into L2
-            const int64_t ahead = tile_slot(p, w.seq, t + 1);
+            const int64_t ahead = tile_slot(p, w.seq, w.tile_at<kWindow>(t + 1));
             if (ahead >= 0) {
               const uint8_t* rows = reinterpret_cast<const uint8_t*>(p.cache.data) + ahead * (kW * 2);
 #pragma unroll 1
@@ -532,10 +548,12 @@ cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st) {
   if (!encode_byte_rows_map(&qmap, p.q, (uint64_t)rows, kW * 2, 128, kNR) ||
       !encode_byte_rows_map(&kmap, p.cache.data, (uint64_t)pool_rows, kW * 2, 128, kTK))
     return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(latent_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(latent_attn_tc, dim3((unsigned)p.plan.ctas), dim3(kThreads), kSmemBytes, st, p, qmap, kmap);
+  auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)p.plan.ctas), dim3(kThreads), kSmemBytes, st, p, qmap, kmap);
+  };
+  return p.window > 0 ? go(latent_attn_tc<true>) : go(latent_attn_tc<false>);
 }
 
 }  // namespace v4a

@@ -9,6 +9,10 @@ chunks (absorbed form, the projections applied around the call by the caller)::
     rope(cfg.rope, q[..., C:], pos, out=q[..., C:])  # q = [q_nope W_uk | q_pe]
     o = lay.attention(cu, start, max_pos, q)         # then out = o W_uv
 
+A cache in 4 bits is a pool of another format (LATENT_FP4) under the same calls; attention with a
+window and first tokens that stay visible is ``attention(.., window=, sinks=)``, after which blocks
+behind the window may be given back (``pages.PageTable``).
+
 Prompts, after a cached prefix or none (expanded form)::
 
     lay.insert(cu, start, c, k_pe)
@@ -22,7 +26,8 @@ from ctypes import byref
 
 import torch
 
-from . import (BF16, FP32, Cache, LatentCfg, RopeCfg, _check, library)
+from . import (BF16, FP32, LATENT_FP4, Cache, LatentCfg, RopeCfg, _check, latent_row_bytes,
+               library)
 from .layer import PagedPool, current_raw as _current_raw, on_stream, scratch
 
 _TYPES = {BF16: torch.bfloat16, FP32: torch.float32}
@@ -156,6 +161,8 @@ class LatentLayer:
 
     pool: PagedPool of [n_pages * 256, latent_dim + rope dim] rows, or None for a layer that
     is only used in the expanded form; gamma: fp32 [latent_dim] or None (no norm at insert).
+    A layer whose cfg has cache_format LATENT_FP4 has a pool of uint8 rows of
+    latent_row_bytes(cfg) bytes with fp32 scales [n_pages * 256].
     """
 
     def __init__(self, cfg: LatentCfg, pool: PagedPool | None, gamma: torch.Tensor | None = None):
@@ -164,13 +171,22 @@ class LatentLayer:
         self.cfg, self.pool, self.gamma = cfg, pool, gamma
         self.dtype = _TYPES[cfg.dtype]
         self.width = cfg.latent_dim + cfg.rope.dim
+        self._fp4 = cfg.cache_format == LATENT_FP4
+        self._rows = ((torch.uint8, latent_row_bytes(cfg)) if self._fp4
+                      else (self.dtype, self.width))   # of the pool: type, elements
         self._desc = None, None
         dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
         if pool is not None:
-            _need(pool.data, "pool.data", dev, self.dtype, (None, self.width))
-            _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
+            self._need_pool(pool, dev)
         if gamma is not None:
             _need(gamma, "gamma", dev, torch.float32, (cfg.latent_dim,))
+
+    def _need_pool(self, pool, dev):
+        dtype, width = self._rows
+        _need(pool.data, "pool.data", dev, dtype, (None, width))
+        _need(pool.block_table, "pool.block_table", dev, torch.int32, (None, None))
+        if self._fp4:
+            _need(pool.scale, "pool.scale", dev, torch.float32, (pool.data.shape[0],))
 
     def _describe(self, dev):
         """(sequences of the block table, C descriptor) of the layer's pool as it is now."""
@@ -178,18 +194,21 @@ class LatentLayer:
         if pool is None:
             raise ValueError("this layer has no cache")
         data, bt, rows = pool.data, pool.block_table, pool.rows_per_block
+        scale = pool.scale if self._fp4 else None
         shape, table = data.shape, bt.shape
-        if not (data.dtype is self.dtype and bt.dtype is torch.int32
-                and len(shape) == len(table) == 2 and shape[1] == self.width
+        dtype, width = self._rows
+        if not (data.dtype is dtype and bt.dtype is torch.int32
+                and len(shape) == len(table) == 2 and shape[1] == width
                 and data.get_device() == dev == bt.get_device()
-                and data.is_contiguous() and bt.is_contiguous()):
-            _need(data, "pool.data", dev, self.dtype, (None, self.width))
-            _need(bt, "pool.block_table", dev, torch.int32, (None, None))
+                and data.is_contiguous() and bt.is_contiguous()
+                and (not self._fp4 or _fits(scale, dev, torch.float32, shape[:1]))):
+            self._need_pool(pool, dev)
         # (the structure is kept for as long as a new one would say the same)
-        key = (data.data_ptr(), bt.data_ptr(), table[1], rows, shape[0])
+        key = (data.data_ptr(), bt.data_ptr(), table[1], rows, shape[0],
+               None if scale is None else scale.data_ptr())
         d = self._desc
         if d[0] != key:
-            d = self._desc = key, Cache(key[0], None, key[1], table[1], rows, shape[0] // rows,
+            d = self._desc = key, Cache(key[0], key[5], key[1], table[1], rows, shape[0] // rows,
                                         self.width, 0)
         return table[0], d[1]
 
@@ -245,9 +264,12 @@ class LatentLayer:
             _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
-    def attention(self, cu, start, max_pos, q, out=None, dev_err=None, stream=None):
+    def attention(self, cu, start, max_pos, q, out=None, dev_err=None, stream=None, window=None,
+                  sinks=0):
         """Absorbed attention of q [n, H, latent_dim + rope dim] over the cache: one new token
-        a sequence (decode) or chunks; returns [n, H, latent_dim]."""
+        a sequence (decode) or chunks; returns [n, H, latent_dim]. With a ``window`` a token
+        sees, of the keys up to its own, the last ``window`` and the sequence's first ``sinks``;
+        blocks that no token sees into need no page."""
         dev, n_seq, cache = self._batch(cu, start)
         h = self.cfg.n_heads
         n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
@@ -258,11 +280,18 @@ class LatentLayer:
         elif not _fits(out, dev, self.dtype, (n, h, self.cfg.latent_dim)):
             _need(out, "out", dev, self.dtype, (n, h, self.cfg.latent_dim))
         lib, cfg = library(), byref(self.cfg)
-        nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
+        if window is None:
+            if sinks:
+                raise ValueError("sinks: without a window every key is visible")
+            name, fn, seen = "v4a_latent_attn", lib.v4a_latent_attn, ()
+            nb = lib.v4a_latent_attn_workspace_size(cfg, n_seq, n, max_pos)
+        else:
+            name, fn, seen = "v4a_latent_attn_window", lib.v4a_latent_attn_window, (window, sinks)
+            nb = lib.v4a_latent_attn_window_workspace_size(cfg, n_seq, n, max_pos, window, sinks)
         ws = scratch(nb, q.device, stream)
-        _check("v4a_latent_attn", lib.v4a_latent_attn(
-            cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, q.data_ptr(), byref(cache),
-            out.data_ptr(), None if ws is None else ws.data_ptr(), nb,
+        _check(name, fn(
+            cfg, n_seq, n, cu.data_ptr(), start.data_ptr(), max_pos, *seen, q.data_ptr(),
+            byref(cache), out.data_ptr(), None if ws is None else ws.data_ptr(), nb,
             None if dev_err is None else _word(dev_err, dev),
             _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
@@ -309,10 +338,12 @@ class LatentLayer:
             _current_raw(dev) if stream is None else _raw(stream, dev)))
         return out
 
-    def step(self, cu, start, max_pos, pos, c, k_pe, q, out=None, dev_err=None, stream=None):
+    def step(self, cu, start, max_pos, pos, c, k_pe, q, out=None, dev_err=None, stream=None,
+             window=None, sinks=0):
         """One decode or chunk step: insert the new tokens, rotate the queries' rotary part in
-        place (pos [n]: the new tokens' positions), attend."""
+        place (pos [n]: the new tokens' positions), attend (under a ``window``, if given)."""
         self.insert(cu, start, c, k_pe, dev_err, stream)
         rot = q[..., self.cfg.latent_dim:]
         _rope(self.cfg.rope, rot, pos, rot, False, dev_err, stream)
-        return self.attention(cu, start, max_pos, q, out=out, dev_err=dev_err, stream=stream)
+        return self.attention(cu, start, max_pos, q, out=out, dev_err=dev_err, stream=stream,
+                              window=window, sinks=sinks)

@@ -58,6 +58,7 @@ typedef struct CUstream_st* v4a_stream_t; /* a cudaStream_t; NULL = legacy defau
 #define V4A_DEV_TIMEOUT 16u       /* a bounded wait inside a kernel gave up (about 1 s); the
                                      kernel drained its copies, released its tensor memory and
                                      returned; its outputs are incomplete */
+#define V4A_DEV_NO_PAGE 32u       /* the pool has no free page left for a block that needs one */
 
 /* layer kinds ([notes] 四大核心技术; 数学附录精要) */
 #define V4A_C4A 0                 /* entry = weighted sum of 8 tokens at stride 4 */
@@ -380,13 +381,35 @@ typedef struct v4a_rope_cfg {
   float amplitude;       /* > 0, on cosine and sine alike (1 = a rotation) */
 } v4a_rope_cfg;
 
+/* Cache formats of a latent layer (v4a_latent_cfg.cache_format).
+ * PLAIN: rows of latent_dim + rope.dim elements of the layer's type, no scales.
+ * FP4:   the latent part in 4 bits (latent_dim a multiple of 32), whatever the layer's type. A pool
+ *   row is V4A_LATENT_FP4_ROW_BYTES(latent_dim, rope.dim) bytes: latent_dim / 2 bytes of e2m1 codes
+ *   (element 2i in the low nibble of byte i, codes as for V4A_IDX_FP4), rope.dim f16 numbers h,
+ *   latent_dim / 16 e4m3 block scales B, padding up to a multiple of 16; v4a_cache.scale holds one
+ *   fp32 scale s a row, and v4a_cache.row_width is latent_dim + rope.dim. The row stands for
+ *     s * (B[i / 16] * code_i)  and  s * h_j.
+ *   v4a_latent_insert chooses them in fp32, r = 1 / sqrt(mean(c^2) + rms_eps) (1 without gamma),
+ *   z = gamma * c, k = rope(k_pe):
+ *     u = max|z| * (1 / 2688), s = r * u; where s is below least = max(max|k| / 32768, 2^-100):
+ *     s = least, u = s / r. Then t = z * (1 / u), B = e4m3(max|t| of the block * (1 / 6)),
+ *     code = e2m1(t * (1 / B)) (0 where B = 0), h = f16(k * (1 / s)), all round to nearest even and
+ *     saturating. (2688 = 6 * 448: the row's largest element uses both formats to their ends. The
+ *     rotary part stays in 16 bits: it carries the positions and is a ninth of the row. The row
+ *     scale takes the norm's r, so which code a value gets does not depend on how the mean square
+ *     is summed.) A row with an element that is not finite is not finite. */
+#define V4A_LATENT_PLAIN 0
+#define V4A_LATENT_FP4 1
+#define V4A_LATENT_FP4_ROW_BYTES(latent_dim, rope_dim) \
+  (((latent_dim) / 2 + 2 * (rope_dim) + (latent_dim) / 16 + 15) / 16 * 16)
+
 typedef struct v4a_latent_cfg {
   int32_t dtype;         /* V4A_BF16 or V4A_FP32: inputs, cache and outputs */
   int32_t n_heads;       /* H */
   int32_t latent_dim;    /* C: a multiple of 8, 8 .. 1024 */
   int32_t nope_dim;      /* dims of an expanded key before its rotary part: multiple of 8, .. 256 */
   int32_t v_dim;         /* dims of an expanded value: multiple of 8, 8 .. 256 */
-  int32_t reserved;      /* must be 0 */
+  int32_t cache_format;  /* V4A_LATENT_PLAIN (0) or V4A_LATENT_FP4 */
   float rms_eps;         /* of v4a_latent_insert's norm */
   float softmax_scale;   /* > 0, of both attention forms */
   v4a_rope_cfg rope;     /* rope.dim: a multiple of 8, 8 .. 128 */
@@ -423,7 +446,8 @@ int v4a_rope(const v4a_rope_cfg* rope, int32_t dtype, int32_t n_tokens, int32_t 
  *        [n_tokens, rope.dim], k_stride apart (two parts of one projection's output, say).
  *        Pointers on 16-byte boundaries, strides multiples of 16 bytes.
  * gamma: device fp32 [C], 16-byte aligned, or NULL
- * cache: rows_per_block 256, row_width C + rope.dim, no scales
+ * cache: rows_per_block 256, row_width C + rope.dim, no scales (FP4: rows and scales as stated at
+ *        V4A_LATENT_FP4; a row's padding is left as it was)
  * Tokens without a page or with a position outside [0, V4A_MAX_POS) are not written and set
  * V4A_DEV_MISSING_PAGE / V4A_DEV_BAD_PAGE / V4A_DEV_BAD_POS.
  */
@@ -434,7 +458,8 @@ int v4a_latent_insert(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens
 
 /*
  * v4a_latent_gather — copy cached rows out: out row cu_rows[b] + i = the cache's row of
- * position start_pos[b] + i of sequence b. out: device [n_rows, C + rope.dim], 16-byte
+ * position start_pos[b] + i of sequence b (FP4: the values that it stands for, computed in fp32 and
+ * rounded once to the layer's type). out: device [n_rows, C + rope.dim], 16-byte
  * aligned. A row without a page (or at a negative position) is zeroed and sets
  * V4A_DEV_MISSING_PAGE / V4A_DEV_BAD_PAGE.
  */
@@ -459,6 +484,9 @@ int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows,
  * and may do so to earlier tokens of the same call.
  * bf16 with C = 512 and rope.dim = 64 runs on the tensor cores; other shapes on CUDA cores, about
  * 16 times slower where the products decide (14-17 TFLOP/s for C of 256 and 512, 6 for 128).
+ * FP4 caches: rows are the values that they stand for. On the tensor cores the products take q and
+ * B * code exactly, and each weight times its row's scale is rounded once, to f16 (11 bits down to
+ * 2^-20 of the largest such product of a head so far, fewer below).
  */
 size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                                       int64_t max_pos);
@@ -466,6 +494,22 @@ int v4a_latent_attn(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                     const int32_t* cu_tokens, const int64_t* start_pos, int64_t max_pos,
                     const void* q, const v4a_cache* cache, void* out, void* workspace,
                     size_t workspace_bytes, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_latent_attn_window — v4a_latent_attn in which a token at position p sees, of the keys x <= p,
+ * those of a sliding window and the sequence's first ones:
+ *   x > p - window  or  x < sinks.
+ * Blocks that no token of the call sees into are not looked up: their pages may have been given
+ * back. window >= 1, sinks >= 0; window > max_pos is v4a_latent_attn. The work of a token is
+ * window + sinks keys, whatever its position. Other arguments, numerics and errors as there.
+ */
+size_t v4a_latent_attn_window_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                                             int64_t max_pos, int64_t window, int64_t sinks);
+int v4a_latent_attn_window(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
+                           const int32_t* cu_tokens, const int64_t* start_pos, int64_t max_pos,
+                           int64_t window, int64_t sinks, const void* q, const v4a_cache* cache,
+                           void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                           v4a_stream_t stream);
 
 /*
  * v4a_latent_attn_expanded — latent attention with projected keys and values, for prompts:
@@ -498,6 +542,92 @@ int v4a_latent_attn_expanded(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n
                              int64_t v_token_stride, int64_t v_head_stride, int32_t causal,
                              void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
                              v4a_stream_t stream);
+
+/*
+ * Pages. Pools whose sequences grow together (the layers of a model, say) share one block table and
+ * one count of references per page: refs[page] is the number of the table's entries that name the
+ * page, 0 where it is free. The calls below keep both, and move rows, on the device and in stream
+ * order; what they choose depends on the table and the counts alone (pages are taken lowest number
+ * first), so a run repeats exactly. Nothing is synchronised, and no list of free pages is kept.
+ *
+ * At most V4A_MAX_SEQ rows of a table, V4A_MAX_POOLS pools and 2^23 pages a call. A page of -1 is
+ * none; a table entry outside [-1, n_pages) sets V4A_DEV_BAD_PAGE and is taken for none (v4a_pages_free
+ * clears it). Counts below 0 are taken for 0. workspace: device, >= v4a_pages_workspace_size(table)
+ * bytes, 256-byte aligned; calls share one under the rule of the latent calls. The table, counts and
+ * lists must not overlap one another, the pools or the workspace.
+ */
+#define V4A_MAX_POOLS 64
+
+typedef struct v4a_page_table {
+  int32_t* block_table;  /* device [n_seq, max_blocks] */
+  int32_t* refs;         /* device [n_pages], 16-byte aligned */
+  int32_t n_seq;
+  int32_t max_blocks;
+  int64_t n_pages;
+} v4a_page_table;
+
+typedef struct v4a_pool {
+  void* data;              /* device [n_pages * rows_per_block][row_bytes], 16-byte aligned */
+  float* scale;            /* device fp32 [n_pages * rows_per_block], or NULL */
+  int64_t row_bytes;       /* a positive multiple of 16 */
+  int32_t rows_per_block;  /* 1 .. 256 */
+  int32_t reserved;        /* must be 0 */
+} v4a_pool;
+
+size_t v4a_pages_workspace_size(const v4a_page_table* table);
+
+/*
+ * v4a_pages_free — give back blocks first[b] .. last[b] - 1 of every row b of the table (first,
+ * last: device int32 [n_seq], clamped to [0, max_blocks]; empty where last <= first): each entry
+ * becomes -1 and its page's count falls by 1. A page whose count was 0 sets V4A_DEV_BAD_PAGE and
+ * stays at 0. Contents are left as they are.
+ */
+int v4a_pages_free(const v4a_page_table* table, const int32_t* first, const int32_t* last,
+                   int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_pages_grow — give every block first[b] .. last[b] - 1 of row b that has no page the lowest free
+ * page, in the order of rows and blocks, with a count of 1. Where the free pages do not suffice, the
+ * blocks last in that order stay without one and V4A_DEV_NO_PAGE is set.
+ */
+int v4a_pages_grow(const v4a_page_table* table, const int32_t* first, const int32_t* last,
+                   void* workspace, size_t workspace_bytes, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_pages_fork — row dst[i] of the table takes over the first length[i] positions of row src[i],
+ * for i < n (device int32 [n], int32 [n], int64 [n]; n <= V4A_MAX_SEQ). Blocks wholly inside them
+ * are shared (the same page, its count one higher; -1 stays -1). The block that length[i] cuts gets
+ * the lowest free page, in the order of i, into which the rows of its positions below length[i] are
+ * copied, in every pool (a pool with R rows a block: its first ceil(R * cut / 256)); the page's
+ * other rows are left as they were. So neither row writes into the other's tokens when both go on.
+ * dst's row must hold no page, and its blocks behind length[i] stay without. A row may have several
+ * children. An entry that is not so is left out whole and sets V4A_DEV_BAD_INDEX: a row outside the
+ * table, src == dst, dst named by another entry as src or dst, a dst that holds a page, a length
+ * below 0 or beyond the table. Where no page is left for a cut block it stays without and
+ * V4A_DEV_NO_PAGE is set.
+ */
+int v4a_pages_fork(const v4a_page_table* table, const v4a_pool* pools, int32_t n_pools, int32_t n,
+                   const int32_t* src, const int32_t* dst, const int64_t* length, void* workspace,
+                   size_t workspace_bytes, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_pages_copy — copy whole pages src[i] -> dst[i] (device int32 [n], n <= 2^20) in every pool;
+ * the table is not read. A page that is written may be neither read nor written by another entry.
+ * An entry outside [0, n_pages) is left out and sets V4A_DEV_BAD_PAGE.
+ */
+int v4a_pages_copy(const v4a_page_table* table, const v4a_pool* pools, int32_t n_pools, int32_t n,
+                   const int32_t* src, const int32_t* dst, int32_t* dev_err, v4a_stream_t stream);
+
+/*
+ * v4a_pages_compact — move the used pages to the front: with U used pages (counts above 0), the k-th
+ * used page at or behind U moves to the k-th free page below U, in every pool, and the table and
+ * the counts follow. Pages behind U are then free, so a server may keep (or copy out) the first U.
+ * n_used: device int32 [1], receives U. moved: device int32 [n_pages] or NULL, receives every page's
+ * new number (its own where it stays, -1 where it was free), for holders of pages besides the table.
+ */
+int v4a_pages_compact(const v4a_page_table* table, const v4a_pool* pools, int32_t n_pools,
+                      int32_t* n_used, int32_t* moved, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_err, v4a_stream_t stream);
 
 /* Synchronise `stream`, read the device error word, clear it. *flags_out (may be NULL)
  * receives the bits. Returns V4A_OK, V4A_ERR_DEVICE if any bit was set, or V4A_ERR_CUDA. */
