@@ -671,7 +671,7 @@ cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st) {
   cudaError_t e;
   if (p.plan.tc) {
-    e = launch_latent_attn_tc(p, st);
+    e = p.fp4 ? launch_latent_attn_fp4_tc(p, st) : launch_latent_attn_tc(p, st);
   } else if (p.fp4) {
     e = dtype == V4A_BF16 ? run_gen<__nv_bfloat16, true, true>(p, p.C + p.R, p.C, p.plan.ctas, st)
                           : run_gen<float, true, true>(p, p.C + p.R, p.C, p.plan.ctas, st);

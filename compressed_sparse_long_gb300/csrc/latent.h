@@ -130,6 +130,7 @@ int launch_latent_gather_fp4(const LatentGatherParams& p, int dtype, cudaStream_
 int launch_latent_attn(const LatentAttnParams& p, int dtype, cudaStream_t st);
 int launch_latent_expanded(const LatentExpandedParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_latent_attn_tc(const LatentAttnParams& p, cudaStream_t st);
+cudaError_t launch_latent_attn_fp4_tc(const LatentAttnParams& p, cudaStream_t st);
 cudaError_t launch_latent_expanded_tc(const LatentExpandedParams& p, cudaStream_t st);
 cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream_t st);
 

@@ -118,7 +118,7 @@ int check_batch(int32_t n_seq, int32_t n, const int32_t* cu, const int64_t* star
 }
 
 bool on_tensor_cores(const v4a_latent_cfg* c) {
-  return c->dtype == V4A_BF16 && c->latent_dim == 512 && c->rope.dim == 64 && !is_fp4(c);
+  return c->dtype == V4A_BF16 && c->latent_dim == 512 && c->rope.dim == 64;
 }
 
 // The device counts the steps of a call in 31 bits, sums of two of them included.

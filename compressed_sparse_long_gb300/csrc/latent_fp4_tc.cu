@@ -1,0 +1,736 @@
+// Absorbed latent attention over FP4 rows (512 latent + 64 rotary dims) on tcgen05 tensor cores, f16.
+//
+//   row = s (B code | h): s an fp32 number a key, B an e4m3 number a block of 16; B code and h are f16
+//   S^T = [B code | h] (2^a Q)^T          M = 128 keys, N = 64 rows, K = 576   (36 MMAs)
+//   x = scale log2(e) 2^-a s S^T + log2 s, P^T = 2^(x - m): the weight times its row's scale, f16
+//   O^T += (B code)^T P^T                 M = 4 x 128 dims, N = 64, K = 128 keys (32 MMAs)
+//   l += P / s,  out = O / l
+// Units, teams and the split along the keys are the plain kernel's (LatentWalk). 2^a is a power of two
+// a unit that brings its largest |q| to [2^14, 2^15): bf16 queries are f16 numbers then, but for
+// elements 2^-32 of that and smaller. m is kept where the first tile's largest weight is 2^6 and raised
+// where one would pass 2^15, so f16 has all its bits down to 2^-20 of the largest weight so far.
+//
+// Bound: the products' shared-memory operands and the instructions that expand the codes. If keys and
+// values went through shared memory (as the plain kernel's do), a tile would move 570 KB there, 4400
+// cycles at 128 bytes a cycle, and the products wait for each softmax besides. So both A operands go
+// through tensor memory, which leaves Q and P^T as the only ones in shared memory:
+//   keys:   a thread a key (tensor-memory lane) expands 64 dims of its row at a time, 32 columns
+//   values: a thread four dims (lane l: dims 4l .. 4l + 3, one for each block of 128 of O^T) expands
+//           32 keys of two of them at a time, 2 x 16 columns. Two keys' codes are brought side by side
+//           in a byte first, so one conversion gives a pair of keys.
+// Each has a ring of three slots of 32 columns (O^T 256, S^T 64, rings 192: all 512). The products of
+// the next tile's S^T run before this tile's O^T, so the softmax has both for company.
+//
+// Warps 0-7: softmax and output, as in the plain kernel. Warps 8-11: keys. Warps 12-15: values.
+// Warp 16: products. Warp 17: copies (raw rows, two tiles; scales; Q).
+#include "kernels.h"
+#include "latent.h"
+#include "latent_tc.cuh"
+
+namespace v4a {
+namespace {
+
+constexpr int kNR = 64, kTK = 128, kC = 512, kR = 64;
+constexpr int kRowBytes = V4A_LATENT_FP4_ROW_BYTES(kC, kR), kRopeAt = kC / 2, kBlockAt = kC / 2 + 2 * kR;
+static_assert(kRowBytes == 416 && kRowBytes % 16 == 0, "row chunks");
+constexpr int kThreads = 640;
+constexpr int kQBlock = kNR * 128;
+constexpr int kRaw = kTK * kRowBytes;
+constexpr int kScPitch = kTK + 4;                                // f16: 8 blocks' words in different banks
+constexpr int kOffQ = 0, kOffP = 9 * kQBlock, kOffRaw = kOffP + kTK * 128;
+constexpr int kOffSc = kOffRaw + 2 * kRaw;                       // [3][32 blocks][kScPitch] f16
+constexpr int kOffInfo = kOffSc + 3 * 32 * kScPitch * 2;         // [3][128] float2: s, log2 s
+constexpr int kOffS = kOffInfo + 3 * kTK * 8;                    // [2][128] row scales
+constexpr int kOffF = kOffS + 2 * kTK * 4;
+// floats: red_max[2][64][4] red_sum[64][4] mrow[8 warps][32]
+constexpr int kNFloats = 512 + 256 + 256;
+constexpr int kOffBar = kOffF + kNFloats * 4;
+constexpr int kNBar = 34;
+constexpr int kOffMisc = kOffBar + kNBar * 8;
+constexpr int kSmemBytes = kOffMisc + 256 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(kOffP % 1024 == 0 && kOffRaw % 1024 == 0, "swizzled operands");
+static_assert((V4A_MAX_SEQ + 1) * 4 <= kRaw, "the plan's prefix sums use a raw tile before its first copy");
+constexpr uint32_t kSCol = 0, kOCol = 64, kKCol = 320, kVCol = 416, kTmemCols = 512;
+constexpr int kSlots = 3;
+constexpr float kRoom = -6.0f, kRaise = 12.0f, kOver = 15.0f;    // log2 units: a reference above its maximum,
+                                                                 // what raises it in masked tiles and in others
+// registers of softmax (x2), key, value and other warpgroups: 640 threads x 96 in all
+constexpr int kRegSoftmax = 112, kRegKeys = 88, kRegValues = 120, kRegOther = 48;
+static_assert(2 * kRegSoftmax + kRegKeys + kRegValues + kRegOther <= 5 * 96, "registers of the launch");
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+// Two neighbouring 16-byte chunks of each lane's row. Rows are 26 chunks apart, so lanes r and r + 4
+// would meet in the same banks: every other four lanes take the two in the other order.
+__device__ __forceinline__ void lds_pair(uint32_t a, bool turn, uint4& lo, uint4& hi) {
+  const uint4 x = lds128(a + (turn ? 16 : 0)), y = lds128(a + (turn ? 0 : 16));
+  lo = turn ? y : x;
+  hi = turn ? x : y;
+}
+// Two e4m3 numbers as f16.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(r) : "r"(w));
+  return r;
+}
+
+template <bool kWindow>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_attn_fp4_tc(const __grid_constant__ LatentAttnParams p, const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* qbuf = sm + kOffQ;
+  uint8_t* pbuf = sm + kOffP;
+  uint8_t* raw = sm + kOffRaw;
+  __half* sc = reinterpret_cast<__half*>(sm + kOffSc);
+  float2* info = reinterpret_cast<float2*>(sm + kOffInfo);
+  float* srow = reinterpret_cast<float*>(sm + kOffS);
+  float* red_max = reinterpret_cast<float*>(sm + kOffF);
+  float* red_sum = red_max + 512;
+  float* mrow = red_sum + 256;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
+  uint64_t* rawfull = bars;                                      // [2]
+  uint64_t* rawempty = bars + 2;                                 // [2] by keys' and values' warps
+  uint64_t* kfull = bars + 4;                                    // [3]
+  uint64_t* kempty = bars + 7;                                   // [3]
+  uint64_t* vfull = bars + 10;                                   // [3]
+  uint64_t* vempty = bars + 13;                                  // [3]
+  uint64_t* infofull = bars + 16;                                // [3] block scales and info of a tile
+  uint64_t* qfull = bars + 19;
+  uint64_t* qready = bars + 20;
+  uint64_t* qempty = bars + 21;
+  uint64_t* sfull = bars + 22;
+  uint64_t* sfree = bars + 23;
+  uint64_t* pfull = bars + 24;
+  uint64_t* pvdone = bars + 25;
+  uint64_t* oempty = bars + 26;
+  uint64_t* redb = bars + 27;                                    // [2] one per group of 4 warps
+  uint64_t* qmaxb = bars + 29;
+  uint64_t* done = bars + 30;
+  int* misc = reinterpret_cast<int*>(sm + kOffMisc);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort_flag = misc + 1;
+  volatile int* raised = misc + 2;                               // [2 halves][2 parities] tile + 1
+  volatile int* tile_ok = misc + 6;                              // [2] by raw buffer
+  volatile int* tile_valid = misc + 8;                           // [3] keys of a tile that exist
+  int* qmax = misc + 11;                                         // [8] largest |q| of a warp's chunks, as bits
+  int32_t* warp_tot = misc + 20;                                 // [20]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(rawfull + i, 1);
+      tc::mbar_init(rawempty + i, 8);
+      tc::mbar_init(redb + i, 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      tc::mbar_init(kfull + i, 4);
+      tc::mbar_init(kempty + i, 1);
+      tc::mbar_init(vfull + i, 4);
+      tc::mbar_init(vempty + i, 1);
+      tc::mbar_init(infofull + i, 4);
+    }
+    tc::mbar_init(qfull, 1);
+    tc::mbar_init(qready, 8);
+    tc::mbar_init(qempty, 1);
+    tc::mbar_init(sfull, 1);
+    tc::mbar_init(sfree, 8);
+    tc::mbar_init(pfull, 8);
+    tc::mbar_init(pvdone, 1);
+    tc::mbar_init(oempty, 8);
+    tc::mbar_init(qmaxb, 8);
+    tc::mbar_init(done, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) raised[i] = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 16) {
+    tc::tmem_alloc(tmem_at, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();
+  LatentWalk walk;
+  LatentPiece w;
+  walk.begin(p, reinterpret_cast<int32_t*>(raw), warp_tot);
+  tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_at;
+  const int quad = warp & 3;
+  const int row = quad * 32 + lane;               // TMEM lane: key of S^T; lane l of O^T: dims 4l ..
+  const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax and output
+    tc::set_regs<true, kRegSoftmax>();
+    const int half = warp >> 2;
+    const uint32_t scol = tmem + lane_base + kSCol + half * 32, ocol = tmem + lane_base + kOCol + half * 32;
+    float* mb = mrow + warp * 32;
+    int g = 0, ru = 0, u = 0;
+    bool ok = true;
+    auto group_sync = [&]() -> bool {             // the four warps of this half
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(redb + half);
+      const bool r = tc::mbar_wait(redb + half, ru & 1, abort_flag, p.err);
+      ++ru;
+      return r;
+    };
+    bool posted = false;
+    while (ok && walk.next(p, w)) {
+      if (tid == 0 && !posted) walk.post(p, &w);
+      posted = true;
+      if (w.rows == 0) continue;
+      // lane c: row c of this half, the keys it sees
+      const int my_row = half * 32 + lane;
+      int64_t vis = 0, from = 0;
+      if (my_row < w.rows) {
+        const int64_t pos = w.start + (w.row0 + my_row - w.seq_row0) / p.H;
+        vis = latent_visible(p, pos);
+        if (kWindow) from = latent_from(p, pos);
+        if (quad == 0) latent_report_pos(p, pos);
+      }
+      const int64_t all_from = kWindow ? latent_from(p, w.start + (w.row0 + w.rows - 1 - w.seq_row0) / p.H) : 0;
+      const bool any = w.tile1 > w.tile0;
+      float k2 = p.scale * kLog2e;
+      if (any) {
+        // Q in place from bf16 to f16 times 2^a. (Rows behind the unit's are another's: they take part
+        // in the products, but not in the choice of a; what they give is not looked at.)
+        if (!tc::mbar_wait(qfull, u & 1, abort_flag, p.err)) { ok = false; break; }
+        uint32_t most = 0;
+        for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
+          const int chunk = tid + 256 * i;
+          if (((chunk >> 3) & (kNR - 1)) >= w.rows) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * chunk);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = (e[k] << 16) & 0x7FFF0000u, b = e[k] & 0x7FFF0000u;
+            if (a < 0x7F800000u) most = max(most, a);
+            if (b < 0x7F800000u) most = max(most, b);
+          }
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+          qmax[warp] = (int)most;
+          tc::mbar_arrive(qmaxb);
+        }
+        if (!tc::mbar_wait(qmaxb, u & 1, abort_flag, p.err)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)qmax[i]);
+        // 2^a as a product of two powers (a reaches 140), 2^-a times the softmax's factor the same way
+        const int a = most < 0x00800000u ? (most ? 126 : 0) : 14 + 127 - (int)(most >> 23);
+        const int a0 = a / 2, a1 = a - a0;
+        const float f0 = __uint_as_float((uint32_t)(127 + a0) << 23), f1 = __uint_as_float((uint32_t)(127 + a1) << 23);
+        k2 = k2 * __uint_as_float((uint32_t)(127 - a0) << 23) * __uint_as_float((uint32_t)(127 - a1) << 23);
+        for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (tid + 256 * i));
+          uint4 v = *at;
+          uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            e[k] = pack_f16(__uint_as_float(e[k] << 16) * f0 * f1, __uint_as_float(e[k] & 0xFFFF0000u) * f0 * f1);
+          *at = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(qready);
+        ++u;
+      }
+      // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
+      // row that sees nothing (or is none) infinity
+      float m = -INFINITY;
+      const float none = vis > 0 ? 0.f : INFINITY;
+      __syncwarp();
+      mb[lane] = none;
+      __syncwarp();
+      float l[32];                                // this key lane's sums, by row
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] = 0.f;
+      for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+        const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
+        if (!tc::mbar_wait(infofull + g % 3, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
+        const float2 in = info[(g % 3) * kTK + row];
+        const int valid = tile_valid[g % 3];
+        const float kf = in.x * k2, ls = in.y, is = in.x != 0.f ? __fdividef(1.f, in.x) : 0.f;
+        bool slow = valid < kTK || w.keys0 < x0 + kTK || (kWindow && x0 < all_from && x0 + kTK > p.sinks) ||
+                    __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
+        if (!tc::mbar_wait(sfull, g & 1, abort_flag, p.err)) { ok = false; break; }
+        tc::fence_after_sync();
+        float s[32];
+        tc::tmem_ld32(scol, s);
+        tc::tmem_wait_ld();
+        if (!slow) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(mb + c);
+            s[c] = fmaf(s[c], kf, ls - mv.x);
+            s[c + 1] = fmaf(s[c + 1], kf, ls - mv.y);
+            s[c + 2] = fmaf(s[c + 2], kf, ls - mv.z);
+            s[c + 3] = fmaf(s[c + 3], kf, ls - mv.w);
+            top = fmaxf(top, fmaxf(fmaxf(s[c], s[c + 1]), fmaxf(s[c + 2], s[c + 3])));
+          }
+          const bool over = __any_sync(0xffffffffu, top > kOver);
+          if (lane == 0) {
+            if (over) raised[half * 2 + (g & 1)] = g + 1;
+            tc::mbar_arrive(redb + half);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = fast_exp2(s[c]);
+          if (!tc::mbar_wait(redb + half, ru & 1, abort_flag, p.err)) { ok = false; break; }
+          ++ru;
+          slow = raised[half * 2 + (g & 1)] == g + 1;
+          if (slow) {
+            tc::tmem_ld32(scol, s);
+            tc::tmem_wait_ld();
+          }
+        }
+        // S^T is in registers: the next tile's may be written
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sfree);
+        bool raise = false;
+        float corr = 1.f;
+        if (slow) {
+          const int seen = min((int)max((int64_t)0, min(vis - x0, (int64_t)kTK)), valid);
+          const int begin = kWindow ? (int)max((int64_t)0, min(from - x0, (int64_t)kTK)) : 0;
+          const bool sink = kWindow && x0 + row < p.sinks;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            s[c] = fmaf(s[c], kf, ls);
+            if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
+            if (kWindow && row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
+          }
+          float* rb = red_max + (ru & 1) * 256 + half * 128;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float mc = redux_max(s[c]);
+            if (lane == c) rb[c * 4 + quad] = mc;
+          }
+          if (!group_sync()) { ok = false; break; }
+          const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
+          const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+          if (t == w.tile0) {
+            m = mt + kRoom;
+          } else if (mt > m + kRaise) {
+            corr = fast_exp2(m - (mt + kRoom));   // 0 from -inf
+            m = mt + kRoom;
+          }
+          __syncwarp();
+          mb[lane] = m == -INFINITY ? none : m;
+          raise = t > w.tile0 && __any_sync(0xffffffffu, corr != 1.f);
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(mb + c);
+            s[c] = fast_exp2(s[c] - mv.x);
+            s[c + 1] = fast_exp2(s[c + 1] - mv.y);
+            s[c + 2] = fast_exp2(s[c + 2] - mv.z);
+            s[c + 3] = fast_exp2(s[c + 3] - mv.w);
+          }
+        }
+        // P^T's buffer and the accumulator are the previous tile's products' until they are done
+        if (g > 0 && !tc::mbar_wait(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (raise) {
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) l[c] *= __shfl_sync(0xffffffffu, corr, c);
+#pragma unroll 1
+          for (int b = 0; b < 16; ++b) {          // 8 columns of a block at a time
+            float o[8];
+            const uint32_t at = ocol + (b >> 2) * kNR + (b & 3) * 8;
+            tc::tmem_ld8(at, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] *= __shfl_sync(0xffffffffu, corr, (b & 3) * 8 + c);
+            tc::tmem_st8(at, o);
+          }
+          tc::tmem_wait_st();
+        }
+        // P^T, MN-major [128 keys][64 rows]: this key's half row. A weight times its row's scale is
+        // rounded to f16, the second product's type; the sums take it unrounded.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(pbuf + tc::sw128_off(row, half * 4 + i)) =
+              make_uint4(pack_f16(s[8 * i], s[8 * i + 1]), pack_f16(s[8 * i + 2], s[8 * i + 3]),
+                         pack_f16(s[8 * i + 4], s[8 * i + 5]), pack_f16(s[8 * i + 6], s[8 * i + 7]));
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(pfull);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) l[c] = fmaf(s[c], is, l[c]);
+      }
+      if (!ok) break;
+      // ---- sums over the keys: lane c gets row c's
+      float lsum = 0.f;
+      if (any) {
+        red_sum[(half * 32 + lane) * 4 + quad] = reduce_scatter_sum(l);
+        if (!group_sync()) { ok = false; break; }
+        const float4 v = *reinterpret_cast<const float4*>(red_sum + (half * 32 + lane) * 4);
+        lsum = (v.x + v.y) + (v.z + v.w);
+        if (!tc::mbar_wait(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        tc::fence_after_sync();
+      }
+      const int n_out = min(32, w.rows - half * 32);   // rows of this half (may be <= 0)
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      const int64_t at = (int64_t)w.slot * kNR + half * 32;
+      if (!w.whole && quad == 0) {
+        p.part_ml[(at + lane) * 2] = m;
+        p.part_ml[(at + lane) * 2 + 1] = lsum;
+      }
+      if (any || w.whole) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < 32; c0 += 8) {      // eight rows, four dims each
+          if (c0 >= n_out) break;
+          float o[4][8];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (any) {
+              tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) o[b][c] = 0.f;
+            }
+          }
+          if (any) tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float f = __shfl_sync(0xffffffffu, inv, c0 + c);
+            if (c0 + c >= n_out) continue;        // alike in every lane
+            if (w.whole) {
+              __nv_bfloat162 a = __floats2bfloat162_rn(o[0][c] * f, o[1][c] * f);
+              __nv_bfloat162 b = __floats2bfloat162_rn(o[2][c] * f, o[3][c] * f);
+              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                        (int64_t)(w.row0 + half * 32 + c0 + c) * kC + 4 * row) =
+                  make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+            } else {
+              *reinterpret_cast<float4*>(p.part_o + (at + c0 + c) * kC + 4 * row) =
+                  make_float4(o[0][c], o[1][c], o[2][c], o[3][c]);
+            }
+          }
+        }
+      }
+      if (any) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(oempty);
+      }
+    }
+    if (tid == 0 && !posted) walk.post(p, nullptr);
+  } else if (warp < 12) {
+    // --------------------------------------------------------------------------- keys
+    tc::set_regs<false, kRegKeys>();
+    const bool turn = (lane >> 2) & 1;
+    const uint32_t dst = tmem + lane_base + kKCol;
+    int g = 0, n = 0;                              // tiles, slots
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      const int64_t first_from = kWindow ? latent_from(p, w.start + (w.row0 - w.seq_row0) / p.H) : 0;
+      for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+        const int buf = g & 1, ring = g % 3;
+        if (!tc::mbar_wait(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
+        const int valid = tile_ok[buf] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
+        // a key that no row sees counts for nothing, whatever its row holds
+        const bool dead = row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks);
+        const uint32_t src = tc::smem_u32(raw + buf * kRaw + row * kRowBytes);
+        uint4 b0, b1;
+        lds_pair(src + kBlockAt, turn, b0, b1);
+        const uint32_t bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        {
+          float s = dead ? 0.f : srow[buf * kTK + row];
+          if (!dead && s == 0.f) s = 0x1p-100f;    // (a row of zeros, as the insert writes it)
+          info[ring * kTK + row] = make_float2(s, dead ? 0.f : log2f(s));
+          if (tid == 256) tile_valid[ring] = valid;
+          __half* to = sc + ring * 32 * kScPitch + row;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t h = dead ? 0u : e4m3x2_to_f16x2(bs[j] >> (16 * k));
+              const __half2 v = *reinterpret_cast<const __half2*>(&h);
+              to[(4 * j + 2 * k) * kScPitch] = __low2half(v);
+              to[(4 * j + 2 * k + 1) * kScPitch] = __high2half(v);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(infofull + ring);
+#pragma unroll
+        for (int j = 0; j < 9; ++j, ++n) {
+          uint32_t o[32];
+          if (j < 8) {                             // 64 latent dims
+            uint4 c0, c1;
+            lds_pair(src + 32 * j, turn, c0, c1);
+            const uint32_t code[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t h = e4m3x2_to_f16x2(bs[j] >> (16 * (k >> 1)));
+              const uint32_t f = __byte_perm(h, 0, k & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint32_t v[4];
+                e2m1x8_to_f16(code[2 * k + q], v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[8 * k + 4 * q + i] = mul_f16(v[i], f);
+              }
+            }
+          } else {                                 // the rotary part
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 c0, c1;
+              lds_pair(src + kRopeAt + 32 * k, turn, c0, c1);
+              const uint32_t v[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[8 * k + i] = v[i];
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(rawempty + buf);
+          }
+          const int slot = n % kSlots;
+          if (ok && n >= kSlots) ok = tc::mbar_wait(kempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
+          tc::fence_after_sync();
+          tc::tmem_st32(dst + slot * 32, o);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(kfull + slot);
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------------------- values
+    tc::set_regs<true, kRegValues>();
+    const uint32_t dst = tmem + lane_base + kVCol;
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+    int g = 0, n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+        const int buf = g & 1, ring = g % 3;
+        if (!tc::mbar_wait(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        const uint32_t src = tc::smem_u32(raw + buf * kRaw + 2 * row);
+        uint32_t c0[32], c1[32];                   // this thread's codes of keys 4i, 4i + 2 and 4i + 1, 4i + 3
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          c0[i] = lds16(src + (4 * i) * kRowBytes) | lds16(src + (4 * i + 2) * kRowBytes) << 16;
+          c1[i] = lds16(src + (4 * i + 1) * kRowBytes) | lds16(src + (4 * i + 3) * kRowBytes) << 16;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(rawempty + buf);
+        if (!tc::mbar_wait(infofull + ring, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
+        const uint32_t scales = tc::smem_u32(sc + (ring * 32 + row / 4) * kScPitch);
+#pragma unroll
+        for (int j = 0; j < 8; ++j, ++n) {         // keys 32 (j / 2) .., dims 4 row + j % 2 and + 2 more
+          uint32_t o[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = 8 * (j >> 1) + i;
+            const uint32_t pair = j & 1 ? ((c0[k] >> 4) & kLow) | (c1[k] & ~kLow)
+                                        : (c0[k] & kLow) | ((c1[k] << 4) & ~kLow);
+            uint32_t v[4];                         // (dim, keys 0 1), (dim + 2, keys 0 1), the same of 2 3
+            e2m1x8_to_f16(pair, v);
+            const uint2 f = lds64(scales + 8 * k);
+            o[2 * i] = mul_f16(v[0], f.x);
+            o[2 * i + 1] = mul_f16(v[2], f.y);
+            o[16 + 2 * i] = mul_f16(v[1], f.x);
+            o[16 + 2 * i + 1] = mul_f16(v[3], f.y);
+          }
+          const int slot = n % kSlots;
+          if (ok && n >= kSlots) ok = tc::mbar_wait(vempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
+          tc::fence_after_sync();
+          tc::tmem_st32(dst + slot * 32, o);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(vfull + slot);
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    tc::set_regs<false, kRegOther>();
+    if (warp == 17 && lane == 0) {
+      // ---------------------------------------------------------------------- copies
+      int g = 0, u = 0, nq = 0, nr[2] = {0, 0};    // phases of each barrier given copies
+      bool ok = true;
+      const uint8_t* data = reinterpret_cast<const uint8_t*>(p.cache.data);
+      while (ok && walk.next(p, w)) {
+        if (w.tile0 >= w.tile1) continue;
+        // the first raw tile does not wait for Q's buffer
+        bool asked = false;
+        auto ask_q = [&]() {
+          asked = true;
+          if (u > 0 && !tc::mbar_wait(qempty, (u - 1) & 1, abort_flag, p.err)) return false;
+          tc::mbar_arrive_tx(qfull, 9 * kQBlock);
+          ++nq;
+          for (int b = 0; b < 9; ++b) tma_2d(qbuf + b * kQBlock, &qmap, b * 128, w.row0, qfull);
+          return true;
+        };
+        for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+          const int buf = g & 1;
+          const int64_t slot = tile_slot(p, w.seq, w.tile_at<kWindow>(t), kTK);
+          const bool have = slot >= 0;
+          if (!have) slot_ok(slot, p.err);
+          if (!asked && u == 0 && !ask_q()) { ok = false; break; }
+          if (g >= 2 && !tc::mbar_wait(rawempty + buf, ((g >> 1) - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+          tile_ok[buf] = have;
+          ++nr[buf];
+          if (have) {
+            tc::mbar_arrive_tx(rawfull + buf, kRaw + kTK * 4);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i)
+              tc::bulk_g2s(raw + buf * kRaw + i * (kRaw / 4), data + slot * kRowBytes + i * (kRaw / 4), kRaw / 4,
+                           rawfull + buf);
+            tc::bulk_g2s(srow + buf * kTK, p.cache.scale + slot, kTK * 4, rawfull + buf);
+          } else {
+            tc::mbar_arrive(rawfull + buf);
+          }
+          if (!asked && !ask_q()) { ok = false; break; }
+          if (t + 1 < w.tile1) {             // the next tile's rows into L2
+            const int64_t ahead = tile_slot(p, w.seq, w.tile_at<kWindow>(t + 1), kTK);
+            if (ahead >= 0) {
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(data + ahead * kRowBytes +
+                                                                               i * (kRaw / 4)),
+                             "r"(kRaw / 4)
+                             : "memory");
+            }
+          }
+        }
+        ++u;
+      }
+      if (*abort_flag) {                          // leave no copy in flight
+        if (nq > 0) tc::mbar_wait_drain(qfull, (nq - 1) & 1);
+        for (int i = 0; i < 2; ++i)
+          if (nr[i] > 0) tc::mbar_wait_drain(rawfull + i, (nr[i] - 1) & 1);
+      }
+    } else if (warp == 16) {
+      // -------------------------------------------------------------------- products
+      constexpr uint32_t idesc_s = tc::idesc_f16(kTK, kNR);
+      constexpr uint32_t idesc_o = tc::idesc_f16(128, kNR, false, true);
+      const uint32_t q_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(qbuf)), 16);
+      const uint32_t p_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(pbuf)), 16);
+      const uint32_t base = tc::uniform(tmem);
+      int u = 0, gs = 0, gv = 0, nk = 0, nv = 0;  // units, tiles of each product, slots of each ring
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, p.err));
+      };
+      auto logits = [&](bool last) -> bool {       // S^T of tile gs
+        if (gs > 0 && !wait_all(sfree, (gs - 1) & 1)) return false;
+#pragma unroll 1
+        for (int j = 0; j < 9; ++j, ++nk) {
+          const int slot = nk % kSlots;
+          if (!wait_all(kfull + slot, (nk / kSlots) & 1)) return false;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)            // 16 dims, 8 columns of A, 32 bytes of B
+              tc::mma_ta_lo<idesc_s>(base + kSCol, base + kKCol + slot * 32 + 8 * s,
+                                     q_lo + ((j * kQBlock) >> 4) + 2 * s, (j | s) ? 1u : 0u);
+            tc::mma_commit(kempty + slot);
+            if (j == 8) {
+              tc::mma_commit(sfull);
+              if (last) tc::mma_commit(qempty);
+            }
+          }
+          __syncwarp();
+        }
+        ++gs;
+        return true;
+      };
+      while (ok && walk.next(p, w)) {
+        if (w.tile0 >= w.tile1) continue;
+        if (!wait_all(qready, u & 1)) break;
+        tc::fence_after_sync();
+        if (!logits(w.tile0 + 1 == w.tile1)) break;
+        for (int t = w.tile0; t < w.tile1; ++t, ++gv) {
+          if (t + 1 < w.tile1 && !logits(t + 2 == w.tile1)) { ok = false; break; }
+          if (!wait_all(pfull, gv & 1)) { ok = false; break; }
+          if (t == w.tile0 && u > 0 && !wait_all(oempty, (u - 1) & 1)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint32_t acc = tc::uniform(t > w.tile0);
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j, ++nv) {
+            const int slot = nv % kSlots;
+            if (!wait_all(vfull + slot, (nv / kSlots) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              const uint32_t a = base + kVCol + slot * 32;
+              const uint32_t d = base + kOCol + (j & 1) * kNR;
+              const uint32_t b = p_lo + (((j >> 1) * 2 * 2048) >> 4);
+              const uint32_t add = j < 2 ? acc : 1u;
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {        // 16 keys, 8 columns of A, 2 KB of B
+                tc::mma_ta_lo<idesc_o>(d, a + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
+                tc::mma_ta_lo<idesc_o>(d + 2 * kNR, a + 16 + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
+              }
+              tc::mma_commit(vempty + slot);
+              if (j == 7) tc::mma_commit(pvdone);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        ++u;
+      }
+      if (tc::elect_one()) {
+        tc::mma_commit(done);
+        tc::mbar_wait_drain(done, 0);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 16) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attn_fp4_tc(const LatentAttnParams& p, cudaStream_t st) {
+  CUtensorMap qmap;
+  const int64_t rows = (int64_t)p.n_tokens * p.H;
+  if (!encode_byte_rows_map(&qmap, p.q, (uint64_t)rows, (kC + kR) * 2, 128, kNR)) return cudaErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)p.plan.ctas), dim3(kThreads), kSmemBytes, st, p, qmap);
+  };
+  return p.window > 0 ? go(latent_attn_fp4_tc<true>) : go(latent_attn_fp4_tc<false>);
+}
+
+}  // namespace v4a

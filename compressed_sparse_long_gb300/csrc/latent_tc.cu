@@ -29,7 +29,7 @@
 // next tile requested into L2 a tile ahead. Warp 9: products.
 #include "kernels.h"
 #include "latent.h"
-#include "tc.cuh"
+#include "latent_tc.cuh"
 
 namespace v4a {
 namespace {
@@ -48,61 +48,13 @@ constexpr int kSmemBytes = kOffMisc + 192 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kKBlock, "the plan's prefix sums use a key block before its first copy");
 constexpr uint32_t kSCol = 0, kOCol = 64, kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRoom = 16.0f, kRaise = -8.0f;                   // log2 units: a reference above its maximum;
                                                                  // a weight that raises it
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
-  tc::tmem_st32(taddr, u);
-}
-
-// Sum of v[c] over the 32 lanes; lane c ends with column c's.
-__device__ __forceinline__ float reduce_scatter_sum(const float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-  float a[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) a[i] = v[i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const float send = up ? a[j] : a[j + o], keep = up ? a[j + o] : a[j];
-      a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return a[0];
-}
-
-// Pool row of the first key of a tile, or a negative number when its page is missing or bad.
-__device__ __forceinline__ int64_t tile_slot(const LatentAttnParams& p, int seq, int64_t tile) {
-  return slot_of(p.cache, seq, tile * kTK);
-}
-
 // kWindow: tokens see a window and the first keys (p.window, p.sinks).
 template <bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -416,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
         for (int b = 0; b < 9; ++b) tma_2d(qbuf + b * kQBlock, &qmap, b * 128, w.row0, qfull);
         for (int t = w.tile0; t < w.tile1; ++t, ++g) {
-          const int64_t slot = tile_slot(p, w.seq, w.tile_at<kWindow>(t));
+          const int64_t slot = tile_slot(p, w.seq, w.tile_at<kWindow>(t), kTK);
           const bool have = slot >= 0;
           if (!have) slot_ok(slot, p.err);
 #pragma unroll
@@ -444,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive(xfull);
           }
           if (t + 1 < w.tile1) {             // the next tile's rows into L2
-            const int64_t ahead = tile_slot(p, w.seq, w.tile_at<kWindow>(t + 1));
+            const int64_t ahead = tile_slot(p, w.seq, w.tile_at<kWindow>(t + 1), kTK);
             if (ahead >= 0) {
               const uint8_t* rows = reinterpret_cast<const uint8_t*>(p.cache.data) + ahead * (kW * 2);
 #pragma unroll 1
