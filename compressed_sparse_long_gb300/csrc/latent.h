@@ -70,7 +70,8 @@ struct LatentGatherParams {
 // there the device decides.
 constexpr int32_t kSplitNone = 0, kSplitAll = 1, kSplitOnDevice = 2;
 struct LatentPlan {
-  int32_t NR, TK;
+  int32_t NR, TK;                     // powers of two
+  int32_t nr_shift, tk_shift;         // and their logarithms
   int32_t max_U;
   int32_t ctas;                       // of the launch, a multiple of max_U
   int32_t split;                      // kSplit*; the workspace and the merge go with all but None
@@ -79,6 +80,12 @@ struct LatentPlan {
   int32_t tc;                         // tensor-core kernel
 };
 
+// The most tiles that the windows of a unit's tokens reach into together, wherever they begin.
+inline int64_t most_window_tiles(int64_t window, int NR, int TK, int H) {
+  const int64_t tokens = (NR + H - 2) / H + 1;
+  return (window + tokens + TK - 3) / TK + 1;
+}
+
 struct LatentAttnParams {
   int32_t n_seq, n_tokens, H, C, R;   // R = rotary dims
   float scale;
@@ -86,6 +93,7 @@ struct LatentAttnParams {
   int64_t end;                        // no key is at or behind it: max_pos + 1 and the table's reach
   int64_t window, sinks;              // of the keys up to its own a token sees the last `window` and
                                       // the first `sinks` (window 0: all)
+  int64_t window_tiles;               // the most tiles that any unit's windows reach into
   int32_t fp4;                        // rows in 4 bits; the cache's width is a row's bytes
   const int32_t* cu;
   const int64_t* start;
@@ -237,13 +245,6 @@ __device__ __forceinline__ int64_t latent_from(const LatentAttnParams& p, int64_
   return max((int64_t)0, pos + 1 - p.window);
 }
 
-// Tiles of the sinks, and the most of them that any unit walks under a window: its tokens' windows
-// together, wherever they begin. (Also on the host, where the workspace is sized.)
-__host__ __device__ __forceinline__ int64_t window_tiles(int64_t window, int64_t sinks, int NR, int TK, int H) {
-  const int64_t tokens = (NR + H - 2) / H + 1;
-  return (sinks + TK - 1) / TK + (window + tokens + TK - 3) / TK + 1;
-}
-
 // One sequence's part of the plan.
 struct LatentSeq {
   int row0;          // first row of the batch's (token, head) rows
@@ -252,7 +253,7 @@ struct LatentSeq {
   int tiles;         // key tiles of the whole sequence, at most those of any unit's windows (1 in
                      // whole-unit plans)
   int64_t start;     // position of its first new token
-  __device__ __forceinline__ int shares(int U) const { return (units + U - 1) / U; }
+  __device__ __forceinline__ int shares(int U) const { return (units + U - 1) >> (U >> 1); }   // U: 1, 2, 4
   __device__ __forceinline__ int pairs(int U) const { return shares(U) * tiles; }
 };
 
@@ -263,11 +264,11 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int b
   s.row0 = a * p.H;
   s.rows = n * p.H;
   s.start = __ldg(p.start + b);
-  s.units = (s.rows + p.plan.NR - 1) / p.plan.NR;
+  s.units = (s.rows + p.plan.NR - 1) >> p.plan.nr_shift;
   const int64_t keys = min(s.start + n, p.end);
-  s.tiles = !split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) / p.plan.TK);
+  s.tiles = !split || keys <= 0 ? 1 : (int)((keys + p.plan.TK - 1) >> p.plan.tk_shift);
   if (p.window > 0 && s.tiles > 1)
-    s.tiles = (int)min((int64_t)s.tiles, window_tiles(p.window, min(p.sinks, keys), p.plan.NR, p.plan.TK, p.H));
+    s.tiles = (int)min((int64_t)s.tiles, p.window_tiles + ((min(p.sinks, keys) + p.plan.TK - 1) >> p.plan.tk_shift));
   return s;
 }
 
@@ -323,7 +324,7 @@ __device__ __forceinline__ bool latent_split(const LatentAttnParams& p, int32_t*
   for (int b = threadIdx.x; b < p.n_seq; b += blockDim.x) {
     const LatentSeq s = latent_seq(p, b, true);
     if (s.units == 0) continue;
-    const int first = (int)min((int64_t)s.tiles, (latent_visible(p, s, 0) + p.plan.TK - 1) / p.plan.TK);
+    const int first = (int)min((int64_t)s.tiles, (latent_visible(p, s, 0) + p.plan.TK - 1) >> p.plan.tk_shift);
     sees += s.units * ((first + s.tiles + 1) / 2);
     line += s.units * s.tiles;
     longest = max(longest, s.tiles);
@@ -423,9 +424,9 @@ struct LatentWalk {
     U = latent_prefix(p, split, pre, warp_tot);
     cta = blockIdx.x;
     const int total = pre[p.n_seq];
-    team = cta / U;
-    member = cta % U;
-    const int teams = (split ? p.plan.split_ctas : p.plan.ctas) / U;
+    team = cta >> (U >> 1);
+    member = cta & (U - 1);
+    const int teams = (split ? p.plan.split_ctas : p.plan.ctas) >> (U >> 1);
     per = latent_per_team(total, teams);
     if (!split) {                  // whole shares in turn, the teams striding over them
       n = teams;
@@ -465,11 +466,11 @@ struct LatentWalk {
     w.rows = max(0, min(p.plan.NR, s.rows - ur));
     w.keys = w.rows > 0 ? latent_visible(p, s, (ur + w.rows - 1) / p.H) : 0;
     w.keys0 = w.rows > 0 ? latent_visible(p, s, ur / p.H) : 0;
-    int unit_tiles = (int)((w.keys + p.plan.TK - 1) / p.plan.TK);
+    int unit_tiles = (int)((w.keys + p.plan.TK - 1) >> p.plan.tk_shift);
     w.sink_tiles = w.skip = 0;
     if (p.window > 0) {
-      const int64_t from = latent_from(p, s.start + ur / p.H) / p.plan.TK;
-      w.sink_tiles = (int)((min(p.sinks, w.keys) + p.plan.TK - 1) / p.plan.TK);
+      const int64_t from = latent_from(p, s.start + ur / p.H) >> p.plan.tk_shift;
+      w.sink_tiles = (int)((min(p.sinks, w.keys) + p.plan.TK - 1) >> p.plan.tk_shift);
       w.skip = (int)max((int64_t)0, min(from, (int64_t)unit_tiles) - w.sink_tiles);
       unit_tiles -= w.skip;
     }

@@ -132,14 +132,16 @@ bool make_plan(const v4a_latent_cfg* c, int32_t n_seq, int32_t n_tokens, int64_t
   pl->tc = tc;
   pl->NR = tc ? 64 : 16;
   pl->TK = tc ? 128 : 32;
+  pl->nr_shift = tc ? 6 : 4;
+  pl->tk_shift = tc ? 7 : 5;
   const int64_t rows = (int64_t)n_tokens * c->n_heads;
   const int64_t units = (rows + pl->NR - 1) / pl->NR + n_seq;   // at most, over the sequences
   int64_t tiles = max_pos / pl->TK + 1;
   if (rows > INT32_MAX / 2) return false;
   if (window > 0) {
     if (tiles >= kMostSteps) return false;       // tiles are numbered in 31 bits
-    const int64_t walked = window_tiles(window < max_pos ? window : max_pos, sinks < max_pos ? sinks : max_pos,
-                                        pl->NR, pl->TK, c->n_heads);
+    const int64_t walked = most_window_tiles(window, pl->NR, pl->TK, c->n_heads) +
+                           (sinks < max_pos ? sinks / pl->TK + 1 : tiles);
     if (walked < tiles) tiles = walked;
   }
   // sharing key tiles pays where an average sequence has several units (the device decides)
@@ -236,6 +238,7 @@ int attn_call(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens, const 
   p.window = window;
   p.sinks = window > 0 ? sinks : 0;
   p.fp4 = is_fp4(cfg);
+  p.window_tiles = window > 0 ? most_window_tiles(window, p.plan.NR, p.plan.TK, cfg->n_heads) : 0;
   const int64_t reach = (int64_t)cache->max_blocks * kBlock;
   p.end = max_pos + 1 < reach ? max_pos + 1 : reach;
   p.cu = cu_tokens;

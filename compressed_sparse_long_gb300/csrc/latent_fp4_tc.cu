@@ -10,19 +10,28 @@
 // elements 2^-32 of that and smaller. m is kept where the first tile's largest weight is 2^6 and raised
 // where one would pass 2^15, so f16 has all its bits down to 2^-20 of the largest weight so far.
 //
-// Bound: the products' shared-memory operands and the instructions that expand the codes. If keys and
-// values went through shared memory (as the plain kernel's do), a tile would move 570 KB there, 4400
-// cycles at 128 bytes a cycle, and the products wait for each softmax besides. So both A operands go
-// through tensor memory, which leaves Q and P^T as the only ones in shared memory:
+// If keys and values went through shared memory, as the plain kernel's do, a tile would move 570 KB
+// there, 4400 cycles at 128 bytes a cycle, and the products would wait for each softmax. So both A
+// operands go through tensor memory (a product of M = 128, N = 64 then takes 33 cycles, not 49):
 //   keys:   a thread a key (tensor-memory lane) expands 64 dims of its row at a time, 32 columns
 //   values: a thread four dims (lane l: dims 4l .. 4l + 3, one for each block of 128 of O^T) expands
 //           32 keys of two of them at a time, 2 x 16 columns. Two keys' codes are brought side by side
 //           in a byte first, so one conversion gives a pair of keys.
-// Each has a ring of three slots of 32 columns (O^T 256, S^T 64, rings 192: all 512). The products of
-// the next tile's S^T run before this tile's O^T, so the softmax has both for company.
+// Each has a ring of three slots of 32 columns (O^T 256, S^T 64, rings 192: all 512), and S^T of the
+// next tile runs beside this tile's softmax and O^T.
 //
-// Warps 0-7: softmax and output, as in the plain kernel. Warps 8-11: keys. Warps 12-15: values.
-// Warp 16: products. Warp 17: copies (raw rows, two tiles; scales; Q).
+// Warps 0-7: softmax and output, as in the plain kernel. Warps 8-15: keys, two warpgroups taking slots
+// in turn. Warps 16-23: values, a warpgroup for each of the two dims. Warps 24 and 26: products, one for
+// each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles; scales;
+// Q).
+//
+// Bound: instructions. A tile takes about 17,000 warp instructions (each code is expanded twice), four
+// schedulers issue 0.55 a cycle between instruction-cache misses: 28 warps in six roles do not fit the
+// small caches, which is why loops over slots are rolled and waits are short. 32 sequences x 32768
+// tokens, 64 heads: 230 us with the merge (640 TFLOP/s); 16 of 4616-108051, 128 heads: 265 us. On the
+// way: one warpgroup a role 276 us, unrolled loops 431. Codes expanded once, from registers, keys to
+// tensor memory and values to shared memory: 319 us (the values' stores wait while O^T's products read
+// shared memory).
 #include "kernels.h"
 #include "latent.h"
 #include "latent_tc.cuh"
@@ -33,7 +42,7 @@ namespace {
 constexpr int kNR = 64, kTK = 128, kC = 512, kR = 64;
 constexpr int kRowBytes = V4A_LATENT_FP4_ROW_BYTES(kC, kR), kRopeAt = kC / 2, kBlockAt = kC / 2 + 2 * kR;
 static_assert(kRowBytes == 416 && kRowBytes % 16 == 0, "row chunks");
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kQBlock = kNR * 128;
 constexpr int kRaw = kTK * kRowBytes;
 constexpr int kScPitch = kTK + 4;                                // f16: 8 blocks' words in different banks
@@ -42,12 +51,13 @@ constexpr int kOffSc = kOffRaw + 2 * kRaw;                       // [3][32 block
 constexpr int kOffInfo = kOffSc + 3 * 32 * kScPitch * 2;         // [3][128] float2: s, log2 s
 constexpr int kOffS = kOffInfo + 3 * kTK * 8;                    // [2][128] row scales
 constexpr int kOffF = kOffS + 2 * kTK * 4;
-// floats: red_max[2][64][4] red_sum[64][4] mrow[8 warps][32]
-constexpr int kNFloats = 512 + 256 + 256;
+// floats: red_max[2][64][4] (red_sum[64][4] in the half that is not in use) mrow[8 warps][32]
+constexpr int kNFloats = 512 + 256;
 constexpr int kOffBar = kOffF + kNFloats * 4;
 constexpr int kNBar = 34;
 constexpr int kOffMisc = kOffBar + kNBar * 8;
-constexpr int kSmemBytes = kOffMisc + 256 + 1024;
+constexpr int kOffWalk = kOffMisc + 256;
+constexpr int kSmemBytes = kOffWalk + kThreads / 32 * (int)sizeof(LatentWalk) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert(kOffP % 1024 == 0 && kOffRaw % 1024 == 0, "swizzled operands");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kRaw, "the plan's prefix sums use a raw tile before its first copy");
@@ -55,9 +65,9 @@ constexpr uint32_t kSCol = 0, kOCol = 64, kKCol = 320, kVCol = 416, kTmemCols = 
 constexpr int kSlots = 3;
 constexpr float kRoom = -6.0f, kRaise = 12.0f, kOver = 15.0f;    // log2 units: a reference above its maximum,
                                                                  // what raises it in masked tiles and in others
-// registers of softmax (x2), key, value and other warpgroups: 640 threads x 96 in all
-constexpr int kRegSoftmax = 112, kRegKeys = 88, kRegValues = 120, kRegOther = 48;
-static_assert(2 * kRegSoftmax + kRegKeys + kRegValues + kRegOther <= 5 * 96, "registers of the launch");
+// registers of softmax, key and value (two each) and other warpgroups: 896 threads x 72 in all
+constexpr int kRegSoftmax = 104, kRegKeys = 56, kRegValues = 72, kRegOther = 40;
+static_assert(2 * (kRegSoftmax + kRegKeys + kRegValues) + kRegOther <= 7 * 72, "registers of the launch");
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   __half2 v = __floats2half2_rn(a, b);
@@ -83,13 +93,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
-// Two neighbouring 16-byte chunks of each lane's row. Rows are 26 chunks apart, so lanes r and r + 4
-// would meet in the same banks: every other four lanes take the two in the other order.
-__device__ __forceinline__ void lds_pair(uint32_t a, bool turn, uint4& lo, uint4& hi) {
-  const uint4 x = lds128(a + (turn ? 16 : 0)), y = lds128(a + (turn ? 0 : 16));
-  lo = turn ? y : x;
-  hi = turn ? x : y;
-}
 // Two e4m3 numbers as f16.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;
@@ -109,8 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* info = reinterpret_cast<float2*>(sm + kOffInfo);
   float* srow = reinterpret_cast<float*>(sm + kOffS);
   float* red_max = reinterpret_cast<float*>(sm + kOffF);
-  float* red_sum = red_max + 512;
-  float* mrow = red_sum + 256;
+  float* mrow = red_max + 512;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
   uint64_t* rawfull = bars;                                      // [2]
   uint64_t* rawempty = bars + 2;                                 // [2] by keys' and values' warps
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* oempty = bars + 26;
   uint64_t* redb = bars + 27;                                    // [2] one per group of 4 warps
   uint64_t* qmaxb = bars + 29;
-  uint64_t* done = bars + 30;
+  uint64_t* done = bars + 30;                                    // [2] of the products' two warps
   int* misc = reinterpret_cast<int*>(sm + kOffMisc);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(rawfull + i, 1);
-      tc::mbar_init(rawempty + i, 8);
+      tc::mbar_init(rawempty + i, 16);
       tc::mbar_init(redb + i, 4);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -163,19 +165,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(oempty, 8);
     tc::mbar_init(qmaxb, 8);
     tc::mbar_init(done, 1);
+    tc::mbar_init(done + 1, 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) raised[i] = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 16) {
+  if (warp == 24) {
     tc::tmem_alloc(tmem_at, kTmemCols);
     tc::tmem_relinquish();
   }
   pdl_wait();
+  // (the walk's place is kept in shared memory, a copy a warp: it is wanted once a piece)
+  LatentWalk* const place = reinterpret_cast<LatentWalk*>(sm + kOffWalk) + warp;
   LatentWalk walk;
   LatentPiece w;
   walk.begin(p, reinterpret_cast<int32_t*>(raw), warp_tot);
   tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
+  if (lane == 0) *place = walk;
+  auto next = [&]() -> bool {                     // by whole warps
+    LatentWalk at = *place;
+    __syncwarp();
+    const bool more = at.next(p, w);
+    if (lane == 0) *place = at;
+    __syncwarp();
+    return more;
+  };
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -195,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto group_sync = [&]() -> bool {             // the four warps of this half
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(redb + half);
-      const bool r = tc::mbar_wait(redb + half, ru & 1, abort_flag, p.err);
+      const bool r = tc::mbar_wait_few(redb + half, ru & 1, abort_flag, p.err);
       ++ru;
       return r;
     };
     bool posted = false;
-    while (ok && walk.next(p, w)) {
-      if (tid == 0 && !posted) walk.post(p, &w);
+    while (ok && next()) {
+      if (tid == 0 && !posted) place->post(p, &w);
       posted = true;
       if (w.rows == 0) continue;
       // lane c: row c of this half, the keys it sees
@@ -219,18 +233,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) {
         // Q in place from bf16 to f16 times 2^a. (Rows behind the unit's are another's: they take part
         // in the products, but not in the choice of a; what they give is not looked at.)
-        if (!tc::mbar_wait(qfull, u & 1, abort_flag, p.err)) { ok = false; break; }
-        uint32_t most = 0;
+        if (!tc::mbar_wait_few(qfull, u & 1, abort_flag, p.err)) { ok = false; break; }
+        // (a thread's chunks are 16 bytes of one row in each of 18 places: row tid / 8 or 32 + tid / 8)
+        __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 6
         for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
-          const int chunk = tid + 256 * i;
-          if (((chunk >> 3) & (kNR - 1)) >= w.rows) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * chunk);
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          if ((i & 1) * 32 + (tid >> 3) >= w.rows) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * (tid + 256 * i));
+          const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = (e[k] << 16) & 0x7FFF0000u, b = e[k] & 0x7FFF0000u;
-            if (a < 0x7F800000u) most = max(most, a);
-            if (b < 0x7F800000u) most = max(most, b);
+          for (int k = 0; k < 4; ++k) top2 = __hmax2(top2, __habs2(e[k]));
+        }
+        const uint32_t two = *reinterpret_cast<const uint32_t*>(&top2);
+        uint32_t most = max(two << 16, two & 0xFFFF0000u);
+        if (most >= 0x7F800000u) {                 // infinities among them: the largest of the others
+          most = 0;
+#pragma unroll 1
+          for (int i = 0; i < 9 * kNR * 8 / 256 * 8; ++i) {
+            const uint32_t at = 16 * (tid + 256 * (i >> 3)) + 2 * (i & 7);
+            const uint32_t a = (uint32_t)(*reinterpret_cast<const uint16_t*>(qbuf + at) & 0x7FFF) << 16;
+            if (((i >> 3) & 1) * 32 + (tid >> 3) < w.rows && a < 0x7F800000u) most = max(most, a);
           }
         }
         most = __reduce_max_sync(0xffffffffu, most);
@@ -238,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           qmax[warp] = (int)most;
           tc::mbar_arrive(qmaxb);
         }
-        if (!tc::mbar_wait(qmaxb, u & 1, abort_flag, p.err)) { ok = false; break; }
+        if (!tc::mbar_wait_few(qmaxb, u & 1, abort_flag, p.err)) { ok = false; break; }
 #pragma unroll
         for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)qmax[i]);
         // 2^a as a product of two powers (a reaches 140), 2^-a times the softmax's factor the same way
@@ -246,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int a0 = a / 2, a1 = a - a0;
         const float f0 = __uint_as_float((uint32_t)(127 + a0) << 23), f1 = __uint_as_float((uint32_t)(127 + a1) << 23);
         k2 = k2 * __uint_as_float((uint32_t)(127 - a0) << 23) * __uint_as_float((uint32_t)(127 - a1) << 23);
+#pragma unroll 3
         for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
           uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (tid + 256 * i));
           uint4 v = *at;
@@ -272,17 +295,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 32; ++c) l[c] = 0.f;
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
-        if (!tc::mbar_wait(infofull + g % 3, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (!tc::mbar_wait_few(infofull + g % 3, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
         const float2 in = info[(g % 3) * kTK + row];
         const int valid = tile_valid[g % 3];
         const float kf = in.x * k2, ls = in.y, is = in.x != 0.f ? __fdividef(1.f, in.x) : 0.f;
         bool slow = valid < kTK || w.keys0 < x0 + kTK || (kWindow && x0 < all_from && x0 + kTK > p.sinks) ||
                     __any_sync(0xffffffffu, m == -INFINITY && vis > 0);
-        if (!tc::mbar_wait(sfull, g & 1, abort_flag, p.err)) { ok = false; break; }
+        if (!tc::mbar_wait_few(sfull, g & 1, abort_flag, p.err)) { ok = false; break; }
         tc::fence_after_sync();
         float s[32];
         tc::tmem_ld32(scol, s);
         tc::tmem_wait_ld();
+        // S^T is in registers: the next tile's may be written
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sfree);
         if (!slow) {
           float top = -INFINITY;
 #pragma unroll
@@ -294,25 +321,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             s[c + 3] = fmaf(s[c + 3], kf, ls - mv.w);
             top = fmaxf(top, fmaxf(fmaxf(s[c], s[c + 1]), fmaxf(s[c + 2], s[c + 3])));
           }
+          // the group agrees whether a weight would pass 2^15
           const bool over = __any_sync(0xffffffffu, top > kOver);
           if (lane == 0) {
             if (over) raised[half * 2 + (g & 1)] = g + 1;
             tc::mbar_arrive(redb + half);
           }
-#pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = fast_exp2(s[c]);
-          if (!tc::mbar_wait(redb + half, ru & 1, abort_flag, p.err)) { ok = false; break; }
+          if (!tc::mbar_wait_few(redb + half, ru & 1, abort_flag, p.err)) { ok = false; break; }
           ++ru;
           slow = raised[half * 2 + (g & 1)] == g + 1;
-          if (slow) {
-            tc::tmem_ld32(scol, s);
-            tc::tmem_wait_ld();
+          if (!slow) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = fast_exp2(s[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] += mb[c];
           }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = fmaf(s[c], kf, ls);
         }
-        // S^T is in registers: the next tile's may be written
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sfree);
         bool raise = false;
         float corr = 1.f;
         if (slow) {
@@ -321,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool sink = kWindow && x0 + row < p.sinks;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            s[c] = fmaf(s[c], kf, ls);
             if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
             if (kWindow && row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
           }
@@ -354,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // P^T's buffer and the accumulator are the previous tile's products' until they are done
-        if (g > 0 && !tc::mbar_wait(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (g > 0 && !tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
         if (raise) {
           tc::fence_after_sync();
 #pragma unroll
@@ -389,11 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- sums over the keys: lane c gets row c's
       float lsum = 0.f;
       if (any) {
-        red_sum[(half * 32 + lane) * 4 + quad] = reduce_scatter_sum(l);
+        float* rb = red_max + (ru & 1) * 256 + half * 128;
+        rb[lane * 4 + quad] = reduce_scatter_sum(l);
         if (!group_sync()) { ok = false; break; }
-        const float4 v = *reinterpret_cast<const float4*>(red_sum + (half * 32 + lane) * 4);
+        const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
         lsum = (v.x + v.y) + (v.z + v.w);
-        if (!tc::mbar_wait(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (!tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
         tc::fence_after_sync();
       }
       const int n_out = min(32, w.rows - half * 32);   // rows of this half (may be <= 0)
@@ -403,36 +431,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.part_ml[(at + lane) * 2] = m;
         p.part_ml[(at + lane) * 2 + 1] = lsum;
       }
-      if (any || w.whole) {
+      // eight rows, four dims each, at a time
+      auto rows_out = [&](auto put) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < 32; c0 += 8) {      // eight rows, four dims each
-          if (c0 >= n_out) break;
+        for (int c0 = 0; c0 < n_out; c0 += 8) {
           float o[4][8];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if (any) {
-              tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
-            } else {
+          for (int b = 0; b < 4; ++b) tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
+          tc::tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 8; ++c) o[b][c] = 0.f;
-            }
-          }
-          if (any) tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float f = __shfl_sync(0xffffffffu, inv, c0 + c);
-            if (c0 + c >= n_out) continue;        // alike in every lane
-            if (w.whole) {
-              __nv_bfloat162 a = __floats2bfloat162_rn(o[0][c] * f, o[1][c] * f);
-              __nv_bfloat162 b = __floats2bfloat162_rn(o[2][c] * f, o[3][c] * f);
-              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                        (int64_t)(w.row0 + half * 32 + c0 + c) * kC + 4 * row) =
-                  make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-            } else {
-              *reinterpret_cast<float4*>(p.part_o + (at + c0 + c) * kC + 4 * row) =
-                  make_float4(o[0][c], o[1][c], o[2][c], o[3][c]);
-            }
-          }
+          for (int c = 0; c < 8; ++c) put(c0 + c, o[0][c], o[1][c], o[2][c], o[3][c]);
+        }
+      };
+      if (!w.whole) {
+        float4* to = reinterpret_cast<float4*>(p.part_o + at * kC) + row;
+        if (any)
+          rows_out([&](int c, float a, float b, float x, float y) {
+            if (c < n_out) to[c * (kC / 4)] = make_float4(a, b, x, y);
+          });
+      } else {
+        uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                             (int64_t)(w.row0 + half * 32) * kC) + row;
+        if (any) {
+          rows_out([&](int c, float a, float b, float x, float y) {
+            const float f = __shfl_sync(0xffffffffu, inv, c & 31);
+            __nv_bfloat162 u = __floats2bfloat162_rn(a * f, b * f), v = __floats2bfloat162_rn(x * f, y * f);
+            if (c < n_out)
+              to[c * (kC / 4)] = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
+          });
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < n_out; ++c) to[c * (kC / 4)] = make_uint2(0u, 0u);
         }
       }
       if (any) {
@@ -441,56 +470,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(oempty);
       }
     }
-    if (tid == 0 && !posted) walk.post(p, nullptr);
-  } else if (warp < 12) {
+    if (tid == 0 && !posted) place->post(p, nullptr);
+  } else if (warp < 16) {
     // --------------------------------------------------------------------------- keys
     tc::set_regs<false, kRegKeys>();
-    const bool turn = (lane >> 2) & 1;
+    const int mine = (warp >> 2) & 1;              // of the two warpgroups: every other slot
     const uint32_t dst = tmem + lane_base + kKCol;
-    int g = 0, n = 0;                              // tiles, slots
+    int g = 0;                                     // tiles
     bool ok = true;
-    while (ok && walk.next(p, w)) {
+    while (ok && next()) {
       const int64_t first_from = kWindow ? latent_from(p, w.start + (w.row0 - w.seq_row0) / p.H) : 0;
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int buf = g & 1, ring = g % 3;
-        if (!tc::mbar_wait(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
-        const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
-        const int valid = tile_ok[buf] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
-        // a key that no row sees counts for nothing, whatever its row holds
-        const bool dead = row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks);
+        if (!tc::mbar_wait_few(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
         const uint32_t src = tc::smem_u32(raw + buf * kRaw + row * kRowBytes);
-        uint4 b0, b1;
-        lds_pair(src + kBlockAt, turn, b0, b1);
-        const uint32_t bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-        {
+        const uint32_t scales = tc::smem_u32(sc + ring * 32 * kScPitch + row);
+        if (mine == (g & 1)) {                     // a tile's scales are one warpgroup's work
+          const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
+          const int valid = tile_ok[buf] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
+          // a key that no row sees counts for nothing, whatever its row holds
+          const bool dead = row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks);
           float s = dead ? 0.f : srow[buf * kTK + row];
           if (!dead && s == 0.f) s = 0x1p-100f;    // (a row of zeros, as the insert writes it)
-          info[ring * kTK + row] = make_float2(s, dead ? 0.f : log2f(s));
-          if (tid == 256) tile_valid[ring] = valid;
+          info[ring * kTK + row] = make_float2(s, dead ? 0.f : __log2f(s));
+          if (row == 0) tile_valid[ring] = valid;
           __half* to = sc + ring * 32 * kScPitch + row;
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            const uint4 b = lds128(src + kBlockAt + 16 * j);
+            const uint32_t bs[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t h = dead ? 0u : e4m3x2_to_f16x2(bs[j] >> (16 * k));
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t h = dead ? 0u : e4m3x2_to_f16x2(bs[k >> 1] >> (16 * (k & 1)));
               const __half2 v = *reinterpret_cast<const __half2*>(&h);
-              to[(4 * j + 2 * k) * kScPitch] = __low2half(v);
-              to[(4 * j + 2 * k + 1) * kScPitch] = __high2half(v);
+              to[(16 * j + 2 * k) * kScPitch] = __low2half(v);
+              to[(16 * j + 2 * k + 1) * kScPitch] = __high2half(v);
             }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(infofull + ring);
+        } else if (!tc::mbar_wait_few(infofull + ring, (g / 3) & 1, abort_flag, p.err)) {
+          ok = false;
+          break;
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(infofull + ring);
-#pragma unroll
-        for (int j = 0; j < 9; ++j, ++n) {
+#pragma unroll 1
+        for (int j = (g ^ mine) & 1; j < 9; j += 2) {   // (one body for all: the instruction cache is small)
+          const int n = 9 * g + j, slot = n % kSlots;
           uint32_t o[32];
           if (j < 8) {                             // 64 latent dims
-            uint4 c0, c1;
-            lds_pair(src + 32 * j, turn, c0, c1);
+            const uint4 c0 = lds128(src + 32 * j), c1 = lds128(src + 32 * j + 16);
             const uint32_t code[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const uint32_t at = scales + 4 * j * kScPitch * 2;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t h = e4m3x2_to_f16x2(bs[j] >> (16 * (k >> 1)));
-              const uint32_t f = __byte_perm(h, 0, k & 1 ? 0x3232 : 0x1010);
+              const uint32_t f = lds16(at + k * kScPitch * 2) * 0x10001u;
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 uint32_t v[4];
@@ -501,19 +534,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {                                 // the rotary part
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 c0, c1;
-              lds_pair(src + kRopeAt + 32 * k, turn, c0, c1);
-              const uint32_t v[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[8 * k + i] = v[i];
+            for (int k = 0; k < 8; ++k) {
+              const uint4 c = lds128(src + kRopeAt + 16 * k);
+              o[4 * k] = c.x;
+              o[4 * k + 1] = c.y;
+              o[4 * k + 2] = c.z;
+              o[4 * k + 3] = c.w;
             }
+          }
+          if (j >= 7) {                            // this warpgroup's last look at the tile
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
           }
-          const int slot = n % kSlots;
-          if (ok && n >= kSlots) ok = tc::mbar_wait(kempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
+          if (n >= kSlots) ok = tc::mbar_wait_few(kempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc::fence_after_sync();
           tc::tmem_st32(dst + slot * 32, o);
           tc::tmem_wait_st();
@@ -524,49 +559,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
     }
-  } else if (warp < 16) {
+  } else if (warp < 24) {
     // ------------------------------------------------------------------------- values
-    tc::set_regs<true, kRegValues>();
+    const int mine = (warp >> 2) & 1;              // of the two warpgroups: dims 4 row + mine and + 2 more
     const uint32_t dst = tmem + lane_base + kVCol;
     constexpr uint32_t kLow = 0x0F0F0F0Fu;
-    int g = 0, n = 0;
+    const int low = mine * 4, high = 4 - low;
+    int g = 0;
     bool ok = true;
-    while (ok && walk.next(p, w)) {
+    while (ok && next()) {
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int buf = g & 1, ring = g % 3;
-        if (!tc::mbar_wait(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (!tc::mbar_wait_few(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
         const uint32_t src = tc::smem_u32(raw + buf * kRaw + 2 * row);
-        uint32_t c0[32], c1[32];                   // this thread's codes of keys 4i, 4i + 2 and 4i + 1, 4i + 3
+        uint32_t c0[8], c1[8];                     // this thread's codes of keys 4i, 4i + 2 and 4i + 1, 4i + 3
+        auto load = [&](int quarter) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          c0[i] = lds16(src + (4 * i) * kRowBytes) | lds16(src + (4 * i + 2) * kRowBytes) << 16;
-          c1[i] = lds16(src + (4 * i + 1) * kRowBytes) | lds16(src + (4 * i + 3) * kRowBytes) << 16;
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(rawempty + buf);
-        if (!tc::mbar_wait(infofull + ring, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t at = src + (32 * quarter + 4 * i) * kRowBytes;
+            c0[i] = lds16(at) | lds16(at + 2 * kRowBytes) << 16;
+            c1[i] = lds16(at + kRowBytes) | lds16(at + 3 * kRowBytes) << 16;
+          }
+        };
+        load(0);
+        if (!tc::mbar_wait_few(infofull + ring, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
         const uint32_t scales = tc::smem_u32(sc + (ring * 32 + row / 4) * kScPitch);
-#pragma unroll
-        for (int j = 0; j < 8; ++j, ++n) {         // keys 32 (j / 2) .., dims 4 row + j % 2 and + 2 more
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {              // 32 keys
+          const int n = 8 * g + 2 * q + mine, slot = n % kSlots;
           uint32_t o[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int k = 8 * (j >> 1) + i;
-            const uint32_t pair = j & 1 ? ((c0[k] >> 4) & kLow) | (c1[k] & ~kLow)
-                                        : (c0[k] & kLow) | ((c1[k] << 4) & ~kLow);
+            const uint32_t pair = ((c0[i] >> low) & kLow) | ((c1[i] << high) & ~kLow);
             uint32_t v[4];                         // (dim, keys 0 1), (dim + 2, keys 0 1), the same of 2 3
             e2m1x8_to_f16(pair, v);
-            const uint2 f = lds64(scales + 8 * k);
+            const uint2 f = lds64(scales + 64 * q + 8 * i);
             o[2 * i] = mul_f16(v[0], f.x);
             o[2 * i + 1] = mul_f16(v[2], f.y);
             o[16 + 2 * i] = mul_f16(v[1], f.x);
             o[16 + 2 * i + 1] = mul_f16(v[3], f.y);
           }
-          const int slot = n % kSlots;
-          if (ok && n >= kSlots) ok = tc::mbar_wait(vempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
+          if (n >= kSlots) ok = tc::mbar_wait_few(vempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc::fence_after_sync();
           tc::tmem_st32(dst + slot * 32, o);
+          if (q < 3) load(q + 1);
+          if (q == 2) {                            // the last codes of the tile are here
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(rawempty + buf);
+          }
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
@@ -577,18 +619,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     tc::set_regs<false, kRegOther>();
-    if (warp == 17 && lane == 0) {
+    if (warp == 25 && lane == 0) {
       // ---------------------------------------------------------------------- copies
       int g = 0, u = 0, nq = 0, nr[2] = {0, 0};    // phases of each barrier given copies
       bool ok = true;
       const uint8_t* data = reinterpret_cast<const uint8_t*>(p.cache.data);
-      while (ok && walk.next(p, w)) {
+      while (ok && place->next(p, w)) {
         if (w.tile0 >= w.tile1) continue;
         // the first raw tile does not wait for Q's buffer
         bool asked = false;
         auto ask_q = [&]() {
           asked = true;
-          if (u > 0 && !tc::mbar_wait(qempty, (u - 1) & 1, abort_flag, p.err)) return false;
+          if (u > 0 && !tc::mbar_wait_few(qempty, (u - 1) & 1, abort_flag, p.err)) return false;
           tc::mbar_arrive_tx(qfull, 9 * kQBlock);
           ++nq;
           for (int b = 0; b < 9; ++b) tma_2d(qbuf + b * kQBlock, &qmap, b * 128, w.row0, qfull);
@@ -600,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool have = slot >= 0;
           if (!have) slot_ok(slot, p.err);
           if (!asked && u == 0 && !ask_q()) { ok = false; break; }
-          if (g >= 2 && !tc::mbar_wait(rawempty + buf, ((g >> 1) - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+          if (g >= 2 && !tc::mbar_wait_few(rawempty + buf, ((g >> 1) - 1) & 1, abort_flag, p.err)) { ok = false; break; }
           tile_ok[buf] = have;
           ++nr[buf];
           if (have) {
@@ -633,66 +675,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i)
           if (nr[i] > 0) tc::mbar_wait_drain(rawfull + i, (nr[i] - 1) & 1);
       }
-    } else if (warp == 16) {
-      // -------------------------------------------------------------------- products
+    } else if (warp == 24) {
+      // ------------------------------------------------------------ products for S^T
       constexpr uint32_t idesc_s = tc::idesc_f16(kTK, kNR);
-      constexpr uint32_t idesc_o = tc::idesc_f16(128, kNR, false, true);
-      const uint32_t q_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(qbuf)), 16);
-      const uint32_t p_lo = tc::sdesc_lo(tc::uniform(tc::smem_u32(pbuf)), 16);
-      const uint32_t base = tc::uniform(tmem);
-      int u = 0, gs = 0, gv = 0, nk = 0, nv = 0;  // units, tiles of each product, slots of each ring
+      const uint32_t q_lo = tc::uniform(tc::sdesc_lo(tc::smem_u32(qbuf), 16));
+      const uint32_t a0 = tc::uniform(tmem + kKCol), d = tc::uniform(tmem + kSCol);
+      int g = 0, u = 0;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, p.err));
+        return __all_sync(0xffffffffu, tc::mbar_wait_few(bar, parity, abort_flag, p.err));
       };
-      auto logits = [&](bool last) -> bool {       // S^T of tile gs
-        if (gs > 0 && !wait_all(sfree, (gs - 1) & 1)) return false;
-#pragma unroll 1
-        for (int j = 0; j < 9; ++j, ++nk) {
-          const int slot = nk % kSlots;
-          if (!wait_all(kfull + slot, (nk / kSlots) & 1)) return false;
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)            // 16 dims, 8 columns of A, 32 bytes of B
-              tc::mma_ta_lo<idesc_s>(base + kSCol, base + kKCol + slot * 32 + 8 * s,
-                                     q_lo + ((j * kQBlock) >> 4) + 2 * s, (j | s) ? 1u : 0u);
-            tc::mma_commit(kempty + slot);
-            if (j == 8) {
-              tc::mma_commit(sfull);
-              if (last) tc::mma_commit(qempty);
-            }
-          }
-          __syncwarp();
-        }
-        ++gs;
-        return true;
-      };
-      while (ok && walk.next(p, w)) {
+      while (ok && next()) {
         if (w.tile0 >= w.tile1) continue;
         if (!wait_all(qready, u & 1)) break;
-        tc::fence_after_sync();
-        if (!logits(w.tile0 + 1 == w.tile1)) break;
-        for (int t = w.tile0; t < w.tile1; ++t, ++gv) {
-          if (t + 1 < w.tile1 && !logits(t + 2 == w.tile1)) { ok = false; break; }
-          if (!wait_all(pfull, gv & 1)) { ok = false; break; }
-          if (t == w.tile0 && u > 0 && !wait_all(oempty, (u - 1) & 1)) { ok = false; break; }
-          tc::fence_after_sync();
-          const uint32_t acc = tc::uniform(t > w.tile0);
+        for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+          if (g > 0 && !wait_all(sfree, (g - 1) & 1)) { ok = false; break; }
+          bool ready = false;
 #pragma unroll 1
-          for (int j = 0; j < 8; ++j, ++nv) {
-            const int slot = nv % kSlots;
-            if (!wait_all(vfull + slot, (nv / kSlots) & 1)) { ok = false; break; }
+          for (int round = 0; round < 3; ++round) {   // a tile's nine slots go three times around the ring
+            const uint32_t b = tc::uniform(q_lo + ((round * 3 * kQBlock) >> 4)), add = tc::uniform(round > 0);
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+              if (ok && !__all_sync(0xffffffffu, ready)) ok = wait_all(kfull + i, (g + round) & 1);
+              if (!ok) continue;
+              tc::fence_after_sync();
+              // (the next slot's barrier is asked while this one's products go out)
+              ready = i < 2 ? tc::mbar_test(kfull + i + 1, (g + round) & 1)
+                            : round < 2 && tc::mbar_test(kfull, (g + round + 1) & 1);
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)        // 16 dims, 8 columns of A, 32 bytes of B
+                  tc::mma_ta_lo<idesc_s>(d, a0 + i * 32 + 8 * s, b + ((i * kQBlock) >> 4) + 2 * s, (i | s) ? 1u : add);
+                tc::mma_commit(kempty + i);
+                if (i == 2 && round == 2) {
+                  tc::mma_commit(sfull);
+                  if (t + 1 == w.tile1) tc::mma_commit(qempty);
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+        }
+        ++u;
+      }
+      if (tc::elect_one()) {
+        tc::mma_commit(done);
+        tc::mbar_wait_drain(done, 0);
+      }
+    } else if (warp == 26) {
+      // ------------------------------------------------------------ products for O^T
+      constexpr uint32_t idesc_o = tc::idesc_f16(128, kNR, false, true);
+      const uint32_t p_lo = tc::uniform(tc::sdesc_lo(tc::smem_u32(pbuf), 16));
+      const uint32_t d = tc::uniform(tmem + kOCol);
+      int g = 0, u = 0, n = 0;
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait_few(bar, parity, abort_flag, p.err));
+      };
+      while (ok && next()) {
+        if (w.tile0 >= w.tile1) continue;
+        for (int t = w.tile0; t < w.tile1; ++t, ++g) {
+          const uint32_t acc = tc::uniform(t > w.tile0);
+          if (!wait_all(pfull, g & 1)) { ok = false; break; }
+          if (t == w.tile0 && u > 0 && !wait_all(oempty, (u - 1) & 1)) { ok = false; break; }
+          bool ready = false;
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j, ++n) {
+            const int slot = n % kSlots;
+            // slot j: keys 32 (j / 2) .., dims 4l + j % 2 and + 2 more
+            const uint32_t a = tc::uniform(tmem + kVCol + slot * 32), at = tc::uniform(d + (j & 1) * kNR);
+            const uint32_t b = tc::uniform(p_lo + (((j >> 1) * 2 * 2048) >> 4)), add = tc::uniform(j < 2 ? acc : 1u);
+            if (!__all_sync(0xffffffffu, ready) && !wait_all(vfull + slot, (n / kSlots) & 1)) { ok = false; break; }
             tc::fence_after_sync();
+            ready = j < 7 && tc::mbar_test(vfull + (n + 1) % kSlots, ((n + 1) / kSlots) & 1);
             if (tc::elect_one()) {
-              const uint32_t a = base + kVCol + slot * 32;
-              const uint32_t d = base + kOCol + (j & 1) * kNR;
-              const uint32_t b = p_lo + (((j >> 1) * 2 * 2048) >> 4);
-              const uint32_t add = j < 2 ? acc : 1u;
 #pragma unroll
               for (int s = 0; s < 2; ++s) {        // 16 keys, 8 columns of A, 2 KB of B
-                tc::mma_ta_lo<idesc_o>(d, a + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
-                tc::mma_ta_lo<idesc_o>(d + 2 * kNR, a + 16 + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
+                tc::mma_ta_lo<idesc_o>(at, a + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
+                tc::mma_ta_lo<idesc_o>(at + 2 * kNR, a + 16 + 8 * s, b + ((s * 2048) >> 4), s ? 1u : add);
               }
               tc::mma_commit(vempty + slot);
               if (j == 7) tc::mma_commit(pvdone);
@@ -704,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++u;
       }
       if (tc::elect_one()) {
-        tc::mma_commit(done);
-        tc::mbar_wait_drain(done, 0);
+        tc::mma_commit(done + 1);
+        tc::mbar_wait_drain(done + 1, 0);
       }
     }
     __syncwarp();
@@ -713,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 24) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }

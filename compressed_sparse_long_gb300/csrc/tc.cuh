@@ -47,6 +47,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase with the given parity is complete now.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase with the given parity to complete. Gives up (returns false) when the
 // CTA's abort flag is set or after kWaitLimitNs, in which case it sets the abort flag and
 // the device error bit so that every other role of the CTA leaves its loop too.
@@ -65,7 +76,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// Same, ignoring the abort flag (used to drain copies still in flight before exit).
+// mbar_wait in few instructions, for kernels whose roles crowd the instruction cache: tries are
+// counted instead of timed. A try that fails suspends the thread for a while, a microsecond or so, so
+// the limit is seconds; were it to return at once, it would still be 40 ms.
+constexpr uint32_t kWaitTries = 1u << 21;
+__device__ __forceinline__ bool mbar_wait_few(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+  for (uint32_t i = 0; !mbar_try(bar, parity); ++i) {
+    if (*abort_flag) return false;
+    if (i > kWaitTries) {
+      *abort_flag = 1;
+      raise_err(err, V4A_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// mbar_wait that ignores the abort flag (used to drain copies still in flight before exit).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try(bar, parity)) {
