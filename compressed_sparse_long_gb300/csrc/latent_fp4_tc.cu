@@ -21,7 +21,7 @@
 // next tile runs beside this tile's softmax and O^T.
 //
 // Warps 0-7: softmax and output, as in the plain kernel. Warps 8-15: keys, two warpgroups taking slots
-// in turn. Warps 16-23: values, a warpgroup for each of the two dims. Warps 24 and 26: products, one for
+// in turn. Warps 16-23: values, a warpgroup for each half of the keys. Warps 24 and 26: products, one for
 // each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles; scales;
 // Q).
 //
@@ -54,10 +54,12 @@ constexpr int kOffF = kOffS + 2 * kTK * 4;
 // floats: red_max[2][64][4] (red_sum[64][4] in the half that is not in use) mrow[8 warps][32]
 constexpr int kNFloats = 512 + 256;
 constexpr int kOffBar = kOffF + kNFloats * 4;
-constexpr int kNBar = 34;
+constexpr int kNBar = 40;
+constexpr int kPieces = 4, kWalkers = 26;                        // pieces of work known ahead; warps that take them
 constexpr int kOffMisc = kOffBar + kNBar * 8;
-constexpr int kOffWalk = kOffMisc + 256;
-constexpr int kSmemBytes = kOffWalk + kThreads / 32 * (int)sizeof(LatentWalk) + 1024;
+constexpr int kOffPiece = kOffMisc + 256;
+constexpr int kSmemBytes = kOffPiece + kPieces * (int)sizeof(LatentPiece) + (int)sizeof(LatentWalk) + 1024;
+static_assert(kOffPiece % 8 == 0 && sizeof(LatentPiece) % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert(kOffP % 1024 == 0 && kOffRaw % 1024 == 0, "swizzled operands");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kRaw, "the plan's prefix sums use a raw tile before its first copy");
@@ -132,6 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* redb = bars + 27;                                    // [2] one per group of 4 warps
   uint64_t* qmaxb = bars + 29;
   uint64_t* done = bars + 30;                                    // [2] of the products' two warps
+  uint64_t* piecefull = bars + 32;                               // [4]
+  uint64_t* pieceempty = bars + 36;                              // [4]
   int* misc = reinterpret_cast<int*>(sm + kOffMisc);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
@@ -155,6 +159,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(vempty + i, 1);
       tc::mbar_init(infofull + i, 4);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      tc::mbar_init(piecefull + i, 1);
+      tc::mbar_init(pieceempty + i, kWalkers);
+    }
     tc::mbar_init(qfull, 1);
     tc::mbar_init(qready, 8);
     tc::mbar_init(qempty, 1);
@@ -175,20 +183,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   pdl_wait();
-  // (the walk's place is kept in shared memory, a copy a warp: it is wanted once a piece)
-  LatentWalk* const place = reinterpret_cast<LatentWalk*>(sm + kOffWalk) + warp;
+  // The copies' thread walks; the others get the pieces from it, a piece ahead. (Walking is some
+  // hundred instructions that would push six roles' loops out of the instruction cache each time.)
+  LatentPiece* const pieces = reinterpret_cast<LatentPiece*>(sm + kOffPiece);
+  LatentWalk* const plan = reinterpret_cast<LatentWalk*>(pieces + kPieces);
   LatentWalk walk;
   LatentPiece w;
   walk.begin(p, reinterpret_cast<int32_t*>(raw), warp_tot);
   tc::fence_proxy_async();     // the prefix sums' buffer is the copies' next
-  if (lane == 0) *place = walk;
+  if (tid == 0) *plan = walk;
+  int np = 0;                                     // pieces taken
   auto next = [&]() -> bool {                     // by whole warps
-    LatentWalk at = *place;
+    const int at = np % kPieces;
+    if (!__all_sync(0xffffffffu, tc::mbar_wait_few(piecefull + at, (np / kPieces) & 1, abort_flag, p.err))) return false;
+    w = pieces[at];
     __syncwarp();
-    const bool more = at.next(p, w);
-    if (lane == 0) *place = at;
-    __syncwarp();
-    return more;
+    if (lane == 0) tc::mbar_arrive(pieceempty + at);
+    ++np;
+    return w.seq >= 0;
   };
   tc::fence_before_sync();
   __syncthreads();
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool posted = false;
     while (ok && next()) {
-      if (tid == 0 && !posted) place->post(p, &w);
+      if (tid == 0 && !posted) plan->post(p, &w);
       posted = true;
       if (w.rows == 0) continue;
       // lane c: row c of this half, the keys it sees
@@ -236,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!tc::mbar_wait_few(qfull, u & 1, abort_flag, p.err)) { ok = false; break; }
         // (a thread's chunks are 16 bytes of one row in each of 18 places: row tid / 8 or 32 + tid / 8)
         __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 6
+#pragma unroll 3
         for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
           if ((i & 1) * 32 + (tid >> 3) >= w.rows) continue;
           const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * (tid + 256 * i));
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int a0 = a / 2, a1 = a - a0;
         const float f0 = __uint_as_float((uint32_t)(127 + a0) << 23), f1 = __uint_as_float((uint32_t)(127 + a1) << 23);
         k2 = k2 * __uint_as_float((uint32_t)(127 - a0) << 23) * __uint_as_float((uint32_t)(127 - a1) << 23);
-#pragma unroll 3
+#pragma unroll 2
         for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
           uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (tid + 256 * i));
           uint4 v = *at;
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(oempty);
       }
     }
-    if (tid == 0 && !posted) place->post(p, nullptr);
+    if (tid == 0 && !posted) plan->post(p, nullptr);
   } else if (warp < 16) {
     // --------------------------------------------------------------------------- keys
     tc::set_regs<false, kRegKeys>();
@@ -561,39 +573,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 24) {
     // ------------------------------------------------------------------------- values
-    const int mine = (warp >> 2) & 1;              // of the two warpgroups: dims 4 row + mine and + 2 more
+    const int mine = (warp >> 2) & 1;              // of the two warpgroups: keys 64 mine ..
     const uint32_t dst = tmem + lane_base + kVCol;
     constexpr uint32_t kLow = 0x0F0F0F0Fu;
-    const int low = mine * 4, high = 4 - low;
     int g = 0;
     bool ok = true;
     while (ok && next()) {
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int buf = g & 1, ring = g % 3;
         if (!tc::mbar_wait_few(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
-        const uint32_t src = tc::smem_u32(raw + buf * kRaw + 2 * row);
+        const uint32_t src = tc::smem_u32(raw + buf * kRaw + 64 * mine * kRowBytes + 2 * row);
         uint32_t c0[8], c1[8];                     // this thread's codes of keys 4i, 4i + 2 and 4i + 1, 4i + 3
-        auto load = [&](int quarter) {
+        auto load = [&](int part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t at = src + (32 * quarter + 4 * i) * kRowBytes;
+            const uint32_t at = src + (32 * part + 4 * i) * kRowBytes;
             c0[i] = lds16(at) | lds16(at + 2 * kRowBytes) << 16;
             c1[i] = lds16(at + kRowBytes) | lds16(at + 3 * kRowBytes) << 16;
           }
         };
         load(0);
         if (!tc::mbar_wait_few(infofull + ring, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
-        const uint32_t scales = tc::smem_u32(sc + (ring * 32 + row / 4) * kScPitch);
+        const uint32_t scales = tc::smem_u32(sc + (ring * 32 + row / 4) * kScPitch + 64 * mine);
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {              // 32 keys
+        for (int q = 0; q < 4; ++q) {              // 32 keys (q / 2), dims 4 row + q % 2 and + 2 more
           const int n = 8 * g + 2 * q + mine, slot = n % kSlots;
+          const int low = (q & 1) * 4, high = 4 - low;
           uint32_t o[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t pair = ((c0[i] >> low) & kLow) | ((c1[i] << high) & ~kLow);
             uint32_t v[4];                         // (dim, keys 0 1), (dim + 2, keys 0 1), the same of 2 3
             e2m1x8_to_f16(pair, v);
-            const uint2 f = lds64(scales + 64 * q + 8 * i);
+            const uint2 f = lds64(scales + 64 * (q >> 1) + 8 * i);
             o[2 * i] = mul_f16(v[0], f.x);
             o[2 * i + 1] = mul_f16(v[2], f.y);
             o[16 + 2 * i] = mul_f16(v[1], f.x);
@@ -604,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc::fence_after_sync();
           tc::tmem_st32(dst + slot * 32, o);
-          if (q < 3) load(q + 1);
-          if (q == 2) {                            // the last codes of the tile are here
+          if (q == 1) {                            // the last codes of the tile
+            load(1);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
           }
@@ -624,7 +636,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0, u = 0, nq = 0, nr[2] = {0, 0};    // phases of each barrier given copies
       bool ok = true;
       const uint8_t* data = reinterpret_cast<const uint8_t*>(p.cache.data);
-      while (ok && place->next(p, w)) {
+      // the next piece, or the end, for everybody
+      auto publish = [&](LatentPiece& x) -> bool {
+        const bool more = walk.next(p, x);
+        if (!more) x.seq = -1;
+        const int at = np % kPieces;
+        if (np >= kPieces) ok = tc::mbar_wait_few(pieceempty + at, (np / kPieces - 1) & 1, abort_flag, p.err);
+        if (!ok) return false;
+        pieces[at] = x;
+        tc::mbar_arrive(piecefull + at);
+        ++np;
+        return more;
+      };
+      LatentPiece after;
+      bool more = false;
+      for (bool have = publish(w); have && ok; w = after, have = more) {
+        more = publish(after);
         if (w.tile0 >= w.tile1) continue;
         // the first raw tile does not wait for Q's buffer
         bool asked = false;
@@ -744,9 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int j = 0; j < 8; ++j, ++n) {
             const int slot = n % kSlots;
-            // slot j: keys 32 (j / 2) .., dims 4l + j % 2 and + 2 more
-            const uint32_t a = tc::uniform(tmem + kVCol + slot * 32), at = tc::uniform(d + (j & 1) * kNR);
-            const uint32_t b = tc::uniform(p_lo + (((j >> 1) * 2 * 2048) >> 4)), add = tc::uniform(j < 2 ? acc : 1u);
+            // slot j: keys 64 (j % 2) + 32 (j / 4) .., dims 4l + j / 2 % 2 and + 2 more
+            const uint32_t a = tc::uniform(tmem + kVCol + slot * 32), at = tc::uniform(d + ((j >> 1) & 1) * kNR);
+            const uint32_t b = tc::uniform(p_lo + ((((j & 1) * 4 + (j >> 2) * 2) * 2048) >> 4));
+            const uint32_t add = tc::uniform(j == 0 || j == 2 ? acc : 1u);
             if (!__all_sync(0xffffffffu, ready) && !wait_all(vfull + slot, (n / kSlots) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             ready = j < 7 && tc::mbar_test(vfull + (n + 1) % kSlots, ((n + 1) / kSlots) & 1);
