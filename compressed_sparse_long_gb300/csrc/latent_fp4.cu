@@ -60,7 +60,7 @@ struct Fp4Row {
 };
 
 template <typename T, int kBlocks>
-__global__ void __launch_bounds__(32 * kInsertWarps, 2)
+__global__ void __launch_bounds__(32 * kInsertWarps, kBlocks == 1 ? 3 : 2)
     latent_insert_fp4_kernel(const __grid_constant__ LatentInsertParams p, int tokens) {
   using Row = Fp4Row<T, kBlocks>;
   constexpr int kV = Row::kV;
@@ -184,14 +184,16 @@ __global__ void __launch_bounds__(32 * kInsertWarps, 2)
 }
 
 // ----------------------------------------------------------------------------- gather
-// A block takes `rows` rows: their pool rows are looked up first, a thread a row; then a thread takes
-// a block of 16 latent values (8 bytes of codes, one block scale) or 16 rotary ones at a time.
+// A block takes `rows` rows: their pool rows are looked up first, a thread a row; then a thread makes 16
+// bytes of a row at a time from 2 or 4 bytes of codes and a block scale (or rotary numbers), four in
+// flight, so that a warp's stores are whole lines. Bound: HBM (254,681 rows: @@gather@@); for few
+// rows, latency (3.6 us).
 constexpr int kGatherRows = 64, kGatherThreads = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kGatherThreads)
     latent_gather_fp4_kernel(const __grid_constant__ LatentGatherParams p, int rows) {
-  constexpr int kV = 16 / (int)sizeof(T);
+  constexpr int kV = 16 / (int)sizeof(T), kFly = 4;
   __shared__ int64_t slots[kGatherRows];   // pool row, -1: zeros, -2: no row of the batch
   __shared__ float scales[kGatherRows];
   const int r0 = blockIdx.x * rows, nr = min(rows, p.n_rows - r0);
@@ -208,43 +210,58 @@ __global__ void __launch_bounds__(kGatherThreads)
     scales[threadIdx.x] = s >= 0 ? __ldg(p.cache.scale + s) : 0.f;
   }
   __syncthreads();
-  const int lat = p.C / 16, items = lat + (p.R + 15) / 16, width = p.C + p.R;
-  for (int k = threadIdx.x; k < nr * items; k += kGatherThreads) {
-    const int r = k / items, i = k - r * items;
-    const int64_t s = slots[r];
-    if (s == -2) continue;
-    float f[16] = {};
-    int n = 16;
-    const uint8_t* row = reinterpret_cast<const uint8_t*>(p.cache.data) + s * (int64_t)p.cache.width;
-    if (i < lat) {
-      if (s >= 0) fp4_block(row, p.C, p.R, i, scales[r], f);
-    } else {
-      const int d = (i - lat) * 16;
-      n = min(16, p.R - d);                    // 8 or 16
-      if (s >= 0) {
-        const uint4* h = reinterpret_cast<const uint4*>(row + p.C / 2 + 2 * d);
+  const int nv = (p.C + p.R) / kV, lat = p.C / kV, total = nr * nv;
+  const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.cache.data);
+  uint4* out = reinterpret_cast<uint4*>(p.out) + (int64_t)r0 * nv;
+  const int dr = kGatherThreads / nv, dc = kGatherThreads % nv;   // a step of all threads
+  int r = threadIdx.x / nv, c = threadIdx.x % nv;
+  for (int k = threadIdx.x; k < total; k += kFly * kGatherThreads) {
+    uint4 raw[kFly];                        // kV f16 numbers, or codes and their block scale
+    int at[kFly], row[kFly];                // the vector of its row (-1: nothing to write); the row
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (8 * j >= n) continue;
-          const uint4 w = __ldg(h + j);
-          const __half2* v = reinterpret_cast<const __half2*>(&w);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 x = __half22float2(v[q]);
-            f[8 * j + 2 * q] = scales[r] * x.x;
-            f[8 * j + 2 * q + 1] = scales[r] * x.y;
+    for (int i = 0; i < kFly; ++i) {
+      at[i] = -1;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (k + i * kGatherThreads < total) {
+        const int64_t s = slots[r];
+        row[i] = r;
+        if (s != -2) at[i] = c;
+        if (s >= 0) {
+          const uint8_t* from = pool + s * p.cache.width;
+          if (c < lat) {
+            if constexpr (kV == 8) raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(from) + c);
+            else raw[i].x = __ldg(reinterpret_cast<const uint16_t*>(from) + c);
+            raw[i].y = __ldg(from + p.C / 2 + 2 * p.R + c * kV / 16);
+          } else if constexpr (kV == 8) {
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(from + p.C / 2) + (c - lat));
+          } else {
+            const uint2 h = __ldg(reinterpret_cast<const uint2*>(from + p.C / 2) + (c - lat));
+            raw[i].x = h.x;
+            raw[i].y = h.y;
           }
         }
+        r += dr;
+        c += dc;
+        if (c >= nv) { c -= nv; ++r; }
       }
     }
-    T* out = reinterpret_cast<T*>(p.out) + (int64_t)(r0 + r) * width + 16 * i;
 #pragma unroll
-    for (int j = 0; j < 16 / kV; ++j) {
-      if (j * kV >= n) continue;
-      float g[kV];
+    for (int i = 0; i < kFly; ++i) {
+      if (at[i] < 0) continue;
+      uint32_t h[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      float block = 1.f;
+      if (at[i] < lat) {
+        block = e4m3_to_f32((uint8_t)raw[i].y);
+        e2m1x8_to_f16(raw[i].x, h);
+      }
+      float f[kV];
 #pragma unroll
-      for (int q = 0; q < kV; ++q) g[q] = f[j * kV + q];
-      store_pack<T, kV>(out + j * kV, g);
+      for (int q = 0; q < kV / 2; ++q) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[q]));
+        f[2 * q] = scales[row[i]] * (block * v.x);
+        f[2 * q + 1] = scales[row[i]] * (block * v.y);
+      }
+      store_pack<T, kV>(reinterpret_cast<T*>(out + k + i * kGatherThreads), f);
     }
   }
 }

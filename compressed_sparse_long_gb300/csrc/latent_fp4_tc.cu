@@ -683,17 +683,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive(rawfull + buf);
           }
           if (!asked && !ask_q()) { ok = false; break; }
-          if (t + 1 < w.tile1) {             // the next tile's rows into L2
-            const int64_t ahead = tile_slot(p, w.seq, w.tile_at<kWindow>(t + 1), kTK);
-            if (ahead >= 0) {
-#pragma unroll 1
-              for (int i = 0; i < 4; ++i)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(data + ahead * kRowBytes +
-                                                                               i * (kRaw / 4)),
-                             "r"(kRaw / 4)
-                             : "memory");
-            }
-          }
         }
         ++u;
       }

@@ -44,7 +44,8 @@ class PageTable:
             refs = refs.index_add_(0, named, torch.ones_like(named, dtype=_I32))[:n].clone()
         _need(refs, "refs", dev, _I32, (None,))
         self.refs = refs
-        self._desc = self._pools = None, None
+        self._desc = None, None
+        self._pools = None, None, None
         self._describe()
 
     def _describe(self):
@@ -65,10 +66,14 @@ class PageTable:
 
     def _describe_pools(self, dev):
         at, n = self.block_table.data_ptr(), self.refs.shape[0]
-        key = at, n, tuple([(p.data.data_ptr(), p.data.get_device(), p.data.shape, p.data.dtype,
-                             p.data.is_contiguous(), p.block_table.data_ptr(), p.rows_per_block,
-                             None if p.scale is None else p.scale.data_ptr())
-                            for p in self.pools])
+        # (tensors that are the same objects, in the same place and of the same size, were looked at)
+        key = [at, n, dev]
+        for p in self.pools:
+            d, s = p.data, p.scale
+            key += (id(d), d.data_ptr(), d.shape, d.is_contiguous(), id(s), p.rows_per_block,
+                    id(p.block_table))
+            if s is not None:
+                key += s.data_ptr(), s.shape
         kept = self._pools
         if kept[0] != key:
             for i, p in enumerate(self.pools):
@@ -83,7 +88,7 @@ class PageTable:
             kept = self._pools = key, (Pool * len(self.pools))(*[
                 Pool(p.data.data_ptr(), None if p.scale is None else p.scale.data_ptr(),
                      p.data.shape[1] * p.data.element_size(), p.rows_per_block, 0)
-                for p in self.pools])
+                for p in self.pools]), [(p.data, p.scale, p.block_table) for p in self.pools]
         return kept[1], len(kept[1])
 
     def _list(self, t, name, dev, dtype, n):
