@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __g
 // and lane l accumulates output dims l, l + 32, .. . Bound: shared-memory reads (a word a product)
 // and fp32 FMA: absorbed 14-17 TFLOP/s with 512 or 256 latent dims (8 sequences x 8,192 tokens, 64
 // heads, 512 + 64, fp32: 538 us), 6 with 128; expanded 5-9 (2,048-token prompt, 16 heads, fp32,
-// 128 + 64 / 128: 2.5 ms). The tensor-core kernels take 33 and 44 us at these sizes.
+// 128 + 64 / 128: 2.5 ms). The tensor-core kernels take 33 and 44 us at these sizes. FP4 rows are expanded
+// as they come into shared memory.
 constexpr int kGenRows = 16, kGenKeys = 32, kGenThreads = 256;
 
 struct RowState {

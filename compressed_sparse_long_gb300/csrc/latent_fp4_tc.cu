@@ -25,13 +25,14 @@
 // each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles; scales;
 // Q).
 //
-// Bound: instructions. A tile takes about 17,000 warp instructions (each code is expanded twice), four
-// schedulers issue 0.55 a cycle between instruction-cache misses: 28 warps in six roles do not fit the
-// small caches, which is why loops over slots are rolled and waits are short. 32 sequences x 32768
-// tokens, 64 heads: 230 us with the merge (640 TFLOP/s); 16 of 4616-108051, 128 heads: 265 us. On the
-// way: one warpgroup a role 276 us, unrolled loops 431. Codes expanded once, from registers, keys to
-// tensor memory and values to shared memory: 319 us (the values' stores wait while O^T's products read
-// shared memory).
+// Bound: instructions. A tile takes 17,500 warp instructions (each code is expanded twice); the four
+// schedulers issue 2.2 a cycle, the tensor pipe is active for 26 % of the time. 28 warps in six roles
+// do not fit the small instruction caches: loops over slots are rolled, waits are short, and one thread
+// walks for all. 32 sequences x 32768 tokens, 64 heads: 217 us with the merge (670 TFLOP/s); 16 of
+// 4616-108051, 128 heads: 247 us. (The bf16 cache takes 202 and 195: a smaller cache, not a faster one.)
+// On the way: one warpgroup a role 276 us, the same with unrolled loops 431. Codes expanded once, from
+// registers, keys to tensor memory and values to shared memory: 319 us (the values' stores wait while
+// O^T's products read shared memory).
 #include "kernels.h"
 #include "latent.h"
 #include "latent_tc.cuh"
@@ -275,11 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!tc::mbar_wait_few(qmaxb, u & 1, abort_flag, p.err)) { ok = false; break; }
 #pragma unroll
         for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)qmax[i]);
-        // 2^a as a product of two powers (a reaches 140), 2^-a times the softmax's factor the same way
-        const int a = most < 0x00800000u ? (most ? 126 : 0) : 14 + 127 - (int)(most >> 23);
-        const int a0 = a / 2, a1 = a - a0;
-        const float f0 = __uint_as_float((uint32_t)(127 + a0) << 23), f1 = __uint_as_float((uint32_t)(127 + a1) << 23);
-        k2 = k2 * __uint_as_float((uint32_t)(127 - a0) << 23) * __uint_as_float((uint32_t)(127 - a1) << 23);
+        // (at most 2^126: queries that small give f16 numbers with all their bits all the same)
+        const int a = most == 0 ? 0 : min(126, 14 + 127 - (int)(most >> 23));
+        const float f = __uint_as_float((uint32_t)(127 + a) << 23);
+        k2 *= __uint_as_float((uint32_t)(127 - a) << 23);
 #pragma unroll 2
         for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
           uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (tid + 256 * i));
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            e[k] = pack_f16(__uint_as_float(e[k] << 16) * f0 * f1, __uint_as_float(e[k] & 0xFFFF0000u) * f0 * f1);
+            e[k] = pack_f16(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xFFFF0000u) * f);
           *at = make_uint4(e[0], e[1], e[2], e[3]);
         }
         tc::fence_proxy_async();

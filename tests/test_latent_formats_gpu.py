@@ -428,3 +428,32 @@ def test_fp4_offsets_pass_31_bits():
     for kw in ({}, dict(window=100, sinks=2)):
         assert torch.equal(lay.attention(ints([0, 1], I32), ints([599], I64), 599, q, **kw),
                            small.attention(ints([0, 1], I32), ints([599], I64), 599, q, **kw))
+
+
+@pytest.mark.parametrize("window", [None, 200])
+def test_fp4_queries_that_are_not_finite_stay_their_own(window):
+    """Heads of one token share a unit of the tensor-core kernel, and one factor that brings its queries
+    into f16: an infinite or missing number in one head reaches no other; nor do queries of 2^120."""
+    rng = np.random.default_rng(38)
+    lay, bt = fp4_layer(rng, BF, 20, [700, 300])
+    q = rand(rng, BF, 2, 20, 576)
+    q[1] *= 2.0 ** -40
+    bad = q.clone()
+    bad[0, 3, 7], bad[0, 11, 570], bad[1, 0, 0] = float("inf"), float("nan"), float("-inf")
+    kw = dict(window=window, sinks=3) if window else {}
+    a, b = ints([0, 1, 2], I32), ints([699, 299], I64)
+    got, want = lay.attention(a, b, 699, bad, **kw), lay.attention(a, b, 699, q, **kw)
+    hit = torch.zeros(2, 20, dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[0, 11] = hit[1, 0] = True
+    assert not torch.isfinite(got[hit]).any() and torch.equal(got[~hit], want[~hit])
+    # one head far larger than the others: its weights are one key's, the others keep their bits
+    big = rand(rng, BF, 2, 20, 576)
+    big[0, 5] *= 2.0 ** 20
+    got, ref, tol = run_attention(lay, bt, [700, 300], [1, 1], big, window, 3 if window else 0)
+    keep = [h for h in range(20) if h != 5]
+    c = lay.cfg
+    live = values(lay)
+    bound = logit_bound(f64(big[:, keep]), live, c.softmax_scale)
+    _, mag = O.attention(live, bt, [0, 1, 2], [699, 299], f64(big), c.softmax_scale, 512, None, window, 3 if window else 0)
+    tol = attn_tolerance(BF, ref, mag, 576, 700, bound) + 2.0 ** -20 * np.abs(live[:, :512]).max()
+    check(got[:, keep], ref[:, keep], tol[:, keep])
