@@ -611,16 +611,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[16 + 2 * i] = mul_f16(v[1], f.x);
             o[16 + 2 * i + 1] = mul_f16(v[3], f.y);
           }
+          if (q == 1) {                            // the last codes of the tile, before the slot's wait: the buffer is wanted
+            load(1);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(rawempty + buf);
+          }
           if (n >= kSlots) ok = tc::mbar_wait_few(vempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
           tc::tmem_st32(dst + slot * 32, o);
-          if (q == 1) {                            // the last codes of the tile
-            load(1);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(rawempty + buf);
-          }
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
