@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[16 + 2 * i] = mul_f16(v[1], f.x);
             o[16 + 2 * i + 1] = mul_f16(v[3], f.y);
           }
-          if (q == 1) {                            // the last codes of the tile, before the slot's wait: the buffer is wanted
+          if (q == 1) {                            // the last codes, before the wait: the buffer is wanted
             load(1);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
