@@ -64,8 +64,8 @@ static_assert(kOffPiece % 8 == 0 && sizeof(LatentPiece) % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert(kOffP % 1024 == 0 && kOffRaw % 1024 == 0, "swizzled operands");
 static_assert((V4A_MAX_SEQ + 1) * 4 <= kRaw, "the plan's prefix sums use a raw tile before its first copy");
-constexpr uint32_t kSCol = 0, kOCol = 64, kKCol = 320, kVCol = 416, kTmemCols = 512;
-constexpr int kSlots = 3;
+constexpr uint32_t kSCol = 0, kOCol = 64, kKCol = 320, kVCol = 384, kTmemCols = 512;
+constexpr int kKeySlots = 2, kValueSlots = 4;   // of 32 columns: one and two a warpgroup
 constexpr float kRoom = -6.0f, kRaise = 12.0f, kOver = 15.0f;    // log2 units: a reference above its maximum,
                                                                  // what raises it in masked tiles and in others
 // registers of softmax, key and value (two each) and other warpgroups: 896 threads x 72 in all
@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
+// Two products and sums in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%5, %6};\n\t"
+      "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
 // Two e4m3 numbers as f16.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;
@@ -119,10 +126,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
   uint64_t* rawfull = bars;                                      // [2]
   uint64_t* rawempty = bars + 2;                                 // [2] by keys' and values' warps
-  uint64_t* kfull = bars + 4;                                    // [3]
-  uint64_t* kempty = bars + 7;                                   // [3]
-  uint64_t* vfull = bars + 10;                                   // [3]
-  uint64_t* vempty = bars + 13;                                  // [3]
+  uint64_t* kfull = bars + 4;                                    // [2]
+  uint64_t* kempty = bars + 6;                                   // [2]
+  uint64_t* vfull = bars + 8;                                    // [4]
+  uint64_t* vempty = bars + 12;                                  // [4]
   uint64_t* infofull = bars + 16;                                // [3] block scales and info of a tile
   uint64_t* qfull = bars + 19;
   uint64_t* qready = bars + 20;
@@ -153,13 +160,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(rawempty + i, 16);
       tc::mbar_init(redb + i, 4);
     }
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kKeySlots; ++i) {
       tc::mbar_init(kfull + i, 4);
       tc::mbar_init(kempty + i, 1);
+    }
+    for (int i = 0; i < kValueSlots; ++i) {
       tc::mbar_init(vfull + i, 4);
       tc::mbar_init(vempty + i, 1);
-      tc::mbar_init(infofull + i, 4);
     }
+    for (int i = 0; i < 3; ++i) tc::mbar_init(infofull + i, 4);
     for (int i = 0; i < kPieces; ++i) {
       tc::mbar_init(piecefull + i, 1);
       tc::mbar_init(pieceempty + i, kWalkers);
@@ -327,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
             const float4 mv = *reinterpret_cast<const float4*>(mb + c);
-            s[c] = fmaf(s[c], kf, ls - mv.x);
-            s[c + 1] = fmaf(s[c + 1], kf, ls - mv.y);
-            s[c + 2] = fmaf(s[c + 2], kf, ls - mv.z);
-            s[c + 3] = fmaf(s[c + 3], kf, ls - mv.w);
+            float d[4];                            // ls - mv
+            fma2(d[0], d[1], mv.x, mv.y, -1.f, ls, ls);
+            fma2(d[2], d[3], mv.z, mv.w, -1.f, ls, ls);
+            fma2(s[c], s[c + 1], s[c], s[c + 1], kf, d[0], d[1]);
+            fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], kf, d[2], d[3]);
             top = fmaxf(top, fmaxf(fmaxf(s[c], s[c + 1]), fmaxf(s[c + 2], s[c + 3])));
           }
           // the group agrees whether a weight would pass 2^15
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(pfull);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) l[c] = fmaf(s[c], is, l[c]);
+        for (int c = 0; c < 32; c += 2) fma2(l[c], l[c + 1], s[c], s[c + 1], is, l[c], l[c + 1]);
       }
       if (!ok) break;
       // ---- sums over the keys: lane c gets row c's
@@ -487,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------------------- keys
     tc::set_regs<false, kRegKeys>();
     const int mine = (warp >> 2) & 1;              // of the two warpgroups: every other slot
-    const uint32_t dst = tmem + lane_base + kKCol;
-    int g = 0;                                     // tiles
+    const uint32_t dst = tmem + lane_base + kKCol + 32 * mine;
+    int g = 0, n = 0;                              // tiles; this warpgroup's slots
     bool ok = true;
     while (ok && next()) {
       const int64_t first_from = kWindow ? latent_from(p, w.start + (w.row0 - w.seq_row0) / p.H) : 0;
@@ -526,8 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
 #pragma unroll 1
-        for (int j = (g ^ mine) & 1; j < 9; j += 2) {   // (one body for all: the instruction cache is small)
-          const int n = 9 * g + j, slot = n % kSlots;
+        for (int j = (g ^ mine) & 1; j < 9; j += 2, ++n) {   // (one body for all: the instruction cache is small)
           uint32_t o[32];
           if (j < 8) {                             // 64 latent dims
             const uint4 c0 = lds128(src + 32 * j), c1 = lds128(src + 32 * j + 16);
@@ -558,15 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
           }
-          if (n >= kSlots) ok = tc::mbar_wait_few(kempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          if (n > 0) ok = tc::mbar_wait_few(kempty + mine, (n - 1) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
-          tc::tmem_st32(dst + slot * 32, o);
+          tc::tmem_st32(dst, o);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(kfull + slot);
+          if (lane == 0) tc::mbar_arrive(kfull + mine);
         }
         if (!ok) break;
       }
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t scales = tc::smem_u32(sc + (ring * 32 + row / 4) * kScPitch + 64 * mine);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {              // 32 keys (q / 2), dims 4 row + q % 2 and + 2 more
-          const int n = 8 * g + 2 * q + mine, slot = n % kSlots;
+          const int n = 2 * g + (q >> 1), slot = 2 * (q & 1) + mine;   // times around the ring
           const int low = (q & 1) * 4, high = 4 - low;
           uint32_t o[32];
 #pragma unroll
@@ -616,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
           }
-          if (n >= kSlots) ok = tc::mbar_wait_few(vempty + slot, (n / kSlots - 1) & 1, abort_flag, p.err);
+          if (n > 0) ok = tc::mbar_wait_few(vempty + slot, (n - 1) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
@@ -695,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ products for S^T
       constexpr uint32_t idesc_s = tc::idesc_f16(kTK, kNR);
       const uint32_t q_lo = tc::uniform(tc::sdesc_lo(tc::smem_u32(qbuf), 16));
-      const uint32_t a0 = tc::uniform(tmem + kKCol), d = tc::uniform(tmem + kSCol);
-      int g = 0, u = 0;
+      const uint32_t d = tc::uniform(tmem + kSCol);
+      int g = 0, u = 0, n = 0;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, tc::mbar_wait_few(bar, parity, abort_flag, p.err));
@@ -708,29 +717,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (g > 0 && !wait_all(sfree, (g - 1) & 1)) { ok = false; break; }
           bool ready = false;
 #pragma unroll 1
-          for (int round = 0; round < 3; ++round) {   // a tile's nine slots go three times around the ring
-            const uint32_t b = tc::uniform(q_lo + ((round * 3 * kQBlock) >> 4)), add = tc::uniform(round > 0);
+          for (int j = 0; j < 9; ++j, ++n) {
+            const int slot = n % kKeySlots;
+            const uint32_t a = tc::uniform(tmem + kKCol + slot * 32), b = tc::uniform(q_lo + ((j * kQBlock) >> 4));
+            const uint32_t add = tc::uniform(j > 0);
+            if (!__all_sync(0xffffffffu, ready) && !wait_all(kfull + slot, (n / kKeySlots) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            // (the next slot's barrier is asked while this one's products go out)
+            ready = j < 8 && tc::mbar_test(kfull + (n + 1) % kKeySlots, ((n + 1) / kKeySlots) & 1);
+            if (tc::elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
-              if (ok && !__all_sync(0xffffffffu, ready)) ok = wait_all(kfull + i, (g + round) & 1);
-              if (!ok) continue;
-              tc::fence_after_sync();
-              // (the next slot's barrier is asked while this one's products go out)
-              ready = i < 2 ? tc::mbar_test(kfull + i + 1, (g + round) & 1)
-                            : round < 2 && tc::mbar_test(kfull, (g + round + 1) & 1);
-              if (tc::elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 4; ++s)        // 16 dims, 8 columns of A, 32 bytes of B
-                  tc::mma_ta_lo<idesc_s>(d, a0 + i * 32 + 8 * s, b + ((i * kQBlock) >> 4) + 2 * s, (i | s) ? 1u : add);
-                tc::mma_commit(kempty + i);
-                if (i == 2 && round == 2) {
-                  tc::mma_commit(sfull);
-                  if (t + 1 == w.tile1) tc::mma_commit(qempty);
-                }
+              for (int s = 0; s < 4; ++s)          // 16 dims, 8 columns of A, 32 bytes of B
+                tc::mma_ta_lo<idesc_s>(d, a + 8 * s, b + 2 * s, s ? 1u : add);
+              tc::mma_commit(kempty + slot);
+              if (j == 8) {
+                tc::mma_commit(sfull);
+                if (t + 1 == w.tile1) tc::mma_commit(qempty);
               }
-              __syncwarp();
             }
-            if (!ok) break;
+            __syncwarp();
           }
           if (!ok) break;
         }
@@ -759,14 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool ready = false;
 #pragma unroll 1
           for (int j = 0; j < 8; ++j, ++n) {
-            const int slot = n % kSlots;
+            const int slot = n % kValueSlots;
             // slot j: keys 64 (j % 2) + 32 (j / 4) .., dims 4l + j / 2 % 2 and + 2 more
             const uint32_t a = tc::uniform(tmem + kVCol + slot * 32), at = tc::uniform(d + ((j >> 1) & 1) * kNR);
             const uint32_t b = tc::uniform(p_lo + ((((j & 1) * 4 + (j >> 2) * 2) * 2048) >> 4));
             const uint32_t add = tc::uniform(j == 0 || j == 2 ? acc : 1u);
-            if (!__all_sync(0xffffffffu, ready) && !wait_all(vfull + slot, (n / kSlots) & 1)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, ready) && !wait_all(vfull + slot, (n / kValueSlots) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            ready = j < 7 && tc::mbar_test(vfull + (n + 1) % kSlots, ((n + 1) / kSlots) & 1);
+            ready = j < 7 && tc::mbar_test(vfull + (n + 1) % kValueSlots, ((n + 1) / kValueSlots) & 1);
             if (tc::elect_one()) {
 #pragma unroll
               for (int s = 0; s < 2; ++s) {        // 16 keys, 8 columns of A, 2 KB of B
