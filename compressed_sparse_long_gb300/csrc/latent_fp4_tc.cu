@@ -91,6 +91,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(vfull + i, 4);
       tc::mbar_init(vempty + i, 1);
     }
-    for (int i = 0; i < 3; ++i) tc::mbar_init(infofull + i, 4);
+    for (int i = 0; i < 3; ++i) tc::mbar_init(infofull + i, 8);
     for (int i = 0; i < kPieces; ++i) {
       tc::mbar_init(piecefull + i, 1);
       tc::mbar_init(pieceempty + i, kWalkers);
@@ -506,45 +511,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = g & 1, ring = g % 3;
         if (!tc::mbar_wait_few(rawfull + buf, (g >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
         const uint32_t src = tc::smem_u32(raw + buf * kRaw + row * kRowBytes);
-        const uint32_t scales = tc::smem_u32(sc + ring * 32 * kScPitch + row);
-        if (mine == (g & 1)) {                     // a tile's scales are one warpgroup's work
-          const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
-          const int valid = tile_ok[buf] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
-          // a key that no row sees counts for nothing, whatever its row holds
-          const bool dead = row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks);
+        const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
+        const int valid = tile_ok[buf] ? (int)min((int64_t)kTK, w.keys - x0) : 0;
+        // a key that no row sees counts for nothing, whatever its row holds
+        const bool dead = row >= valid || (kWindow && x0 + row < first_from && x0 + row >= p.sinks);
+        if (mine != (g & 1)) {                     // the warpgroup with four slots
           float s = dead ? 0.f : srow[buf * kTK + row];
           if (!dead && s == 0.f) s = 0x1p-100f;    // (a row of zeros, as the insert writes it)
           info[ring * kTK + row] = make_float2(s, dead ? 0.f : __log2f(s));
           if (row == 0) tile_valid[ring] = valid;
-          __half* to = sc + ring * 32 * kScPitch + row;
-#pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            const uint4 b = lds128(src + kBlockAt + 16 * j);
-            const uint32_t bs[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t h = dead ? 0u : e4m3x2_to_f16x2(bs[k >> 1] >> (16 * (k & 1)));
-              const __half2 v = *reinterpret_cast<const __half2*>(&h);
-              to[(16 * j + 2 * k) * kScPitch] = __low2half(v);
-              to[(16 * j + 2 * k + 1) * kScPitch] = __high2half(v);
-            }
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(infofull + ring);
-        } else if (!tc::mbar_wait_few(infofull + ring, (g / 3) & 1, abort_flag, p.err)) {
-          ok = false;
-          break;
         }
+        __half* const scales = sc + ring * 32 * kScPitch + row;
 #pragma unroll 1
         for (int j = (g ^ mine) & 1; j < 9; j += 2, ++n) {   // (one body for all: the instruction cache is small)
           uint32_t o[32];
           if (j < 8) {                             // 64 latent dims
             const uint4 c0 = lds128(src + 32 * j), c1 = lds128(src + 32 * j + 16);
             const uint32_t code[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const uint32_t at = scales + 4 * j * kScPitch * 2;
+            const uint32_t block = dead ? 0u : lds32(src + kBlockAt + 4 * j);
+            const uint32_t two[2] = {e4m3x2_to_f16x2(block), e4m3x2_to_f16x2(block >> 16)};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t f = lds16(at + k * kScPitch * 2) * 0x10001u;
+              const uint32_t f = __byte_perm(two[k >> 1], 0, k & 1 ? 0x3232 : 0x1010);
+              scales[(4 * j + k) * kScPitch] = __ushort_as_half((unsigned short)f);   // (for the values)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 uint32_t v[4];
@@ -566,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= 7) {                            // this warpgroup's last look at the tile
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(rawempty + buf);
+          }
+          if ((j | 1) == 7) {                      // its last scales
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(infofull + ring);
           }
           if (n > 0) ok = tc::mbar_wait_few(kempty + mine, (n - 1) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
@@ -723,8 +716,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t add = tc::uniform(j > 0);
             if (!__all_sync(0xffffffffu, ready) && !wait_all(kfull + slot, (n / kKeySlots) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            // (the next slot's barrier is asked while this one's products go out)
-            ready = j < 8 && tc::mbar_test(kfull + (n + 1) % kKeySlots, ((n + 1) / kKeySlots) & 1);
             if (tc::elect_one()) {
 #pragma unroll
               for (int s = 0; s < 4; ++s)          // 16 dims, 8 columns of A, 32 bytes of B
@@ -735,6 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t + 1 == w.tile1) tc::mma_commit(qempty);
               }
             }
+            // (the next slot's barrier is asked as this one's products go out)
+            ready = j < 8 && tc::mbar_test(kfull + (n + 1) % kKeySlots, ((n + 1) / kKeySlots) & 1);
             __syncwarp();
           }
           if (!ok) break;
