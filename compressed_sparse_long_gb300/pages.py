@@ -45,7 +45,7 @@ class PageTable:
         _need(refs, "refs", dev, _I32, (None,))
         self.refs = refs
         self._desc = None, None
-        self._pools = None, None, None
+        self._pools = None, None
         self._describe()
 
     def _describe(self):
@@ -65,15 +65,17 @@ class PageTable:
         return dev, d[1]
 
     def _describe_pools(self, dev):
-        at, n = self.block_table.data_ptr(), self.refs.shape[0]
-        # (tensors that are the same objects, in the same place and of the same size, were looked at)
-        key = [at, n, dev]
+        table, n = self.block_table, self.refs.shape[0]
+        at = table.data_ptr()
+        # (all that the checks below look at: where it says the same, so would they)
+        key = [at, table.shape, n, dev]
         for p in self.pools:
-            d, s = p.data, p.scale
-            key += (id(d), d.data_ptr(), d.shape, d.is_contiguous(), id(s), p.rows_per_block,
-                    id(p.block_table))
-            if s is not None:
-                key += s.data_ptr(), s.shape
+            d, s, t = p.data, p.scale, p.block_table
+            key += (d.data_ptr(), d.shape, d.dtype, d.get_device(), d.is_contiguous(),
+                    p.rows_per_block)
+            key += (None,) if s is None else (s.data_ptr(), s.shape, s.dtype, s.get_device(),
+                                              s.is_contiguous())
+            key += (None,) if t is table else (t.data_ptr(), t.shape)
         kept = self._pools
         if kept[0] != key:
             for i, p in enumerate(self.pools):
@@ -81,14 +83,14 @@ class PageTable:
                 _need(p.data, name + ".data", dev, p.data.dtype, (n * p.rows_per_block, None))
                 if p.scale is not None:
                     _need(p.scale, name + ".scale", dev, torch.float32, (n * p.rows_per_block,))
-                if p.block_table.data_ptr() != at or p.block_table.shape != self.block_table.shape:
+                if p.block_table.data_ptr() != at or p.block_table.shape != table.shape:
                     raise ValueError("%s has another block table" % name)
                 if p.data.shape[1] * p.data.element_size() % 16:
                     raise ValueError("%s: rows of a multiple of 16 bytes are needed" % name)
             kept = self._pools = key, (Pool * len(self.pools))(*[
                 Pool(p.data.data_ptr(), None if p.scale is None else p.scale.data_ptr(),
                      p.data.shape[1] * p.data.element_size(), p.rows_per_block, 0)
-                for p in self.pools]), [(p.data, p.scale, p.block_table) for p in self.pools]
+                for p in self.pools])
         return kept[1], len(kept[1])
 
     def _list(self, t, name, dev, dtype, n):
