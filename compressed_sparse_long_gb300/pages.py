@@ -44,12 +44,12 @@ class PageTable:
             refs = refs.index_add_(0, named, torch.ones_like(named, dtype=_I32))[:n].clone()
         _need(refs, "refs", dev, _I32, (None,))
         self.refs = refs
-        self._desc = None, None
+        self._desc = None, None, 0
         self._pools = None, None
         self._describe()
 
     def _describe(self):
-        """(device, table descriptor, pool descriptors) as the tensors are now."""
+        """(device, table descriptor, workspace bytes) as the tensors are now."""
         dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
         bt, refs = self.block_table, self.refs
         if not (len(bt.shape) == 2 and _fits(bt, dev, _I32, bt.shape)
@@ -57,12 +57,13 @@ class PageTable:
             _need(bt, "block_table", dev, _I32, (None, None))
             _need(refs, "refs", dev, _I32, (None,))
         n = refs.shape[0]
-        # (the structures are kept for as long as new ones would say the same)
+        # (the structure is kept for as long as a new one would say the same)
         key = (bt.data_ptr(), refs.data_ptr(), *bt.shape, n)
         d = self._desc
         if d[0] != key:
-            d = self._desc = key, PageTableDesc(*key)
-        return dev, d[1]
+            desc = PageTableDesc(*key)
+            d = self._desc = key, desc, library().v4a_pages_workspace_size(byref(desc))
+        return dev, d[1], d[2]
 
     def _describe_pools(self, dev):
         table, n = self.block_table, self.refs.shape[0]
@@ -98,10 +99,6 @@ class PageTable:
             _need(t, name, dev, dtype, (n,))
         return t.data_ptr()
 
-    def _scratch(self, desc, stream):
-        nb = library().v4a_pages_workspace_size(byref(desc))
-        return scratch(nb, self.refs.device, stream), nb
-
     @staticmethod
     def _end(dev, dev_err, stream):
         return (None if dev_err is None else _word(dev_err, dev),
@@ -109,7 +106,7 @@ class PageTable:
 
     def free(self, first, last, dev_err=None, stream=None):
         """Give back blocks first[b] .. last[b] - 1 (int32 [n_seq]) of every row b."""
-        dev, desc = self._describe()
+        dev, desc, _ = self._describe()
         n = self.block_table.shape[0]
         _check("v4a_pages_free", library().v4a_pages_free(
             byref(desc), self._list(first, "first", dev, _I32, n),
@@ -117,10 +114,10 @@ class PageTable:
 
     def grow(self, first, last, dev_err=None, stream=None):
         """Give the lowest free pages to those of blocks first[b] .. last[b] - 1 that have none."""
-        dev, desc = self._describe()
+        dev, desc, nb = self._describe()
         n = self.block_table.shape[0]
         a, b = self._list(first, "first", dev, _I32, n), self._list(last, "last", dev, _I32, n)
-        ws, nb = self._scratch(desc, stream)
+        ws = scratch(nb, self.refs.device, stream)
         _check("v4a_pages_grow", library().v4a_pages_grow(
             byref(desc), a, b, None if ws is None else ws.data_ptr(), nb,
             *self._end(dev, dev_err, stream)))
@@ -129,12 +126,12 @@ class PageTable:
         """Row dst[i] takes over the first length[i] positions of row src[i] (int32, int32, int64
         [n]): whole blocks are shared, the block that length[i] cuts is copied to a page of its
         own, in every pool. dst's row must hold no page."""
-        dev, desc = self._describe()
+        dev, desc, nb = self._describe()
         n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() else 0
         a, b = self._list(src, "src", dev, _I32, n), self._list(dst, "dst", dev, _I32, n)
         c = self._list(length, "length", dev, _I64, n)
         pools, n_pools = self._describe_pools(dev)
-        ws, nb = self._scratch(desc, stream)
+        ws = scratch(nb, self.refs.device, stream)
         _check("v4a_pages_fork", library().v4a_pages_fork(
             byref(desc), pools, n_pools, n, a, b, c, None if ws is None else ws.data_ptr(), nb,
             *self._end(dev, dev_err, stream)))
@@ -142,7 +139,7 @@ class PageTable:
     def copy(self, src, dst, dev_err=None, stream=None):
         """Copy whole pages src[i] -> dst[i] (int32 [n]) in every pool. No page that is written may
         be in another pair."""
-        dev, desc = self._describe()
+        dev, desc, _ = self._describe()
         n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() else 0
         a, b = self._list(src, "src", dev, _I32, n), self._list(dst, "dst", dev, _I32, n)
         pools, n_pools = self._describe_pools(dev)
@@ -153,11 +150,11 @@ class PageTable:
         """Move the used pages to the pools' front; the table and the counts follow. Returns how
         many there are (int32 [1] on the device). moved: int32 [n_pages] to receive every page's
         new number (-1: was free), for holders of pages besides the table."""
-        dev, desc = self._describe()
+        dev, desc, nb = self._describe()
         m = None if moved is None else self._list(moved, "moved", dev, _I32, self.refs.shape[0])
         pools, n_pools = self._describe_pools(dev)
         used = _new((1,), _I32, self.refs.device, stream)
-        ws, nb = self._scratch(desc, stream)
+        ws = scratch(nb, self.refs.device, stream)
         _check("v4a_pages_compact", library().v4a_pages_compact(
             byref(desc), pools, n_pools, used.data_ptr(), m,
             None if ws is None else ws.data_ptr(), nb, *self._end(dev, dev_err, stream)))
