@@ -241,21 +241,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       return r;
     };
     bool posted = false;
-    while (ok && next()) {
-      if (tid == 0 && !posted) plan->post(p, &w);
-      posted = true;
-      if (w.rows == 0) continue;
-      // lane c: row c of this half, the keys it sees
-      const int my_row = half * 32 + lane;
-      int64_t vis = 0, from = 0;
-      if (my_row < w.rows) {
-        const int64_t pos = w.start + (w.row0 + my_row - w.seq_row0) / p.H;
-        vis = latent_visible(p, pos);
-        if (kWindow) from = latent_from(p, pos);
-        if (quad == 0) latent_report_pos(p, pos);
+    // The piece before, whose result is still to be written: that is done when the next piece's Q is
+    // ready, so that its first logits run beside the last products and the output.
+    struct { int rows, row0, slot, whole; bool any; float m, l; } last;
+    last.rows = 0;
+    while (ok) {
+      const bool more = next();
+      if (more) {
+        if (tid == 0 && !posted) plan->post(p, &w);
+        posted = true;
       }
-      const int64_t all_from = kWindow ? latent_from(p, w.start + (w.row0 + w.rows - 1 - w.seq_row0) / p.H) : 0;
-      const bool any = w.tile1 > w.tile0;
+      const bool any = more && w.rows > 0 && w.tile1 > w.tile0;
       float k2 = p.scale * kLog2e;
       if (any) {
         // Q in place from bf16 to f16 times 2^a. (Rows behind the unit's are another's: they take part
@@ -309,6 +305,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(qready);
         ++u;
       }
+      if (last.rows > 0) {
+        // ---- the piece before's result
+        if (last.any) {
+          if (!tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+          tc::fence_after_sync();
+        }
+        const int n_out = min(32, last.rows - half * 32);   // rows of this half (may be <= 0)
+        const float inv = last.l == 0.f ? 0.f : 1.f / last.l;
+        const int64_t at = (int64_t)last.slot * kNR + half * 32;
+        if (!last.whole && quad == 0) {
+          p.part_ml[(at + lane) * 2] = last.m;
+          p.part_ml[(at + lane) * 2 + 1] = last.l;
+        }
+        // eight rows, four dims each, at a time
+        auto rows_out = [&](auto put) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < n_out; c0 += 8) {
+            float o[4][8];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) put(c0 + c, o[0][c], o[1][c], o[2][c], o[3][c]);
+          }
+        };
+        if (!last.whole) {
+          float4* to = reinterpret_cast<float4*>(p.part_o + at * kC) + row;
+          if (last.any)
+            rows_out([&](int c, float a, float b, float x, float y) {
+              if (c < n_out) to[c * (kC / 4)] = make_float4(a, b, x, y);
+            });
+        } else {
+          uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                               (int64_t)(last.row0 + half * 32) * kC) + row;
+          if (last.any) {
+            rows_out([&](int c, float a, float b, float x, float y) {
+              const float f = __shfl_sync(0xffffffffu, inv, c & 31);
+              __nv_bfloat162 u = __floats2bfloat162_rn(a * f, b * f), v = __floats2bfloat162_rn(x * f, y * f);
+              if (c < n_out)
+                to[c * (kC / 4)] = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
+            });
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < n_out; ++c) to[c * (kC / 4)] = make_uint2(0u, 0u);
+          }
+        }
+        if (last.any) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(oempty);
+        }
+      }
+      if (!more) break;
+      last.rows = 0;
+      if (w.rows == 0) continue;
+      // lane c: row c of this half, the keys it sees
+      const int my_row = half * 32 + lane;
+      int64_t vis = 0, from = 0;
+      if (my_row < w.rows) {
+        const int64_t pos = w.start + (w.row0 + my_row - w.seq_row0) / p.H;
+        vis = latent_visible(p, pos);
+        if (kWindow) from = latent_from(p, pos);
+        if (quad == 0) latent_report_pos(p, pos);
+      }
+      const int64_t all_from = kWindow ? latent_from(p, w.start + (w.row0 + w.rows - 1 - w.seq_row0) / p.H) : 0;
       // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
       // row that sees nothing (or is none) infinity
       float m = -INFINITY;
@@ -374,17 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int seen = min((int)max((int64_t)0, min(vis - x0, (int64_t)kTK)), valid);
           const int begin = kWindow ? (int)max((int64_t)0, min(from - x0, (int64_t)kTK)) : 0;
           const bool sink = kWindow && x0 + row < p.sinks;
+          if (__any_sync(0xffffffffu, seen < kTK)) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
-            if (kWindow && row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
+            for (int c = 0; c < 32; ++c)
+              if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
+          }
+          if (kWindow && __any_sync(0xffffffffu, begin > 0)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
           }
           float* rb = red_max + (ru & 1) * 256 + half * 128;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float mc = redux_max(s[c]);
-            if (lane == c) rb[c * 4 + quad] = mc;
-          }
+          rb[lane * 4 + quad] = reduce_scatter<true>(s);
           if (!group_sync()) { ok = false; break; }
           const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
           const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
@@ -444,58 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lsum = 0.f;
       if (any) {
         float* rb = red_max + (ru & 1) * 256 + half * 128;
-        rb[lane * 4 + quad] = reduce_scatter_sum(l);
+        rb[lane * 4 + quad] = reduce_scatter<false>(l);
         if (!group_sync()) { ok = false; break; }
         const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
         lsum = (v.x + v.y) + (v.z + v.w);
-        if (!tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
-        tc::fence_after_sync();
       }
-      const int n_out = min(32, w.rows - half * 32);   // rows of this half (may be <= 0)
-      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      const int64_t at = (int64_t)w.slot * kNR + half * 32;
-      if (!w.whole && quad == 0) {
-        p.part_ml[(at + lane) * 2] = m;
-        p.part_ml[(at + lane) * 2 + 1] = lsum;
-      }
-      // eight rows, four dims each, at a time
-      auto rows_out = [&](auto put) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < n_out; c0 += 8) {
-          float o[4][8];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) put(c0 + c, o[0][c], o[1][c], o[2][c], o[3][c]);
-        }
-      };
-      if (!w.whole) {
-        float4* to = reinterpret_cast<float4*>(p.part_o + at * kC) + row;
-        if (any)
-          rows_out([&](int c, float a, float b, float x, float y) {
-            if (c < n_out) to[c * (kC / 4)] = make_float4(a, b, x, y);
-          });
-      } else {
-        uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                             (int64_t)(w.row0 + half * 32) * kC) + row;
-        if (any) {
-          rows_out([&](int c, float a, float b, float x, float y) {
-            const float f = __shfl_sync(0xffffffffu, inv, c & 31);
-            __nv_bfloat162 u = __floats2bfloat162_rn(a * f, b * f), v = __floats2bfloat162_rn(x * f, y * f);
-            if (c < n_out)
-              to[c * (kC / 4)] = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
-          });
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < n_out; ++c) to[c * (kC / 4)] = make_uint2(0u, 0u);
-        }
-      }
-      if (any) {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(oempty);
-      }
+      last.rows = w.rows;
+      last.row0 = w.row0;
+      last.slot = w.slot;
+      last.whole = w.whole;
+      last.any = any;
+      last.m = m;
+      last.l = lsum;
     }
     if (tid == 0 && !posted) plan->post(p, nullptr);
   } else if (warp < 16) {

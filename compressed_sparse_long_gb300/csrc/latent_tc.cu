@@ -217,22 +217,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (slow) {
           const int seen = min((int)max((int64_t)0, min(vis - x0, (int64_t)kTK)), valid);
+          if (__any_sync(0xffffffffu, seen < kTK)) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
+            for (int c = 0; c < 32; ++c)
+              if (row >= __shfl_sync(0xffffffffu, seen, c)) s[c] = -INFINITY;
+          }
           if (kWindow) {
             const int begin = (int)max((int64_t)0, min(from - x0, (int64_t)kTK));
             const bool sink = x0 + row < p.sinks;
+            if (__any_sync(0xffffffffu, begin > 0)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
+              for (int c = 0; c < 32; ++c)
+                if (row < __shfl_sync(0xffffffffu, begin, c) && !sink) s[c] = -INFINITY;
+            }
           }
           float* rb = red_max + (ru & 1) * 256 + half * 128;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float mc = redux_max(s[c]);
-            if (lane == c) rb[c * 4 + quad] = mc;
-          }
+          rb[lane * 4 + quad] = reduce_scatter<true>(s);
           if (!group_sync()) { ok = false; break; }
           const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
           const float mt = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * k2;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = w.tile1 > w.tile0;
       float ls = 0.f;
       if (any) {
-        red_sum[(half * 32 + lane) * 4 + quad] = reduce_scatter_sum(l);
+        red_sum[(half * 32 + lane) * 4 + quad] = reduce_scatter<false>(l);
         if (!group_sync()) { ok = false; break; }
         const float4 v = *reinterpret_cast<const float4*>(red_sum + (half * 32 + lane) * 4);
         ls = (v.x + v.y) + (v.z + v.w);

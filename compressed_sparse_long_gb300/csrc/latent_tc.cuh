@@ -13,11 +13,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -32,8 +27,9 @@ __device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
   tc::tmem_st32(taddr, u);
 }
 
-// Sum of v[c] over the 32 lanes; lane c ends with column c's.
-__device__ __forceinline__ float reduce_scatter_sum(const float (&v)[32]) {
+// Sum or largest of v[c] over the 32 lanes; lane c ends with column c's.
+template <bool kMax>
+__device__ __forceinline__ float reduce_scatter(const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   float a[32];
 #pragma unroll
@@ -44,7 +40,8 @@ __device__ __forceinline__ float reduce_scatter_sum(const float (&v)[32]) {
 #pragma unroll
     for (int j = 0; j < o; ++j) {
       const float send = up ? a[j] : a[j + o], keep = up ? a[j + o] : a[j];
-      a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      a[j] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
   return a[0];
