@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* tile_ok = misc + 6;                              // [2] by raw buffer
   volatile int* tile_valid = misc + 8;                           // [3] keys of a tile that exist
   int* qmax = misc + 11;                                         // [8] largest |q| of a warp's chunks, as bits
+  volatile float* qscale = reinterpret_cast<float*>(misc + 40);  // [2] 2^-a of a piece
   int32_t* warp_tot = misc + 20;                                 // [20]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,124 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return r;
     };
     bool posted = false;
-    // The piece before, whose result is still to be written: that is done when the next piece's Q is
-    // ready, so that its first logits run beside the last products and the output.
-    struct { int rows, row0, slot, whole; bool any; float m, l; } last;
-    last.rows = 0;
-    while (ok) {
-      const bool more = next();
-      if (more) {
-        if (tid == 0 && !posted) plan->post(p, &w);
-        posted = true;
-      }
-      const bool any = more && w.rows > 0 && w.tile1 > w.tile0;
-      float k2 = p.scale * kLog2e;
-      if (any) {
-        // Q in place from bf16 to f16 times 2^a. (Rows behind the unit's are another's: they take part
-        // in the products, but not in the choice of a; what they give is not looked at.)
-        if (!tc::mbar_wait_few(qfull, u & 1, abort_flag, p.err)) { ok = false; break; }
-        // (a thread's chunks are 16 bytes of one row in each of 18 places: row tid / 8 or 32 + tid / 8)
-        __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 3
-        for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
-          if ((i & 1) * 32 + (tid >> 3) >= w.rows) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * (tid + 256 * i));
-          const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top2 = __hmax2(top2, __habs2(e[k]));
-        }
-        const uint32_t two = *reinterpret_cast<const uint32_t*>(&top2);
-        uint32_t most = max(two << 16, two & 0xFFFF0000u);
-        if (most >= 0x7F800000u) {                 // infinities among them: the largest of the others
-          most = 0;
-#pragma unroll 1
-          for (int i = 0; i < 9 * kNR * 8 / 256 * 8; ++i) {
-            const uint32_t at = 16 * (tid + 256 * (i >> 3)) + 2 * (i & 7);
-            const uint32_t a = (uint32_t)(*reinterpret_cast<const uint16_t*>(qbuf + at) & 0x7FFF) << 16;
-            if (((i >> 3) & 1) * 32 + (tid >> 3) < w.rows && a < 0x7F800000u) most = max(most, a);
-          }
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-          qmax[warp] = (int)most;
-          tc::mbar_arrive(qmaxb);
-        }
-        if (!tc::mbar_wait_few(qmaxb, u & 1, abort_flag, p.err)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)qmax[i]);
-        // (at most 2^126: queries that small give f16 numbers with all their bits all the same)
-        const int a = most == 0 ? 0 : min(126, 14 + 127 - (int)(most >> 23));
-        const float f = __uint_as_float((uint32_t)(127 + a) << 23);
-        k2 *= __uint_as_float((uint32_t)(127 - a) << 23);
-#pragma unroll 2
-        for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
-          uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (tid + 256 * i));
-          uint4 v = *at;
-          uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            e[k] = pack_f16(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xFFFF0000u) * f);
-          *at = make_uint4(e[0], e[1], e[2], e[3]);
-        }
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(qready);
-        ++u;
-      }
-      if (last.rows > 0) {
-        // ---- the piece before's result
-        if (last.any) {
-          if (!tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
-          tc::fence_after_sync();
-        }
-        const int n_out = min(32, last.rows - half * 32);   // rows of this half (may be <= 0)
-        const float inv = last.l == 0.f ? 0.f : 1.f / last.l;
-        const int64_t at = (int64_t)last.slot * kNR + half * 32;
-        if (!last.whole && quad == 0) {
-          p.part_ml[(at + lane) * 2] = last.m;
-          p.part_ml[(at + lane) * 2 + 1] = last.l;
-        }
-        // eight rows, four dims each, at a time
-        auto rows_out = [&](auto put) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < n_out; c0 += 8) {
-            float o[4][8];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) put(c0 + c, o[0][c], o[1][c], o[2][c], o[3][c]);
-          }
-        };
-        if (!last.whole) {
-          float4* to = reinterpret_cast<float4*>(p.part_o + at * kC) + row;
-          if (last.any)
-            rows_out([&](int c, float a, float b, float x, float y) {
-              if (c < n_out) to[c * (kC / 4)] = make_float4(a, b, x, y);
-            });
-        } else {
-          uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                               (int64_t)(last.row0 + half * 32) * kC) + row;
-          if (last.any) {
-            rows_out([&](int c, float a, float b, float x, float y) {
-              const float f = __shfl_sync(0xffffffffu, inv, c & 31);
-              __nv_bfloat162 u = __floats2bfloat162_rn(a * f, b * f), v = __floats2bfloat162_rn(x * f, y * f);
-              if (c < n_out)
-                to[c * (kC / 4)] = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
-            });
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < n_out; ++c) to[c * (kC / 4)] = make_uint2(0u, 0u);
-          }
-        }
-        if (last.any) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(oempty);
-        }
-      }
-      if (!more) break;
-      last.rows = 0;
+    while (ok && next()) {
+      if (tid == 0 && !posted) plan->post(p, &w);
+      posted = true;
       if (w.rows == 0) continue;
       // lane c: row c of this half, the keys it sees
       const int my_row = half * 32 + lane;
@@ -370,6 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (quad == 0) latent_report_pos(p, pos);
       }
       const int64_t all_from = kWindow ? latent_from(p, w.start + (w.row0 + w.rows - 1 - w.seq_row0) / p.H) : 0;
+      const bool any = w.tile1 > w.tile0;
+      float k2 = 0.f;
       // row c's reference, log2 units; for the exponentials a row without one yet subtracts 0, a
       // row that sees nothing (or is none) infinity
       float m = -INFINITY;
@@ -383,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int64_t x0 = w.tile_at<kWindow>(t) * kTK;
         if (!tc::mbar_wait_few(infofull + g % 3, (g / 3) & 1, abort_flag, p.err)) { ok = false; break; }
+        if (t == w.tile0) k2 = p.scale * kLog2e * qscale[u++ & 1];
         const float2 in = info[(g % 3) * kTK + row];
         const int valid = tile_valid[g % 3];
         const float kf = in.x * k2, ls = in.y, is = in.x != 0.f ? __fdividef(1.f, in.x) : 0.f;
@@ -510,14 +399,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!group_sync()) { ok = false; break; }
         const float4 v = *reinterpret_cast<const float4*>(rb + lane * 4);
         lsum = (v.x + v.y) + (v.z + v.w);
+        if (!tc::mbar_wait_few(pvdone, (g - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        tc::fence_after_sync();
       }
-      last.rows = w.rows;
-      last.row0 = w.row0;
-      last.slot = w.slot;
-      last.whole = w.whole;
-      last.any = any;
-      last.m = m;
-      last.l = lsum;
+      const int n_out = min(32, w.rows - half * 32);   // rows of this half (may be <= 0)
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      const int64_t at = (int64_t)w.slot * kNR + half * 32;
+      if (!w.whole && quad == 0) {
+        p.part_ml[(at + lane) * 2] = m;
+        p.part_ml[(at + lane) * 2 + 1] = lsum;
+      }
+      // eight rows, four dims each, at a time
+      auto rows_out = [&](auto put) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < n_out; c0 += 8) {
+          float o[4][8];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tc::tmem_ld8(ocol + b * kNR + c0, o[b]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) put(c0 + c, o[0][c], o[1][c], o[2][c], o[3][c]);
+        }
+      };
+      if (!w.whole) {
+        float4* to = reinterpret_cast<float4*>(p.part_o + at * kC) + row;
+        if (any)
+          rows_out([&](int c, float a, float b, float x, float y) {
+            if (c < n_out) to[c * (kC / 4)] = make_float4(a, b, x, y);
+          });
+      } else {
+        uint2* to = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                             (int64_t)(w.row0 + half * 32) * kC) + row;
+        if (any) {
+          rows_out([&](int c, float a, float b, float x, float y) {
+            const float f = __shfl_sync(0xffffffffu, inv, c & 31);
+            __nv_bfloat162 u = __floats2bfloat162_rn(a * f, b * f), v = __floats2bfloat162_rn(x * f, y * f);
+            if (c < n_out)
+              to[c * (kC / 4)] = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
+          });
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < n_out; ++c) to[c * (kC / 4)] = make_uint2(0u, 0u);
+        }
+      }
+      if (any) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(oempty);
+      }
     }
     if (tid == 0 && !posted) plan->post(p, nullptr);
   } else if (warp < 16) {
@@ -525,9 +454,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::set_regs<false, kRegKeys>();
     const int mine = (warp >> 2) & 1;              // of the two warpgroups: every other slot
     const uint32_t dst = tmem + lane_base + kKCol + 32 * mine;
-    int g = 0, n = 0;                              // tiles; this warpgroup's slots
+    int g = 0, n = 0, u = 0;                       // tiles, this warpgroup's slots, pieces
     bool ok = true;
+    const int kt = tid - 256;
     while (ok && next()) {
+      if (w.tile0 >= w.tile1) continue;
+      // Q in place from bf16 to f16 times 2^a. (Rows behind the unit's are another's: they take part
+      // in the products, but not in the choice of a; what they give is not looked at.)
+      if (!tc::mbar_wait_few(qfull, u & 1, abort_flag, p.err)) break;
+      // (a thread's chunks are 16 bytes of one row in each of 18 places: row kt / 8 or 32 + kt / 8)
+      __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 3
+      for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
+        if ((i & 1) * 32 + (kt >> 3) >= w.rows) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(qbuf + 16 * (kt + 256 * i));
+        const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top2 = __hmax2(top2, __habs2(e[k]));
+      }
+      const uint32_t two = *reinterpret_cast<const uint32_t*>(&top2);
+      uint32_t most = max(two << 16, two & 0xFFFF0000u);
+      if (most >= 0x7F800000u) {                 // infinities among them: the largest of the others
+        most = 0;
+#pragma unroll 1
+        for (int i = 0; i < 9 * kNR * 8 / 256 * 8; ++i) {
+          const uint32_t at = 16 * (kt + 256 * (i >> 3)) + 2 * (i & 7);
+          const uint32_t a = (uint32_t)(*reinterpret_cast<const uint16_t*>(qbuf + at) & 0x7FFF) << 16;
+          if (((i >> 3) & 1) * 32 + (kt >> 3) < w.rows && a < 0x7F800000u) most = max(most, a);
+        }
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) {
+        qmax[warp - 8] = (int)most;
+        tc::mbar_arrive(qmaxb);
+      }
+      if (!tc::mbar_wait_few(qmaxb, u & 1, abort_flag, p.err)) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)qmax[i]);
+      // (at most 2^126: queries that small give f16 numbers with all their bits all the same)
+      const int a = most == 0 ? 0 : min(126, 14 + 127 - (int)(most >> 23));
+      const float f = __uint_as_float((uint32_t)(127 + a) << 23);
+      if (kt == 0) qscale[u & 1] = __uint_as_float((uint32_t)(127 - a) << 23);
+#pragma unroll 2
+      for (int i = 0; i < 9 * kNR * 8 / 256; ++i) {
+        uint4* at = reinterpret_cast<uint4*>(qbuf + 16 * (kt + 256 * i));
+        uint4 v = *at;
+        uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          e[k] = pack_f16(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xFFFF0000u) * f);
+        *at = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(qready);
+      ++u;
       const int64_t first_from = kWindow ? latent_from(p, w.start + (w.row0 - w.seq_row0) / p.H) : 0;
       for (int t = w.tile0; t < w.tile1; ++t, ++g) {
         const int buf = g & 1, ring = g % 3;
