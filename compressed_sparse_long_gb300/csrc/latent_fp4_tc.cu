@@ -17,22 +17,27 @@
 //   values: a thread four dims (lane l: dims 4l .. 4l + 3, one for each block of 128 of O^T) expands
 //           32 keys of two of them at a time, 2 x 16 columns. Two keys' codes are brought side by side
 //           in a byte first, so one conversion gives a pair of keys.
-// Each has a ring of three slots of 32 columns (O^T 256, S^T 64, rings 192: all 512), and S^T of the
-// next tile runs beside this tile's softmax and O^T.
+// Keys have a ring of two slots of 32 columns, values one of four (O^T 256, S^T 64, rings 192: all 512),
+// and S^T of the next tile runs beside this tile's softmax and O^T. (Three and three: 217 us in the case
+// below where this took 209. The values of a tile can wait for its weights in four slots.)
 //
-// Warps 0-7: softmax and output, as in the plain kernel. Warps 8-15: keys, two warpgroups taking slots
-// in turn. Warps 16-23: values, a warpgroup for each half of the keys. Warps 24 and 26: products, one for
-// each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles; scales;
-// Q).
+// Warps 0-7: softmax and output, as in the plain kernel. Warps 8-15: queries and keys, two warpgroups
+// with a slot each. Warps 16-23: values, a warpgroup for each half of the keys. Warps 24 and 26: products,
+// one for each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles;
+// scales; Q).
 //
-// Bound: instructions. A tile takes 17,500 warp instructions (each code is expanded twice); the four
-// schedulers issue 2.2 a cycle, the tensor pipe is active for 26 % of the time. 28 warps in six roles
-// do not fit the small instruction caches: loops over slots are rolled, waits are short, and one thread
-// walks for all. 32 sequences x 32768 tokens, 64 heads: 217 us with the merge (670 TFLOP/s); 16 of
-// 4616-108051, 128 heads: 247 us. (The bf16 cache takes 202 and 195: a smaller cache, not a faster one.)
-// On the way: one warpgroup a role 276 us, the same with unrolled loops 431. Codes expanded once, from
-// registers, keys to tensor memory and values to shared memory: 319 us (the values' stores wait while
-// O^T's products read shared memory).
+// Bound: instructions, and the waits between roles. A tile takes 17,400 warp instructions (each code is
+// expanded twice); the four schedulers issue 2.3 a cycle, the tensor pipe is active for 29 % of the time.
+// A slot's way from one hand to the next (wait, store, arrive, wait, products, commit) is 1,200 cycles of a
+// tile's 6,300. 28 warps in six roles do not fit the small instruction caches: loops over slots are rolled
+// (S^T's unrolled by three: 216 us), waits are short, and one thread walks for all.
+// 32 sequences x 32768 tokens, 64 heads: 200 us with the merge (730 TFLOP/s); 16 of 4616-108051, 128 heads:
+// 224 us; 4 chunks, 4012 tokens, 16 heads, window 1024: 241 us. (The bf16 cache takes 198, 192 and 219: a
+// smaller cache, not a faster one.)
+// On the way: one warpgroup a role 276 us, the same with unrolled loops 431; masked tiles' maxima by
+// redux.sync, 170 cycles each, 207 (300 under the window). Codes expanded once, from registers, keys to
+// tensor memory and values to shared memory: 319 us (the values' stores wait while O^T's products read
+// shared memory). P^T and its products by halves, to overlap the tiles' O^T: 255 us.
 #include "kernels.h"
 #include "latent.h"
 #include "latent_tc.cuh"

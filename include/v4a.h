@@ -489,7 +489,7 @@ int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows,
  * the largest |q| of up to 64 neighbouring (token, head) rows, and each weight times its row's scale is
  * rounded once, to f16 (11 bits down to 2^-20 of the largest such product of a head so far, fewer below;
  * rows whose scales are 2^126 apart are not told from nothing). Against a plain cache: a third of the
- * bytes; 217 against 202 us at 32 x 32,768 tokens and 64 heads.
+ * bytes; 200 against 198 us at 32 x 32,768 tokens and 64 heads.
  */
 size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                                       int64_t max_pos);
