@@ -457,3 +457,46 @@ def test_fp4_queries_that_are_not_finite_stay_their_own(window):
     _, mag = O.attention(live, bt, [0, 1, 2], [699, 299], f64(big), c.softmax_scale, 512, None, window, 3 if window else 0)
     tol = attn_tolerance(BF, ref, mag, 576, 700, bound) + 2.0 ** -20 * np.abs(live[:, :512]).max()
     check(got[:, keep], ref[:, keep], tol[:, keep])
+
+
+@pytest.mark.parametrize("heads,window", [(64, None), (16, None), (128, 3)])
+def test_fp4_many_pieces_of_one_tile(heads, window):
+    """Several pieces a CTA, of one tile each, whose queries' sizes are far apart: what brings one piece's
+    queries into f16 reaches no other."""
+    rng = np.random.default_rng(39)
+    total = [1 + 41 * i % 128 for i in range(620)]
+    lay, bt = fp4_layer(rng, BF, heads, total, junk=True)
+    size = torch.from_numpy(2.0 ** rng.integers(-24, 1, 620)).to("cuda", BF)
+    q, e = rand(rng, BF, 620, heads, 576) * size[:, None, None], err_word()
+    got, ref, tol = run_attention(lay, bt, total, [1] * 620, q, window, 1 if window else 0, e)
+    assert v4a.v4a_get_error(e) == 0
+    check(got, ref, tol)
+
+
+@pytest.mark.parametrize("dtype,latent,dim,heads", [(BF, 512, 64, 16), (F32, 128, 32, 3)])
+def test_rows_behind_the_last_sequence_stay(dtype, latent, dim, heads):
+    """A batch padded to more rows than its sequences have: the rows behind them are neither read nor
+    written, by any of the calls."""
+    rng = np.random.default_rng(40)
+    total, new = [300, 0, 700], [2, 0, 3]
+    cu, start = ints([0, 2, 2, 5], I32), ints([298, 0, 697], I64)
+    a, bt = fp4_layer(rng, dtype, heads, total, latent, dim)
+    b = LatentLayer(a.cfg, PagedPool(a.pool.data.clone(), a.pool.scale.clone(), a.pool.block_table, 256))
+    x = rand(rng, dtype, 9, latent + dim)
+    x[5:] = float("nan")
+    a.insert(cu, start, x[:5, :latent], x[:5, latent:])
+    b.insert(cu, start, x[:, :latent], x[:, latent:])
+    assert torch.equal(a.pool.data, b.pool.data) and torch.equal(a.pool.scale, b.pool.scale)
+    rows = torch.full((9, latent + dim), 7.0, dtype=dtype, device="cuda")
+    b.gather(cu, start, 9, out=rows)
+    assert torch.equal(rows[:5], a.gather(cu, start, 5)) and (rows[5:] == 7).all()
+    q = rand(rng, dtype, 9, heads, latent + dim)
+    q[5:] = float("nan")
+    for window, sinks in ((None, 0), (200, 3)):
+        e = err_word()
+        out = torch.full((9, heads, latent), 7.0, dtype=dtype, device="cuda")
+        b.attention(cu, start, 699, q, out=out, dev_err=e, window=window, sinks=sinks)
+        got, ref, tol = run_attention(a, bt, total, new, q[:5], window, sinks)
+        assert v4a.v4a_get_error(e) == 0 and (out[5:] == 7).all()
+        check(out[:5], ref, tol)
+        check(got, ref, tol)
