@@ -26,6 +26,40 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
+// A sum of fp32 numbers and the sum of its roundings' errors, and 1 / sqrt(sum / n + eps) of it to half
+// a step and little more. (fp32 layers: r reaches the row scale, and with it the rotary part's f16
+// numbers; a scale a step off gives one in 7,000 of those its neighbour, 2^-10 away.)
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b));
+    hi = t;
+  }
+  __device__ __forceinline__ void add_square(float z) {
+    const float p = __fmul_rn(z, z);
+    lo += __fmaf_rn(z, z, -p);
+    add(p);
+  }
+  __device__ __forceinline__ void over_warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo += __shfl_xor_sync(0xffffffffu, lo, o);
+      add(h);
+    }
+  }
+  __device__ __forceinline__ float inv_root(float n, float eps) const {
+    Sum2 m;
+    m.hi = __fdiv_rn(hi, n);
+    m.lo = (__fmaf_rn(-m.hi, n, hi) + lo) / n;
+    m.add(eps);
+    const float r = 1.0f / sqrtf(m.hi), rr = __fmul_rn(r, r);
+    const float e = __fmaf_rn(-m.hi, rr, 1.f) - m.hi * __fmaf_rn(r, r, -rr) - m.lo * rr;   // 1 - m r^2
+    return e > -1.f && e < 1.f ? __fmaf_rn(0.5f * r, e, r) : r;      // (r as it is at 0, infinity, NaN)
+  }
+};
+
 // ----------------------------------------------------------------------------- insert
 // As the kernel for plain rows: a block looks the pool rows of up to 32 tokens up, a thread a token,
 // then a warp takes one token after the other, the next one's row requested ahead. A lane holds whole
@@ -103,7 +137,9 @@ __global__ void __launch_bounds__(32 * kInsertWarps, kBlocks == 1 ? 3 : 2)
     if (k + kInsertWarps < nt) next.load(p, t0 + k + kInsertWarps, lane);
     const int64_t slot = slots[k], pos = at[k];
     if (slot < 0) continue;
+    constexpr bool kExact = sizeof(T) == 4;
     float z[kBlocks][16], ss = 0.f, zmax = 0.f, kmax = 0.f;
+    Sum2 sq;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       const int b = lane + 32 * i;
@@ -112,7 +148,8 @@ __global__ void __launch_bounds__(32 * kInsertWarps, kBlocks == 1 ? 3 : 2)
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         z[i][q] = Elem<T>::to_f(e[q]);
-        ss = fmaf(z[i][q], z[i][q], ss);
+        if constexpr (kExact) sq.add_square(z[i][q]);
+        else ss = fmaf(z[i][q], z[i][q], ss);
       }
       if (p.gamma) {
 #pragma unroll
@@ -136,11 +173,20 @@ __global__ void __launch_bounds__(32 * kInsertWarps, kBlocks == 1 ? 3 : 2)
       cc *= p.rot.amp;
       sn *= p.rot.amp;
       const float a = Elem<T>::to_f(in.x0[j]), b = Elem<T>::to_f(in.x1[j]);
-      y0[j] = a * cc - b * sn;
-      y1[j] = a * sn + b * cc;
+      // (rounded one by one: h then is the formula's f16 number wherever cosine and sine are its own)
+      y0[j] = __fsub_rn(__fmul_rn(a, cc), __fmul_rn(b, sn));
+      y1[j] = __fadd_rn(__fmul_rn(a, sn), __fmul_rn(b, cc));
       kmax = max_nan(kmax, max_nan(fabsf(y0[j]), fabsf(y1[j])));
     }
-    const float r = p.gamma ? 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps) : 1.f;
+    float r = 1.f;
+    if (p.gamma) {
+      if constexpr (kExact) {
+        sq.over_warp();
+        r = sq.inv_root((float)p.C, p.eps);
+      } else {
+        r = 1.0f / sqrtf(warp_sum(ss) / (float)p.C + p.eps);
+      }
+    }
     zmax = warp_max_nan(zmax);
     kmax = warp_max_nan(kmax);
     float u = __fmul_rn(zmax, 1.0f / 2688.0f), s = __fmul_rn(r, u);
