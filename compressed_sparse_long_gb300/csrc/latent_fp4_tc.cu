@@ -75,6 +75,7 @@ constexpr float kRoom = -6.0f, kRaise = 12.0f, kOver = 15.0f;    // log2 units: 
                                                                  // what raises it in masked tiles and in others
 // registers of softmax, key and value (two each) and other warpgroups: 896 threads x 72 in all
 constexpr int kRegSoftmax = 104, kRegKeys = 56, kRegValues = 72, kRegOther = 40;
+static_assert(kRegValues == 72, "the values' warpgroups keep what the launch gives");
 static_assert(2 * (kRegSoftmax + kRegKeys + kRegValues) + kRegOther <= 7 * 72, "registers of the launch");
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
