@@ -100,7 +100,7 @@ class PageTableDesc(ctypes.Structure):
 class Pool(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("row_bytes", ctypes.c_int64), ("rows_per_block", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("late", ctypes.c_int16), ("reserved", ctypes.c_int16)]
 
 
 _P = ctypes.c_void_p

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------------------- fork
-constexpr int32_t kForkOk = 1, kForkCut = 2;
+// An entry is to be carried out; its cut block, and the last whole block before it, need pages.
+constexpr int32_t kForkOk = 1, kForkCut = 2, kForkLate = 4;
 struct ForkParams {
   v4a_page_table t;
   const int32_t* src;
@@ -239,9 +240,10 @@ struct ForkParams {
   const int64_t* length;
   int32_t* free_cnt;   // [n_chunks]
   int32_t* state;      // [n] kFork* bits
-  int32_t* page;       // [n] the cut block's new page, or -1
+  int32_t* page;       // [2][n] new pages of cut blocks, and of last whole blocks, or -1
   int32_t* err;
   int32_t n, n_chunks;
+  int32_t late;        // the most of the pools': tokens behind a block that still write into it
 };
 
 // Blocks 0 .. n_chunks - 1 count free pages, the others look an entry over.
@@ -266,23 +268,26 @@ __global__ void __launch_bounds__(kCountThreads) pages_fork_check_kernel(const F
     raise_err(p.err, V4A_DEV_BAD_INDEX);
   } else {
     state = kForkOk;
-    if (len % kBlock &&
-        page_of(p.t.block_table[(int64_t)s * p.t.max_blocks + len / kBlock], p.t.n_pages, p.err) >= 0)
-      state |= kForkCut;
+    const int32_t* at = p.t.block_table + (int64_t)s * p.t.max_blocks + len / kBlock;
+    if (len % kBlock && page_of(at[0], p.t.n_pages, p.err) >= 0) state |= kForkCut;
+    if (len >= kBlock && len % kBlock < p.late && page_of(at[-1], p.t.n_pages, p.err) >= 0) state |= kForkLate;
   }
   p.state[i] = state;
 }
 
-// The free page of each cut block: the k-th for the k-th of them.
+// Their free pages: the k-th for the k-th block that needs one. Block (entry, 0): of the cut block,
+// (entry, 1): of the one before it.
 __global__ void __launch_bounds__(kCountThreads) pages_fork_find_kernel(const ForkParams p) {
   __shared__ int32_t tot[32];
   __shared__ int32_t found, left;
   pdl_wait();
-  const int i = blockIdx.x;
-  if (!(p.state[i] & kForkCut)) return;
+  const int i = blockIdx.x, state = p.state[i];
+  if (!(state & (blockIdx.y ? kForkLate : kForkCut))) return;
+  int32_t* const page_at = p.page + (int64_t)blockIdx.y * p.n + i;
   int k = 0, rank, all;
-  for (int j = threadIdx.x; j < i; j += kCountThreads) k += (p.state[j] & kForkCut) != 0;
+  for (int j = threadIdx.x; j < i; j += kCountThreads) k += __popc(p.state[j] & (kForkCut | kForkLate));
   block_scan<kCountThreads>(k, tot, &rank);
+  if (blockIdx.y == 0 && (state & kForkLate)) ++rank;
   if (threadIdx.x == 0) found = -1;
   for (int c0 = 0; c0 < p.n_chunks; c0 += kCountThreads) {      // the chunk that holds it
     const int c = c0 + threadIdx.x, n = c < p.n_chunks ? p.free_cnt[c] : 0;
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kCountThreads) pages_fork_find_kernel(const Fo
   rank = left;
   if (chunk < 0) {
     if (threadIdx.x == 0) {
-      p.page[i] = -1;
+      *page_at = -1;
       raise_err(p.err, V4A_DEV_NO_PAGE);
     }
     return;
@@ -311,13 +316,14 @@ __global__ void __launch_bounds__(kCountThreads) pages_fork_find_kernel(const Fo
     const int before = block_scan<kCountThreads>(__popc(is_free), tot, &all);
     if (before <= rank && rank < before + __popc(is_free)) {
       for (int drop = rank - before; drop > 0; --drop) is_free &= is_free - 1;
-      p.page[i] = (int32_t)(page + __ffs(is_free) - 1);
+      *page_at = (int32_t)(page + __ffs(is_free) - 1);
     }
     rank -= all;
   }
 }
 
-// Block (part, entry): its part of the cut block's rows; the first also writes table and counts.
+// Block (part, entry, 0): its part of the cut block's rows; the first also writes table and counts.
+// Block (part, entry, 1): the same part of the whole block before it, where that one is copied.
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_move_kernel(const ForkParams p,
                                                                        const __grid_constant__ Pools pools) {
   pdl_wait();
@@ -327,25 +333,31 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_move_kernel(const For
   const int64_t len = __ldg(p.length + i);
   const int whole = (int)(len / kBlock), cut = (int)(len % kBlock);
   const int32_t* from = p.t.block_table + (int64_t)__ldg(p.src + i) * p.t.max_blocks;
-  const int32_t page = state & kForkCut ? p.page[i] : -1;
-  if (blockIdx.x == 0) {
+  const bool before = blockIdx.z;
+  const int32_t cut_page = state & kForkCut ? p.page[i] : -1, late_page = state & kForkLate ? p.page[p.n + i] : -1;
+  if (blockIdx.x == 0 && !before) {
     int32_t* to = p.t.block_table + (int64_t)__ldg(p.dst + i) * p.t.max_blocks;
-    for (int k = threadIdx.x; k < whole; k += kCopyThreads) {
+    for (int k = threadIdx.x; k < (state & kForkLate ? whole - 1 : whole); k += kCopyThreads) {
       const int32_t v = page_of(from[k], p.t.n_pages, p.err);
       if (v < 0) continue;
       to[k] = v;
       atomicAdd(p.t.refs + v, 1);
     }
-    if (threadIdx.x == 0 && page >= 0) {
-      to[whole] = page;
-      p.t.refs[page] = 1;
+    if (threadIdx.x == 0 && cut_page >= 0) {
+      to[whole] = cut_page;
+      p.t.refs[cut_page] = 1;
+    }
+    if (threadIdx.x == 0 && late_page >= 0) {
+      to[whole - 1] = late_page;
+      p.t.refs[late_page] = 1;
     }
   }
+  const int32_t page = before ? late_page : cut_page;
   if (page < 0 || pools.n == 0) return;
   int part = blockIdx.x;
   const v4a_pool& pool = pools.pool[pool_of(pools, part)];
-  const int rows = (pool.rows_per_block * cut + kBlock - 1) / kBlock;
-  copy_part(pool, from[whole], page, part, rows * pool.row_bytes, rows);
+  const int rows = before ? pool.rows_per_block : (pool.rows_per_block * cut + kBlock - 1) / kBlock;
+  copy_part(pool, from[before ? whole - 1 : whole], page, part, rows * pool.row_bytes, rows);
 }
 
 // ---------------------------------------------------------------------------- compact
@@ -463,6 +475,7 @@ int check_pools(const v4a_pool* pools, int32_t n, Pools* out) {
     if (!p.data || !aligned(p.data, 16) || !aligned(p.scale, 4) || p.reserved != 0) return V4A_ERR_ARG;
     if (p.rows_per_block < 1 || p.rows_per_block > kBlock) return V4A_ERR_ARG;
     if (p.row_bytes <= 0 || p.row_bytes % 16) return V4A_ERR_ARG;
+    if (p.late < 0 || p.late >= kBlock) return V4A_ERR_ARG;
     if (p.row_bytes > (1 << 20)) return V4A_ERR_UNSUPPORTED;
     const int64_t parts = (p.row_bytes * p.rows_per_block + kPart - 1) / kPart;
     out->pool[i] = p;
@@ -472,10 +485,10 @@ int check_pools(const v4a_pool* pools, int32_t n, Pools* out) {
 }
 
 // Words of the workspace: chunk counts, then what the calls keep (n_seq words and the table's size,
-// two lists of forks, three of the pool's size and one word).
+// three lists of forks, three of the pool's size and one word).
 size_t words(const v4a_page_table* t) {
   size_t most = (size_t)t->n_seq * t->max_blocks + t->n_seq;
-  if (most < 2 * (size_t)V4A_MAX_SEQ) most = 2 * V4A_MAX_SEQ;
+  if (most < 3 * (size_t)V4A_MAX_SEQ) most = 3 * V4A_MAX_SEQ;
   if (most < 3 * (size_t)t->n_pages + 1) most = 3 * (size_t)t->n_pages + 1;
   return (size_t)chunks_of(t) + most;
 }
@@ -554,12 +567,14 @@ int v4a_pages_fork(const v4a_page_table* table, const v4a_pool* pools, int32_t n
   p.state = p.free_cnt + p.n_chunks;
   p.page = p.state + n;
   p.err = dev_err;
+  for (int i = 0; i < pl.n; ++i) p.late = p.late > pl.pool[i].late ? p.late : pl.pool[i].late;
+  const unsigned places = p.late > 0 ? 2 : 1;     // (no blocks for what no pool asks for)
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(pages_fork_check_kernel, dim3((unsigned)(p.n_chunks + n)), dim3(kCountThreads), 0, st, p);
-  if (e == cudaSuccess) e = launch_pdl(pages_fork_find_kernel, dim3((unsigned)n), dim3(kCountThreads), 0, st, p);
+  if (e == cudaSuccess) e = launch_pdl(pages_fork_find_kernel, dim3((unsigned)n, places), dim3(kCountThreads), 0, st, p);
   const int parts = pl.parts[pl.n] > 0 ? pl.parts[pl.n] : 1;
   if (e == cudaSuccess)
-    e = launch_pdl(pages_fork_move_kernel, dim3((unsigned)parts, (unsigned)n), dim3(kCopyThreads), 0, st, p, pl);
+    e = launch_pdl(pages_fork_move_kernel, dim3((unsigned)parts, (unsigned)n, places), dim3(kCopyThreads), 0, st, p, pl);
   return done(e);
 }
 

@@ -59,6 +59,7 @@ class PagedPool:
     block_table: torch.Tensor
     rows_per_block: int
     elems_per_byte: int = 1      # 2 for packed fp4 rows
+    late: int = 0                # tokens behind a block's end that still write into its rows
 
     @property
     def c(self):
@@ -67,7 +68,8 @@ class PagedPool:
 
     def clone(self) -> "PagedPool":
         return PagedPool(self.data.clone(), None if self.scale is None else self.scale.clone(),
-                         self.block_table.clone(), self.rows_per_block, self.elems_per_byte)
+                         self.block_table.clone(), self.rows_per_block, self.elems_per_byte,
+                         self.late)
 
 
 def pool_from_host(p, elem_dtype, device, elems_per_byte=1) -> PagedPool:
@@ -81,12 +83,19 @@ def pool_from_host(p, elem_dtype, device, elems_per_byte=1) -> PagedPool:
 
 
 class Layer:
-    """One attention layer on the device: config, compressor parameters, four pools."""
+    """One attention layer on the device: config, compressor parameters, four pools.
+
+    The entry pools are told how far their blocks reach (``late``): an entry in a block's last rows
+    may be completed by tokens behind the block, 4 of them for c4a.
+    """
 
     def __init__(self, cfg, bias, gamma, ibias, attn: PagedPool, idx: PagedPool | None,
                  swa: PagedPool, state: PagedPool, top_k: int = 0):
         self.cfg, self.bias, self.gamma, self.ibias = cfg, bias, gamma, ibias
         self.attn, self.idx, self.swa, self.state = attn, idx, swa, state
+        for pool in (attn, idx):
+            if pool is not None:
+                pool.late = max(0, cfg.window - cfg.stride + cfg.win_off)
         self.top_k = top_k
         self.in_dtype = torch.bfloat16 if cfg.dtype == BF16_FP8 else torch.float32
 

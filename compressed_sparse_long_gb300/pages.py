@@ -23,7 +23,8 @@ _I32, _I64 = torch.int32, torch.int64
 class PageTable:
     """A block table, its pages' reference counts, and the pools whose rows they name.
 
-    pools: PagedPool list (may be empty) of the same number of pages, whose block_table is this one;
+    pools: PagedPool list (may be empty) of the same number of pages, whose block_table is this one
+    (a compressed layer's are lay.attn, lay.idx, lay.swa and lay.state);
     block_table: int32 [n_seq, max_blocks], -1 = no page; refs: int32 [n_pages], how many entries of
     the table name each page (0 = free). Without refs they are counted from the table, and the pools
     say how many pages there are. Nothing here waits for the device.
@@ -73,7 +74,7 @@ class PageTable:
         for p in self.pools:
             d, s, t = p.data, p.scale, p.block_table
             key += (d.data_ptr(), d.shape, d.dtype, d.get_device(), d.is_contiguous(),
-                    p.rows_per_block)
+                    p.rows_per_block, p.late)
             key += (None,) if s is None else (s.data_ptr(), s.shape, s.dtype, s.get_device(),
                                               s.is_contiguous())
             key += (None,) if t is table else (t.data_ptr(), t.shape)
@@ -86,11 +87,13 @@ class PageTable:
                     _need(p.scale, name + ".scale", dev, torch.float32, (n * p.rows_per_block,))
                 if p.block_table.data_ptr() != at or p.block_table.shape != table.shape:
                     raise ValueError("%s has another block table" % name)
+                if not 0 <= p.late < 256:
+                    raise ValueError("%s.late: 0 .. 255 is needed" % name)
                 if p.data.shape[1] * p.data.element_size() % 16:
                     raise ValueError("%s: rows of a multiple of 16 bytes are needed" % name)
             kept = self._pools = key, (Pool * len(self.pools))(*[
                 Pool(p.data.data_ptr(), None if p.scale is None else p.scale.data_ptr(),
-                     p.data.shape[1] * p.data.element_size(), p.rows_per_block, 0)
+                     p.data.shape[1] * p.data.element_size(), p.rows_per_block, p.late, 0)
                 for p in self.pools])
         return kept[1], len(kept[1])
 
@@ -124,8 +127,9 @@ class PageTable:
 
     def fork(self, src, dst, length, dev_err=None, stream=None):
         """Row dst[i] takes over the first length[i] positions of row src[i] (int32, int32, int64
-        [n]): whole blocks are shared, the block that length[i] cuts is copied to a page of its
-        own, in every pool. dst's row must hold no page."""
+        [n]): blocks that are complete there are shared, the block that length[i] cuts is copied to
+        a page of its own, in every pool, and so is the one before it where some pool's ``late``
+        says that tokens behind length[i] still write into it. dst's row must hold no page."""
         dev, desc, nb = self._describe()
         n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() else 0
         a, b = self._list(src, "src", dev, _I32, n), self._list(dst, "dst", dev, _I32, n)

@@ -574,7 +574,11 @@ typedef struct v4a_pool {
   float* scale;            /* device fp32 [n_pages * rows_per_block], or NULL */
   int64_t row_bytes;       /* a positive multiple of 16 */
   int32_t rows_per_block;  /* 1 .. 256 */
-  int32_t reserved;        /* must be 0 */
+  int16_t late;            /* 0 .. 255: up to this many tokens behind a block's last position still
+                              write into its rows. 0 for token caches; max(0, W - S + win_off) for
+                              the entry caches (attn, idx) of a compressed layer: 4 for c4a and 0 for
+                              c128a at win_off 0 */
+  int16_t reserved;        /* must be 0 */
 } v4a_pool;
 
 size_t v4a_pages_workspace_size(const v4a_page_table* table);
@@ -598,15 +602,19 @@ int v4a_pages_grow(const v4a_page_table* table, const int32_t* first, const int3
 
 /*
  * v4a_pages_fork — row dst[i] of the table takes over the first length[i] positions of row src[i],
- * for i < n (device int32 [n], int32 [n], int64 [n]; n <= V4A_MAX_SEQ). Blocks wholly inside them
- * are shared (the same page, its count one higher; -1 stays -1). The block that length[i] cuts gets
- * the lowest free page, in the order of i, into which the rows of its positions below length[i] are
- * copied, in every pool (a pool with R rows a block: its first ceil(R * cut / 256)); the page's
- * other rows are left as they were. So neither row writes into the other's tokens when both go on.
+ * for i < n (device int32 [n], int32 [n], int64 [n]; n <= V4A_MAX_SEQ). Blocks into which no later
+ * token writes are shared (the same page, its count one higher; -1 stays -1): those wholly below
+ * length[i], but for the last of them where length[i] % 256 is below some pool's `late`. That one and
+ * the block that length[i] cuts get the lowest free pages, in the order of i and of blocks. The rows
+ * are copied in every pool: of the first all, of the cut block those of its positions below length[i]
+ * (a pool with R rows a block: its first ceil(R * cut / 256)); the page's other rows are left as they
+ * were. So neither row writes into the other's tokens when both go on. (A compressed layer goes on
+ * from the residual rows of the last W positions below length[i]. v4a_compress_insert has written
+ * those where one of its calls ended there, or the tokens behind came in calls of their own.)
  * dst's row must hold no page, and its blocks behind length[i] stay without. A row may have several
  * children. An entry that is not so is left out whole and sets V4A_DEV_BAD_INDEX: a row outside the
  * table, src == dst, dst named by another entry as src or dst, a dst that holds a page, a length
- * below 0 or beyond the table. Where no page is left for a cut block it stays without and
+ * below 0 or beyond the table. Where no page is left for a block it stays without and
  * V4A_DEV_NO_PAGE is set.
  */
 int v4a_pages_fork(const v4a_page_table* table, const v4a_pool* pools, int32_t n_pools, int32_t n,

@@ -44,28 +44,31 @@ def fork_ok(bt, src, dst, length, i):
     return not any(dst[j] == d or src[j] == d for j in others) and (bt[d] < 0).all()
 
 
-def fork(bt, refs, pools, src, dst, length):
-    """True when every cut block got a page."""
+def fork(bt, refs, pools, src, dst, length, late=0):
+    """True when every block that needs a page got one. late: how many tokens behind a block's end
+    still write into its rows, the most of the pools'."""
     good = [i for i in range(len(src)) if fork_ok(bt, src, dst, length, i)]
     new = {}
     for i in good:
-        whole, cut = divmod(int(length[i]), BLOCK)
-        if cut and bt[src[i], whole] >= 0:
-            new[i] = take(refs)
+        n = int(length[i])
+        for k in range(-(-n // BLOCK)):
+            # the block's last rows are written by the token at (k + 1) * BLOCK + late - 1
+            if bt[src[i], k] >= 0 and n < (k + 1) * BLOCK + late:
+                new[i, k] = take(refs)
     for i in good:
-        whole, cut = divmod(int(length[i]), BLOCK)
-        for k in range(whole):
+        n = int(length[i])
+        for k in range(-(-n // BLOCK)):
             page = bt[src[i], k]
-            bt[dst[i], k] = page
-            if page >= 0:
-                refs[page] += 1
-        page = new.get(i, -1)
-        if page >= 0:
-            bt[dst[i], whole] = page
-            for data, R in pools:
-                rows = -(-R * cut // BLOCK)
-                a, b = bt[src[i], whole] * R, page * R
-                data[b:b + rows] = data[a:a + rows]
+            if (i, k) not in new:
+                bt[dst[i], k] = page
+                if page >= 0:
+                    refs[page] += 1
+            elif new[i, k] >= 0:
+                bt[dst[i], k] = new[i, k]
+                for data, R in pools:
+                    rows = -(-R * min(BLOCK, n - k * BLOCK) // BLOCK)
+                    a, b = page * R, new[i, k] * R
+                    data[b:b + rows] = data[a:a + rows]
     return all(p >= 0 for p in new.values())
 
 
