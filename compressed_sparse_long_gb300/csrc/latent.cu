@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(const __g
 // word, so the lanes' reads fall in different banks), the softmax statistics go by shuffles,
 // and lane l accumulates output dims l, l + 32, .. . Bound: shared-memory reads (a word a product)
 // and fp32 FMA: absorbed 14-17 TFLOP/s with 512 or 256 latent dims (8 sequences x 8,192 tokens, 64
-// heads, 512 + 64, fp32: 538 us), 6 with 128; expanded 5-9 (2,048-token prompt, 16 heads, fp32,
-// 128 + 64 / 128: 2.5 ms). The tensor-core kernels take 33 and 44 us at these sizes. FP4 rows are expanded
+// heads, 512 + 64, fp32: 535 us), 6 with 128; expanded 5-9 (2,048-token prompt, 16 heads, fp32,
+// 128 + 64 / 128: 2.3 ms). The tensor-core kernels take 33 and 44 us at these sizes. FP4 rows are expanded
 // as they come into shared memory.
 constexpr int kGenRows = 16, kGenKeys = 32, kGenThreads = 256;
 
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
       const float* q0 = qs + 2 * warp * DK;
       const float* q1 = q0 + DK;
       const float* kr = ks + lane * KS;
-#pragma unroll 4
+#pragma unroll 8
       for (int d = 0; d < DK; d += 4) {
         const float4 a = *reinterpret_cast<const float4*>(q0 + d), b = *reinterpret_cast<const float4*>(q1 + d);
         const float k0 = kr[d], k1 = kr[d + 1], k2 = kr[d + 2], k3 = kr[d + 3];
@@ -480,9 +480,12 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
         s1 = fmaf(b.x, k0, fmaf(b.y, k1, fmaf(b.z, k2, fmaf(b.w, k3, s1))));
       }
       const float k2e = p.scale * kLog2e;
-      const bool ok = kvalid[lane];
-      s0 = ok && sees(0, x0 + lane) ? s0 * k2e : -INFINITY;
-      s1 = ok && sees(1, x0 + lane) ? s1 * k2e : -INFINITY;
+      const bool ok = kvalid[lane], ok0 = ok && sees(0, x0 + lane), ok1 = ok && sees(1, x0 + lane);
+      s0 = ok0 ? s0 * k2e : -INFINITY;
+      s1 = ok1 ? s1 * k2e : -INFINITY;
+      // bit k: the row takes key k. (Asked for each key again, by positions, the window made calls without
+      // one 4 to 9 % slower.)
+      const uint32_t take0 = __ballot_sync(0xffffffffu, ok0), take1 = __ballot_sync(0xffffffffu, ok1);
       float c0, c1;
       const float p0 = softmax_step(s0, st[0], c0), p1 = softmax_step(s1, st[1], c1);
 #pragma unroll
@@ -490,16 +493,17 @@ __global__ void __launch_bounds__(kGenThreads) latent_attn_gen(const __grid_cons
         o[0][d] *= c0;
         o[1][d] *= c1;
       }
+#pragma unroll 4
       for (int k = 0; k < kGenKeys; ++k) {
         const float a = __shfl_sync(0xffffffffu, p0, k), b = __shfl_sync(0xffffffffu, p1, k);
-        const bool sees0 = sees(0, x0 + k), sees1 = sees(1, x0 + k);   // alike in every lane
-        if (!sees0 && !sees1) continue;
+        const uint32_t bit = 1u << k;
+        if (!((take0 | take1) & bit)) continue;
         const float* v = vs + k * VS + lane;
 #pragma unroll
         for (int d = 0; d < kNV; ++d) {
           const float x = lane + 32 * d < DV ? v[32 * d] : 0.f;
-          if (sees0) o[0][d] = fmaf(a, x, o[0][d]);
-          if (sees1) o[1][d] = fmaf(b, x, o[1][d]);
+          if (take0 & bit) o[0][d] = fmaf(a, x, o[0][d]);
+          if (take1 & bit) o[1][d] = fmaf(b, x, o[1][d]);
         }
       }
     }
