@@ -63,7 +63,13 @@ constexpr int kOffBar = kOffF + kNFloats * 4;
 constexpr int kNBar = 40;
 constexpr int kPieces = 4, kWalkers = 26;                        // pieces of work known ahead; warps that take them
 constexpr int kOffMisc = kOffBar + kNBar * 8;
-constexpr int kOffPiece = kOffMisc + 256;
+// words there: tensor memory's address, the abort flag, and what the roles tell one another
+constexpr int kAbort = 1, kRaised = 2, kTileOk = 6, kTileValid = 8, kQMax = 11, kQScale = 19, kWarpTot = 32;
+constexpr int kMiscWords = 64;
+static_assert(kRaised + 4 <= kTileOk && kTileOk + 2 <= kTileValid && kTileValid + 3 <= kQMax && kQMax + 8 <= kQScale &&
+                  kQScale + 2 <= kWarpTot && kWarpTot + kThreads / 32 <= kMiscWords,
+              "words of their own: the plan's sums have one a warp");
+constexpr int kOffPiece = kOffMisc + kMiscWords * 4;
 constexpr int kSmemBytes = kOffPiece + kPieces * (int)sizeof(LatentPiece) + (int)sizeof(LatentWalk) + 1024;
 static_assert(kOffPiece % 8 == 0 && sizeof(LatentPiece) % 8 == 0, "alignment");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
@@ -157,13 +163,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pieceempty = bars + 36;                              // [4]
   int* misc = reinterpret_cast<int*>(sm + kOffMisc);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc);
-  volatile int* abort_flag = misc + 1;
-  volatile int* raised = misc + 2;                               // [2 halves][2 parities] tile + 1
-  volatile int* tile_ok = misc + 6;                              // [2] by raw buffer
-  volatile int* tile_valid = misc + 8;                           // [3] keys of a tile that exist
-  int* qmax = misc + 11;                                         // [8] largest |q| of a warp's chunks, as bits
-  volatile float* qscale = reinterpret_cast<float*>(misc + 40);  // [2] 2^-a of a piece
-  int32_t* warp_tot = misc + 20;                                 // [20]
+  volatile int* abort_flag = misc + kAbort;
+  volatile int* raised = misc + kRaised;                         // [2 halves][2 parities] tile + 1
+  volatile int* tile_ok = misc + kTileOk;                        // [2] by raw buffer
+  volatile int* tile_valid = misc + kTileValid;                  // [3] keys of a tile that exist
+  int* qmax = misc + kQMax;                                      // [8] largest |q| of a warp's chunks, as bits
+  volatile float* qscale = reinterpret_cast<float*>(misc + kQScale);   // [2] 2^-a of a piece
+  int32_t* warp_tot = misc + kWarpTot;                           // [28] by warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
