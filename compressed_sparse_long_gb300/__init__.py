@@ -90,6 +90,15 @@ class LatentCfg(ctypes.Structure):
                 ("rms_eps", ctypes.c_float), ("softmax_scale", ctypes.c_float),
                 ("rope", RopeCfg)]
 
+    @property
+    def reserved(self):
+        """cache_format, by the name that the field had before it had a meaning."""
+        return self.cache_format
+
+    @reserved.setter
+    def reserved(self, value):
+        self.cache_format = value
+
 
 class PageTableDesc(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("refs", ctypes.c_void_p),

@@ -409,7 +409,10 @@ typedef struct v4a_latent_cfg {
   int32_t latent_dim;    /* C: a multiple of 8, 8 .. 1024 */
   int32_t nope_dim;      /* dims of an expanded key before its rotary part: multiple of 8, .. 256 */
   int32_t v_dim;         /* dims of an expanded value: multiple of 8, 8 .. 256 */
-  int32_t cache_format;  /* V4A_LATENT_PLAIN (0) or V4A_LATENT_FP4 */
+  __extension__ union {
+    int32_t cache_format; /* V4A_LATENT_PLAIN (0) or V4A_LATENT_FP4 */
+    int32_t reserved;     /* the field's name before it had a meaning */
+  };
   float rms_eps;         /* of v4a_latent_insert's norm */
   float softmax_scale;   /* > 0, of both attention forms */
   v4a_rope_cfg rope;     /* rope.dim: a multiple of 8, 8 .. 128 */

@@ -3,6 +3,7 @@ pinned by tables and brute force."""
 import ctypes
 import json
 import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -144,3 +145,28 @@ def test_windowed_attention_by_brute_force():
             for h in range(2):
                 w = np.exp(0.3 * rows @ q[i, h])
                 assert np.allclose(o[i, h], w @ rows[:, :8] / w.sum())
+
+
+def test_the_format_field_by_its_name_before(lib, tmp_path):
+    """The field was called `reserved` and had to be 0: programs that say so go on, and another value
+    is not taken for 0."""
+    rope = v4a.rope_cfg(64)
+    kw = dict(dtype=v4a.BF16, n_heads=4, latent_dim=512, nope_dim=128, v_dim=128, rms_eps=1e-6,
+              softmax_scale=0.1, rope=rope)
+    for value, ok in ((0, True), (v4a.LATENT_FP4, True), (7, False)):
+        cfg = v4a.LatentCfg(reserved=value, **kw)
+        assert cfg.cache_format == cfg.reserved == value
+        assert (lib.v4a_latent_attn_workspace_size(B(cfg), 2, 2, 1000) > 0) == ok
+    cfg = v4a.LatentCfg(**kw)
+    assert cfg.reserved == 0
+    prog = tmp_path / "names.c"
+    prog.write_text('#include "v4a.h"\n'
+                    'int main(void){ v4a_latent_cfg a = {.dtype = V4A_BF16, .v_dim = 128, .reserved = 0},'
+                    ' b = {.dtype = V4A_BF16, .cache_format = V4A_LATENT_FP4};'
+                    ' v4a_latent_cfg c = {V4A_BF16, 4, 512, 128, 128, 0, 1e-6f, 0.1f, a.rope};'
+                    ' b.reserved -= 1; return a.cache_format + b.cache_format + c.reserved; }\n')
+    exe = tmp_path / "names"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Wno-missing-field-initializers",
+                    "-Wno-missing-braces", "-Werror",
+                    "-I", os.path.join(ROOT, "include"), str(prog), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
