@@ -29,3 +29,11 @@ def test_reference_arm_prints_the_contract_line():
     assert e2e["value"] == line["value"] and e2e["h2d_bytes_per_step"] == 0
     assert e2e["d2h_bytes_per_step"] == 0 and e2e["unit"] == line["unit"]
     assert "workload" in line["config"]
+
+
+def test_traffic_of_the_rooflines_is_of_this_library():
+    """The line's DRAM bytes come from committed profiles, and only from those that state the library's
+    version: a version whose profiles say another one would leave them out."""
+    import bench
+    for call in ("attention", "index_topk"):
+        assert bench._profile_traffic(call) > 1e7, call
