@@ -15,8 +15,6 @@
 namespace v4a {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 // ------------------------------------------------------------------------------- rope
 // Bound: HBM for many tokens (8192 x 64 heads x 64 dims fp32: 44 us, 6.1 TB/s), latency for few
 // (4.3 us). A thread takes `VEC` consecutive elements of

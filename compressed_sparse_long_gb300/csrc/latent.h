@@ -145,6 +145,8 @@ cudaError_t launch_latent_merge(const LatentAttnParams& p, int dtype, cudaStream
 // ------------------------------------------------------------------ device-side plan
 #ifdef __CUDACC__
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // A kernel parameter array read with an index of each thread's own: through its address, as
 // ordinary memory. (From the constant bank the lanes' different words come one at a time.)
 __device__ __forceinline__ const float* by_address(const float* v) {

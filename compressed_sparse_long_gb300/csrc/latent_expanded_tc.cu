@@ -36,7 +36,6 @@ namespace {
 constexpr int kThreads = 384, kStages = 3;
 constexpr int kT = 128;                                          // a CTA's queries of a tile; keys of a step
 constexpr int kItem = 512;                                       // queries of an item
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRoom = 16.0f, kRaise = -8.0f;                   // log2 units: a reference above its maximum;
                                                                  // a weight that raises it
 

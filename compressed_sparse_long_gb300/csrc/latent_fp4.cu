@@ -98,7 +98,6 @@ template <typename T, int kBlocks>
 __global__ void __launch_bounds__(32 * kInsertWarps, kBlocks == 1 ? 3 : 2)
     latent_insert_fp4_kernel(const __grid_constant__ LatentInsertParams p, int tokens) {
   using Row = Fp4Row<T, kBlocks>;
-  constexpr int kV = Row::kV;
   __shared__ int64_t slots[kInsertTokens], at[kInsertTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int np = p.rot.dim / 2, nb = p.C / 16;

@@ -26,14 +26,18 @@
 // one for each of the two (a wait is long against four products). Warp 25: copies (raw rows, two tiles;
 // scales; Q).
 //
-// Bound: instructions, and the waits between roles. A tile takes 17,400 warp instructions (each code is
-// expanded twice); the four schedulers issue 2.3 a cycle, the tensor pipe is active for 29 % of the time.
-// A slot's way from one hand to the next (wait, store, arrive, wait, products, commit) is 1,200 cycles of a
-// tile's 6,300. 28 warps in six roles do not fit the small instruction caches: loops over slots are rolled
-// (S^T's unrolled by three: 216 us), waits are short, and one thread walks for all.
-// 32 sequences x 32768 tokens, 64 heads: 200 us with the merge (730 TFLOP/s); 16 of 4616-108051, 128 heads:
-// 224 us; 4 chunks, 4012 tokens, 16 heads, window 1024: 241 us. (The bf16 cache takes 198, 192 and 219: a
-// smaller cache, not a faster one.)
+// Bound: instructions, and the waits between roles. A tile takes 16,900 warp instructions (each code is
+// expanded twice) and 3.06 us, about 6,000 cycles: the four schedulers issue 2.8 a cycle. Over a whole
+// launch, with its start and end, they issue 2.3, and the tensor pipe is active for 29 % of the time.
+// A slot's way from one hand to the next (wait, store, arrive, wait, products, commit) is 1,200 cycles of
+// those. 28 warps in six roles do not fit the small instruction caches: loops over slots are rolled
+// (S^T's unrolled by three: 216 us), waits are short, and one thread walks for all. ptxas spills 196 bytes
+// (248 under a window): more than half of them are the copies' thread's, which holds the walk in 40
+// registers and has time, the rest the softmax's (a dozen words of a piece, 104 registers) and a few of
+// the keys'; the values have none.
+// 32 sequences x 32768 tokens, 64 heads: 192 us with the merge (760 TFLOP/s); 16 of 4616-108051, 128 heads:
+// 216 us; 4 chunks, 3020 tokens, 16 heads, window 1024: 233 us. (The bf16 cache takes 196, 191 and 217: a
+// smaller cache, not a faster one. The trials below are to be held against 200, the time of their day.)
 // On the way: one warpgroup a role 276 us, the same with unrolled loops 431; masked tiles' maxima by
 // redux.sync, 170 cycles each, 207 (300 under the window). Codes expanded once, from registers, keys to
 // tensor memory and values to shared memory: 319 us (the values' stores wait while O^T's products read
@@ -286,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == w.tile0) k2 = p.scale * kLog2e * qscale[u++ & 1];
         const float2 in = info[(g % 3) * kTK + row];
         const int valid = tile_valid[g % 3];
+        // (1 / s to 2 ulp, log2 s to 2^-20 or so, the exponentials to 2^-22: beside the weights' 2^-11)
         const float kf = in.x * k2, ls = in.y, is = in.x != 0.f ? __fdividef(1.f, in.x) : 0.f;
         bool slow = valid < kTK || w.keys0 < x0 + kTK || (kWindow && x0 < all_from && x0 + kTK > p.sinks) ||
                     __any_sync(0xffffffffu, m == -INFINITY && vis > 0);

@@ -6,8 +6,6 @@
 
 namespace v4a {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -483,16 +483,16 @@ int v4a_latent_gather(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_rows,
  *        NULL where that is 0)
  * Keys in a block without a page are left out (and set the error word); a token that sees no
  * key gives zeros. Rows of the cache behind a sequence's last token are not used, whatever
- * they hold. A key that is not finite makes the outputs of its call's later tokens not finite,
- * and may do so to earlier tokens of the same call.
+ * they hold. A key that is not finite makes the outputs of the tokens that see it not finite, and
+ * may do so to other tokens of its sequence in the same call.
  * bf16 with C = 512 and rope.dim = 64 runs on the tensor cores; other shapes on CUDA cores, about
  * 16 times slower where the products decide (14-17 TFLOP/s for C of 256 and 512, 6 for 128).
- * FP4 caches: rows are the values that they stand for (scales s > 0; a row with s = 0 is a row of
- * zeros). On the tensor cores the products take B * code exactly and q but for elements below 2^-32 of
+ * FP4 caches: rows are the values that they stand for (scales 0 < s <= 2^126; a row with s = 0 is a
+ * row of zeros). On the tensor cores the products take B * code exactly and q but for elements below 2^-32 of
  * the largest |q| of up to 64 neighbouring (token, head) rows, and each weight times its row's scale is
  * rounded once, to f16 (11 bits down to 2^-20 of the largest such product of a head so far, fewer below;
  * rows whose scales are 2^126 apart are not told from nothing). Against a plain cache: a third of the
- * bytes; 200 against 198 us at 32 x 32,768 tokens and 64 heads.
+ * bytes; 192 against 196 us at 32 x 32,768 tokens and 64 heads.
  */
 size_t v4a_latent_attn_workspace_size(const v4a_latent_cfg* cfg, int32_t n_seq, int32_t n_tokens,
                                       int64_t max_pos);
