@@ -612,8 +612,8 @@ int v4a_pages_grow(const v4a_page_table* table, const int32_t* first, const int3
  * are copied in every pool: of the first all, of the cut block those of its positions below length[i]
  * (a pool with R rows a block: its first ceil(R * cut / 256)); the page's other rows are left as they
  * were. So neither row writes into the other's tokens when both go on. (A compressed layer goes on
- * from the residual rows of the last W positions below length[i]. v4a_compress_insert has written
- * those where one of its calls ended there, or the tokens behind came in calls of their own.)
+ * from the residual rows of the last W - 1 positions below length[i]. v4a_compress_insert has written
+ * those where one of its calls ended at length[i], or each of them was among the last W of its call.)
  * dst's row must hold no page, and its blocks behind length[i] stay without. A row may have several
  * children. An entry that is not so is left out whole and sets V4A_DEV_BAD_INDEX: a row outside the
  * table, src == dst, dst named by another entry as src or dst, a dst that holds a page, a length

@@ -327,3 +327,30 @@ def test_fork_equals_the_plain_form(late):
         there = P.fork(c.bt, c.refs, c.host, src, dst, length, late)
         assert v4a.v4a_get_error(e) == (0 if there else v4a.DEV_NO_PAGE)
         c.check()
+
+
+@pytest.mark.gpu
+def test_a_captured_fork_follows_lengths_and_tables():
+    """One capture, on a stream of its own, replayed with other lengths and sources."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from test_pages_gpu import Case
+    rng = np.random.default_rng(17)
+    c, e = Case(rng, 9, 5, 60, ("entries", "bf16"), fill=0.8), torch.zeros(1, dtype=I32, device="cuda")
+    c.pools[0].late = 4
+    full = np.array([0] * 5 + [5] * 4)
+    zero, last = dev(np.zeros(9), I32), dev(full, I32)
+    src, dst, length = dev(np.zeros(4), I32), dev(np.arange(5, 9), I32), dev(np.zeros(4), I64)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        c.table.free(zero, last, dev_err=e)
+        c.table.fork(src, dst, length, dev_err=e)
+    for lengths in ([256, 257, 259, 260], [1280, 1024, 515, 3], [0, 512, 768, 771]):
+        parents = rng.integers(0, 5, 4)
+        src.copy_(dev(parents, I32))
+        length.copy_(dev(np.asarray(lengths), I64))
+        graph.replay()
+        P.free(c.bt, c.refs, [0] * 9, full)
+        there = P.fork(c.bt, c.refs, c.host, parents, list(range(5, 9)), lengths, 4)
+        assert v4a.v4a_get_error(e) == (0 if there else v4a.DEV_NO_PAGE)
+        c.check()

@@ -73,6 +73,6 @@ def test_a_wait_gives_up_after_a_second(lib, which, status, bits):
     so = ctypes.CDLL(str(lib))
     assert so.run(which, ctypes.c_void_p(err.data_ptr()), ctypes.c_void_p(ns.data_ptr()),
                   ctypes.c_void_p(gave_up.data_ptr())) == 0
-    # the limit, and up to two rounds of 64 tries: those are some microseconds each
+    # the limit, and up to 64 tries until the clock is looked at: those are some microseconds each
     assert 1.0e9 <= ns.item() <= 1.5e9, ns.item()
     assert gave_up.item() == status and v4a.v4a_get_error(err) == bits
